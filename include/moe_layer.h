@@ -15,6 +15,15 @@
  *   dense_ffn_fa     one dense SwiGLU FFN over all tokens: the DenseFA
  *                    baseline, and the shared experts of a layer
  *
+ * Around it, for the block that holds the layer:
+ *
+ *   moe_permute, moe_unpermute    tokens as rows in the alignment's order, and
+ *                                 back with weights; their gradients, and
+ *                                 moe_route_backward, the routing weights'
+ *   moe_norm, moe_norm_residual   the norm before the block, and the norm, gate
+ *                                 and residual sum after it; their gradients
+ *   moe_combine_norm_residual     moe_combine with the latter in one launch
+ *
  * Sources for what each call computes are cited at the call.  "Serving-tax
  * notes" below means the talk notes on "Demystifying the Mixture of Experts
  * Serving Tax" (MLSys 2026); "TEMPO page" means the article on TEMPO
@@ -324,6 +333,140 @@ moe_status moe_combine(const void *y_pairs, moe_dtype ydt, const float *topk_w, 
 moe_status dense_ffn_fa(const void *x, moe_dtype dt, int64_t T, int H, int I_fa, const void *w13,
                         const void *w2, void *workspace, int64_t workspace_bytes, void *out,
                         moe_dtype odt, moe_schedule sched, void *stream);
+
+/*
+ * Tokens sorted by expert and back, as rows in memory (the grouped FFN gathers
+ * by index instead): for experts of the caller's own, an exchange of rows
+ * between GPUs, or training.  `plan` is an alignment filled by moe_align,
+ * moe_align_ex (either padding) or moe_route_align for the same T, K, E; row r
+ * of a row buffer [plan->cap][H] belongs to row r of the alignment.
+ *
+ *   moe_permute             rows[r] = x[p / K] for the pair p of row r; zero in
+ *                           the padding rows below expert_offsets[E]; rows past
+ *                           it are left as they were
+ *   moe_permute_backward    dx[t] = sum_k drows[inv_pos[t*K + k]]
+ *   moe_unpermute           out[t] = sum_k topk_w[t][k] * rows[inv_pos[t*K + k]]
+ *                                    (+ shared[t])
+ *   moe_unpermute_backward  drows[r] = topk_w[p] * dout[p / K], padding rows as
+ *                           by moe_permute; dw[t][k] = <dout[t],
+ *                           rows[inv_pos[t*K + k]]>, 0 for an unused slot
+ *
+ * Sums run in slot order in fp32 and are rounded once; unused slots (inv_pos
+ * -1) are left out.  moe_unpermute also skips slots of weight 0 and does not
+ * read their rows, as moe_combine does, so that the two agree bit for bit on
+ * the same rows.  topk_w NULL: every weight 1 (dw must then be NULL).  The
+ * gradient of `shared` is dout itself.  Either of drows and dw may be NULL;
+ * drows may be rows.  dw is fp32, summed over H in a fixed order.  No atomics:
+ * every result is the same on every run.
+ * x, dx [T][H] dt; rows, drows [plan->cap][H] dt / rdt; dout, out [T][H] odt;
+ * shared [T][H] sdt; topk_w, dw [T][K] fp32.  dout and rows have the same type.
+ * Limits: H a multiple of 8.  Row indices of the plan outside [0, plan->cap)
+ * are taken as unused slots.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED (H, dtype), MOE_ECAPACITY (a plan whose
+ * cap is below what either padding may need).
+ */
+moe_status moe_permute(const void *x, moe_dtype dt, int64_t T, int H, int E, int K,
+                       const moe_plan *plan, void *rows, void *stream);
+moe_status moe_permute_backward(const void *drows, moe_dtype dt, int64_t T, int H, int E, int K,
+                                const moe_plan *plan, void *dx, void *stream);
+moe_status moe_unpermute(const void *rows, moe_dtype rdt, const float *topk_w, const void *shared,
+                         moe_dtype sdt, int64_t T, int H, int E, int K, const moe_plan *plan,
+                         void *out, moe_dtype odt, void *stream);
+moe_status moe_unpermute_backward(const void *dout, const void *rows, moe_dtype dt,
+                                  const float *topk_w, int64_t T, int H, int E, int K,
+                                  const moe_plan *plan, void *drows, float *dw, void *stream);
+
+/*
+ * Gradient of moe_route's (or moe_route_var's) weights: with w the softmax over
+ * a token's selected logits,
+ *   dlogits[t][id_j] = w_j * (dw_j - sum_i w_i dw_i), 0 for experts not selected.
+ * topk_ids, topk_w: as routed; a slot with a negative id (unused), or one that
+ * is >= E, takes no part.  An expert listed twice gets the sum.
+ * topk_ids [T][K] int32; topk_w, dw [T][K] fp32; dlogits [T][E] fp32 (every
+ * element written).  Errors: as moe_route.
+ */
+moe_status moe_route_backward(const int32_t *topk_ids, const float *topk_w, const float *dw,
+                              int64_t T, int E, int K, float *dlogits, void *stream);
+
+/*
+ * The norms around a block of a residual stream.
+ *   MOE_NORM_RMS    norm(v) = v * rstd * weight + bias, rstd = 1 / sqrt(mean(v^2) + eps)
+ *   MOE_NORM_LAYER  norm(v) = (v - mean(v)) * rstd * weight + bias,
+ *                   rstd = 1 / sqrt(mean((v - mean(v))^2) + eps)
+ *   MOE_NORM_NONE   norm(v) = v (weight and bias must be NULL)
+ * weight, bias [H]; NULL: ones, zeros.  Statistics are fp32 (the variance from
+ * the centred values); results are rounded once.
+ */
+typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
+
+typedef struct {
+    int32_t kind;         /* moe_norm_kind */
+    float eps;            /* finite, >= 0 */
+    const void *weight;   /* [H] of the call's parameter type, or NULL */
+    const void *bias;
+} moe_norm_params;
+
+/* What a block's normed output is multiplied with: alpha * channel[h] * token[t]. */
+typedef struct {
+    float alpha;           /* residual scale; finite */
+    const void *channel;   /* [H] of the call's parameter type, or NULL: ones */
+    const float *token;    /* [T] fp32, or NULL: ones */
+} moe_gate_params;
+
+/*
+ * Norm before a block and residual after it, next to moe_combine:
+ *
+ *   moe_norm                   n = norm(x)                        (RMS or LAYER)
+ *   moe_norm_residual          r = x + gate * post(y);  n = pre(r) where n is given
+ *   moe_combine_norm_residual  the same with y[t] = sum_k topk_w[t][k] *
+ *                              y_pairs[t*K + k] (+ shared[t]) as summed by
+ *                              moe_combine (slots of weight 0 skipped), held in
+ *                              fp32: the end of a layer pass and the next
+ *                              block's norm in one launch
+ *   moe_norm_backward          dx = d norm(x)/dx . dn (+ dres, the gradient that
+ *                              passes the block by); dweight, dbias
+ *   moe_norm_residual_backward from dr: dy, the gradients of post's weight and
+ *                              bias and of the gates.  x's is dr itself; where n
+ *                              was taken too, dr is moe_norm_backward's dx at r,
+ *                              with r's own gradient as dres.
+ *
+ * n is computed from r before r is rounded.  pdt is the type of every weight,
+ * bias and channel gate of the call.  x, r, dx, dres and dr are of type xdt; y,
+ * dy and moe_norm_residual's n of type ydt; moe_norm's n and dn of type odt.
+ * Parameter gradients are fp32 [H] (dtoken fp32 [T]), overwritten, summed over
+ * the tokens in a fixed order: the same on every run.  Each may be NULL; one of
+ * a parameter that the call has not (a NULL weight's is that of ones) is refused
+ * for the gates and for MOE_NORM_NONE.  r may be x, n may be y, dx may be dn or
+ * dres, and dy may be dr or y where the types agree; other overlaps are not
+ * allowed.
+ * workspace: >= moe_norm_workspace_bytes(T, H) bytes for the partial sums, needed
+ * only where a gradient of weight, bias or channel is asked for (else may be
+ * NULL).  T = 0 writes zeros to those gradients and does nothing else.
+ * Limits: H a multiple of 8, at most 16384.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY (workspace).
+ */
+int64_t moe_norm_workspace_bytes(int64_t T, int H);   /* -1 on bad arguments */
+moe_status moe_norm(const void *x, moe_dtype xdt, int64_t T, int H, const moe_norm_params *norm,
+                    moe_dtype pdt, void *n, moe_dtype odt, void *stream);
+moe_status moe_norm_backward(const void *dn, moe_dtype odt, const void *x, moe_dtype xdt,
+                             const void *dres, int64_t T, int H, const moe_norm_params *norm,
+                             moe_dtype pdt, void *dx, float *dweight, float *dbias,
+                             void *workspace, int64_t workspace_bytes, void *stream);
+moe_status moe_norm_residual(const void *y, moe_dtype ydt, const void *x, moe_dtype xdt, int64_t T,
+                             int H, const moe_norm_params *post, const moe_gate_params *gate,
+                             moe_dtype pdt, void *r, const moe_norm_params *pre, void *n,
+                             void *stream);
+moe_status moe_combine_norm_residual(const void *y_pairs, moe_dtype ydt, const float *topk_w,
+                                     const void *shared, moe_dtype sdt, const void *x,
+                                     moe_dtype xdt, int64_t T, int K, int H,
+                                     const moe_norm_params *post, const moe_gate_params *gate,
+                                     moe_dtype pdt, void *r, const moe_norm_params *pre, void *n,
+                                     void *stream);
+moe_status moe_norm_residual_backward(const void *dr, moe_dtype xdt, const void *y, moe_dtype ydt,
+                                      int64_t T, int H, const moe_norm_params *post,
+                                      const moe_gate_params *gate, moe_dtype pdt, void *dy,
+                                      float *dweight, float *dbias, float *dchannel, float *dtoken,
+                                      void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
  * FP8 weights: weight quantization, the notes' decode-phase remedy (Serving-tax

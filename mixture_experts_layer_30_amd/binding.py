@@ -16,13 +16,17 @@ MOE_OK, MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY, MOE_EHIP = range(5)
 MOE_F32, MOE_BF16 = 0, 1
 SCHED_AUTO, SCHED_STREAM, SCHED_TILE, SCHED_RING, SCHED_SPAN = 0, 1, 2, 3, 4
 PAD_BLOCK, PAD_MAX = 0, 1
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 
 # every function the C header declares
 EXPORTS = ["moe_last_error", "moe_status_string", "moe_align_capacity", "moe_align_capacity_ex",
            "moe_ffn_workspace_bytes", "moe_ffn_workspace_bytes_ex", "dense_ffn_workspace_bytes",
            "moe_route", "moe_route_var", "moe_align", "moe_align_ex", "moe_route_align", "moe_grouped_ffn", "moe_grouped_gate_up", "moe_grouped_down",
            "moe_combine", "dense_ffn_fa", "moe_grouped_gate_up_fp8", "moe_grouped_down_fp8",
-           "dense_ffn_fp8", "moe_grouped_ffn_noalloc"]
+           "dense_ffn_fp8", "moe_grouped_ffn_noalloc", "moe_permute", "moe_permute_backward",
+           "moe_unpermute", "moe_unpermute_backward", "moe_route_backward",
+           "moe_norm_workspace_bytes", "moe_norm", "moe_norm_backward", "moe_norm_residual",
+           "moe_norm_residual_backward", "moe_combine_norm_residual"]
 
 # workspace bytes held per GPU by moe_grouped_ffn_noalloc (MOE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -38,6 +42,15 @@ class moe_plan(ctypes.Structure):
     _fields_ = [("expert_counts", ctypes.c_void_p), ("expert_offsets", ctypes.c_void_p),
                 ("sorted_ids", ctypes.c_void_p), ("block_expert", ctypes.c_void_p),
                 ("inv_pos", ctypes.c_void_p), ("block_m", ctypes.c_int32), ("cap", ctypes.c_int64)]
+
+
+class moe_norm_params(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int32), ("eps", ctypes.c_float), ("weight", ctypes.c_void_p),
+                ("bias", ctypes.c_void_p)]
+
+
+class moe_gate_params(ctypes.Structure):
+    _fields_ = [("alpha", ctypes.c_float), ("channel", ctypes.c_void_p), ("token", ctypes.c_void_p)]
 
 
 _lib = None
@@ -93,6 +106,25 @@ def lib():
         L.moe_grouped_down_fp8.argtypes = [vp, vp, i64, i32, i32, i32, i32, P, vp, i64, vp, vp]
         L.dense_ffn_fp8.restype = i32
         L.dense_ffn_fp8.argtypes = [vp, i64, i32, i32, vp, vp, vp, vp, vp, i64, vp, i32, vp]
+        N, G = ctypes.POINTER(moe_norm_params), ctypes.POINTER(moe_gate_params)
+        for name, args in (
+                ("moe_permute", [vp, i32, i64, i32, i32, i32, P, vp, vp]),
+                ("moe_permute_backward", [vp, i32, i64, i32, i32, i32, P, vp, vp]),
+                ("moe_unpermute", [vp, i32, vp, vp, i32, i64, i32, i32, i32, P, vp, i32, vp]),
+                ("moe_unpermute_backward", [vp, vp, i32, vp, i64, i32, i32, i32, P, vp, vp, vp]),
+                ("moe_route_backward", [vp, vp, vp, i64, i32, i32, vp, vp]),
+                ("moe_norm", [vp, i32, i64, i32, N, i32, vp, i32, vp]),
+                ("moe_norm_backward", [vp, i32, vp, i32, vp, i64, i32, N, i32, vp, vp, vp, vp, i64,
+                                       vp]),
+                ("moe_norm_residual", [vp, i32, vp, i32, i64, i32, N, G, i32, vp, N, vp, vp]),
+                ("moe_combine_norm_residual", [vp, i32, vp, vp, i32, vp, i32, i64, i32, i32, N, G,
+                                               i32, vp, N, vp, vp]),
+                ("moe_norm_residual_backward", [vp, i32, vp, i32, i64, i32, N, G, i32, vp, vp, vp,
+                                                vp, vp, vp, i64, vp])):
+            getattr(L, name).restype = i32
+            getattr(L, name).argtypes = args
+        L.moe_norm_workspace_bytes.restype = i64
+        L.moe_norm_workspace_bytes.argtypes = [i64, i32]
         _lib = L
     return _lib
 
@@ -283,3 +315,283 @@ def dense_ffn_fp8(x, q13, s13, q2, s2, workspace, out, stream=None):
                                _ptr(workspace), workspace.numel() * workspace.element_size(),
                                _ptr(out), _dt(out), _stream(stream)))
 
+
+
+# ---------------------------------------------- around the experts: rows, norms, gates
+
+
+def _refuse(what):
+    raise MoEError(MOE_EINVAL, what)
+
+
+def _shaped(t, shape, what, dtype=None):
+    """t is a tensor of this shape (and type), its elements in row-major order."""
+    if t.shape != shape:
+        _refuse(f"{what} must have shape {list(shape)}, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise MoEError(MOE_EUNSUPPORTED, f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        _refuse(f"{what} must be contiguous")
+
+
+def _call(fn, device, stream, *args):
+    """fn(*args, stream) with the tensors' GPU current: on `stream`, or that GPU's current one."""
+    if device.type != "cuda":
+        _refuse(f"tensors must be on a GPU, got {device}")
+    if stream is not None and stream.device != device:
+        _refuse(f"a stream of {stream.device} for tensors on {device}")
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(stream)))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream(stream)))
+
+
+def _one_device(first, *rest):
+    for t in rest:
+        if t is not None and t.device != first.device:
+            _refuse(f"tensors on {first.device} and {t.device}")
+    return first.device
+
+
+class Norm:
+    """A norm's kind, eps and parameters (see moe_norm_params in include/moe_layer.h).
+    weight, bias [H] fp32 or bf16, or None: ones, zeros.  Holds the tensors it points to."""
+
+    def __init__(self, kind=NORM_RMS, eps=1e-6, weight=None, bias=None):
+        self.kind, self.eps, self.weight, self.bias = kind, eps, weight, bias
+
+    @property
+    def c(self):
+        return moe_norm_params(self.kind, self.eps, _ptr(self.weight), _ptr(self.bias))
+
+    def tensors(self):
+        return self.weight, self.bias
+
+
+class Gate:
+    """alpha * channel[h] * token[t] (see moe_gate_params): channel [H] of the parameters'
+    type, token [T] fp32, either None.  Holds the tensors it points to."""
+
+    def __init__(self, alpha=1.0, channel=None, token=None):
+        self.alpha, self.channel, self.token = alpha, channel, token
+
+    @property
+    def c(self):
+        return moe_gate_params(self.alpha, _ptr(self.channel), _ptr(self.token))
+
+
+def _params(T, H, device, norms, gate=None):
+    """Checks the parameters of a call; returns their type."""
+    dt = None
+    named = [(t, w) for n in norms if n is not None for t, w in zip(n.tensors(), ("weight", "bias"))]
+    if gate is not None:
+        named.append((gate.channel, "channel"))
+        if gate.token is not None:
+            _shaped(gate.token, (T,), "token", torch.float32)
+    for t, what in named:
+        if t is None:
+            continue
+        _shaped(t, (H,), what)
+        if dt is not None and t.dtype != dt:
+            raise MoEError(MOE_EUNSUPPORTED, f"parameters of {dt} and {t.dtype} in one call")
+        dt = t.dtype
+        if t.device != device:
+            _refuse(f"{what} on {t.device}, the tokens on {device}")
+    if gate is not None and gate.token is not None and gate.token.device != device:
+        _refuse(f"token on {gate.token.device}, the tokens on {device}")
+    if dt is None or dt == torch.float32:
+        return MOE_F32
+    if dt == torch.bfloat16:
+        return MOE_BF16
+    raise MoEError(MOE_EUNSUPPORTED, f"parameter dtype {dt}")
+
+
+def _rows(t, plan, H, what, dtype=None):
+    """t holds the plan's rows: [cap][H] or more."""
+    if t.dim() != 2 or t.shape[0] < plan.cap or t.shape[1] != H:
+        _refuse(f"{what} must have shape [{plan.cap}, {H}] or more rows, got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise MoEError(MOE_EUNSUPPORTED, f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        _refuse(f"{what} must be contiguous")
+
+
+def _tokens(t, what):
+    if t.dim() != 2 or not t.is_contiguous():
+        _refuse(f"{what} must be a contiguous [T, H] tensor, got {list(t.shape)}")
+    return t.shape
+
+
+def _planned(t, plan, what):
+    """(T, H) of the tokens t, as many as the plan's"""
+    T, H = _tokens(t, what)
+    if T != plan.T:
+        _refuse(f"{what} has {T} tokens, the plan {plan.T}")
+    return T, H
+
+
+def moe_permute(x, plan, rows, stream=None):
+    """rows[r] = the token of alignment row r; zeros in padding rows; rows past the
+    padded total are left as they were.  x [T,H], rows [plan.cap,H] of x's type."""
+    T, H = _planned(x, plan, "x")
+    _rows(rows, plan, H, "rows", x.dtype)
+    dev = _one_device(x, rows, plan.inv_pos)
+    _call(lib().moe_permute, dev, stream, _ptr(x), _dt(x), T, H, plan.E, plan.K,
+          ctypes.byref(plan.c), _ptr(rows))
+
+
+def moe_permute_backward(drows, plan, dx, stream=None):
+    """dx[t] = the sum of the rows of token t, in slot order."""
+    T, H = _planned(dx, plan, "dx")
+    _rows(drows, plan, H, "drows", dx.dtype)
+    dev = _one_device(dx, drows, plan.inv_pos)
+    _call(lib().moe_permute_backward, dev, stream, _ptr(drows), _dt(dx), T, H, plan.E, plan.K,
+          ctypes.byref(plan.c), _ptr(dx))
+
+
+def moe_unpermute(rows, topk_w, plan, out, shared=None, stream=None):
+    """out[t] = sum_k topk_w[t,k] * (row of pair t,k) (+ shared[t]); topk_w None: weights 1."""
+    T, H = _planned(out, plan, "out")
+    _rows(rows, plan, H, "rows")
+    if topk_w is not None:
+        _shaped(topk_w, (T, plan.K), "topk_w", torch.float32)
+    if shared is not None:
+        _shaped(shared, (T, H), "shared")
+    dev = _one_device(out, rows, topk_w, shared, plan.inv_pos)
+    _call(lib().moe_unpermute, dev, stream, _ptr(rows), _dt(rows), _ptr(topk_w), _ptr(shared),
+          _dt(shared) if shared is not None else MOE_F32, T, H, plan.E, plan.K,
+          ctypes.byref(plan.c), _ptr(out), _dt(out))
+
+
+def moe_unpermute_backward(dout, rows, topk_w, plan, drows=None, dw=None, stream=None):
+    """Gradients of moe_unpermute: drows (padding rows as by moe_permute; may be rows) and
+    dw [T,K] fp32, either None.  rows may be None where dw is."""
+    T, H = _planned(dout, plan, "dout")
+    for t, what in ((rows, "rows"), (drows, "drows")):
+        if t is not None:
+            _rows(t, plan, H, what, dout.dtype)
+    for t, what in ((topk_w, "topk_w"), (dw, "dw")):
+        if t is not None:
+            _shaped(t, (T, plan.K), what, torch.float32)
+    dev = _one_device(dout, rows, topk_w, drows, dw, plan.inv_pos)
+    _call(lib().moe_unpermute_backward, dev, stream, _ptr(dout), _ptr(rows), _dt(dout),
+          _ptr(topk_w), T, H, plan.E, plan.K, ctypes.byref(plan.c), _ptr(drows), _ptr(dw))
+
+
+def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None):
+    """dlogits [T,E] fp32 from the gradient dw [T,K] of the routing weights."""
+    if topk_ids.dim() != 2 or dlogits.dim() != 2:
+        _refuse("topk_ids must be [T, K] and dlogits [T, E]")
+    T, K = topk_ids.shape
+    E = dlogits.shape[1]
+    _shaped(topk_ids, (T, K), "topk_ids", torch.int32)
+    _shaped(topk_w, (T, K), "topk_w", torch.float32)
+    _shaped(dw, (T, K), "dw", torch.float32)
+    _shaped(dlogits, (T, E), "dlogits", torch.float32)
+    dev = _one_device(topk_ids, topk_w, dw, dlogits)
+    _call(lib().moe_route_backward, dev, stream, _ptr(topk_ids), _ptr(topk_w), _ptr(dw), T, E, K,
+          _ptr(dlogits))
+
+
+def moe_norm_workspace_bytes(T, H):
+    return lib().moe_norm_workspace_bytes(T, H)
+
+
+def _workspace(t):
+    if t is None:
+        return None, 0
+    if not t.is_contiguous():
+        _refuse("workspace must be contiguous")
+    return _ptr(t), t.numel() * t.element_size()
+
+
+def _optional(H, **named):
+    for what, t in named.items():
+        if t is not None:
+            _shaped(t, (H,), what, torch.float32)
+
+
+def moe_norm(x, norm, out, stream=None):
+    """out = norm(x): x, out [T,H], each fp32 or bf16."""
+    T, H = _tokens(x, "x")
+    _shaped(out, (T, H), "out")
+    dev = _one_device(x, out)
+    pdt = _params(T, H, dev, (norm,))
+    _call(lib().moe_norm, dev, stream, _ptr(x), _dt(x), T, H, ctypes.byref(norm.c), pdt, _ptr(out),
+          _dt(out))
+
+
+def moe_norm_backward(dout, x, norm, dx, workspace=None, dres=None, dweight=None, dbias=None,
+                      stream=None):
+    """Gradients of moe_norm: dx (+ dres, both of x's type), dweight and dbias [H] fp32, where
+    given (they need a workspace of moe_norm_workspace_bytes(T, H))."""
+    T, H = _tokens(x, "x")
+    _shaped(dout, (T, H), "dout")
+    _shaped(dx, (T, H), "dx", x.dtype)
+    if dres is not None:
+        _shaped(dres, (T, H), "dres", x.dtype)
+    _optional(H, dweight=dweight, dbias=dbias)
+    dev = _one_device(x, dout, dx, dres, dweight, dbias, workspace)
+    pdt = _params(T, H, dev, (norm,))
+    ws, n = _workspace(workspace)
+    _call(lib().moe_norm_backward, dev, stream, _ptr(dout), _dt(dout), _ptr(x), _dt(x), _ptr(dres),
+          T, H, ctypes.byref(norm.c), pdt, _ptr(dx), _ptr(dweight), _ptr(dbias), ws, n)
+
+
+def _next_norm(pre, n, T, H, dtype):
+    if n is not None:
+        _shaped(n, (T, H), "n", dtype)
+    return ctypes.byref(pre.c) if pre is not None else None
+
+
+def moe_norm_residual(y, x, post, gate, r, pre=None, n=None, stream=None):
+    """r = x + gate * post(y) and, with pre, n = pre(r): x, r of one type, y, n of one type."""
+    T, H = _tokens(x, "x")
+    _shaped(y, (T, H), "y")
+    _shaped(r, (T, H), "r", x.dtype)
+    nx = _next_norm(pre, n, T, H, y.dtype)
+    dev = _one_device(x, y, r, n)
+    pdt = _params(T, H, dev, (post, pre), gate)
+    _call(lib().moe_norm_residual, dev, stream, _ptr(y), _dt(y), _ptr(x), _dt(x), T, H,
+          ctypes.byref(post.c), ctypes.byref(gate.c), pdt, _ptr(r), nx, _ptr(n))
+
+
+def moe_combine_norm_residual(y_pairs, topk_w, x, post, gate, r, pre=None, n=None, shared=None,
+                              stream=None):
+    """moe_norm_residual of y[t] = sum_k topk_w[t,k] y_pairs[t*K + k] (+ shared[t])."""
+    T, H = _tokens(x, "x")
+    if topk_w.dim() != 2:
+        _refuse("topk_w must be [T, K]")
+    K = topk_w.shape[1]
+    _shaped(topk_w, (T, K), "topk_w", torch.float32)
+    if y_pairs.dim() != 2 or y_pairs.shape[0] < T * K or y_pairs.shape[1] != H or \
+            not y_pairs.is_contiguous():
+        _refuse(f"y_pairs must be a contiguous [{T * K}, {H}] tensor, got {list(y_pairs.shape)}")
+    _shaped(r, (T, H), "r", x.dtype)
+    if shared is not None:
+        _shaped(shared, (T, H), "shared")
+    nx = _next_norm(pre, n, T, H, y_pairs.dtype)
+    dev = _one_device(x, y_pairs, topk_w, shared, r, n)
+    pdt = _params(T, H, dev, (post, pre), gate)
+    _call(lib().moe_combine_norm_residual, dev, stream, _ptr(y_pairs), _dt(y_pairs), _ptr(topk_w),
+          _ptr(shared), _dt(shared) if shared is not None else MOE_F32, _ptr(x), _dt(x), T, K, H,
+          ctypes.byref(post.c), ctypes.byref(gate.c), pdt, _ptr(r), nx, _ptr(n))
+
+
+def moe_norm_residual_backward(dr, y, post, gate, dy, workspace=None, dweight=None, dbias=None,
+                               dchannel=None, dtoken=None, stream=None):
+    """Gradients of moe_norm_residual's y, of post's parameters and of the gates, where given;
+    that of x is dr itself."""
+    T, H = _tokens(y, "y")
+    _shaped(dr, (T, H), "dr")
+    _shaped(dy, (T, H), "dy", y.dtype)
+    _optional(H, dweight=dweight, dbias=dbias, dchannel=dchannel)
+    if dtoken is not None:
+        _shaped(dtoken, (T,), "dtoken", torch.float32)
+    dev = _one_device(y, dr, dy, dweight, dbias, dchannel, dtoken, workspace)
+    pdt = _params(T, H, dev, (post,), gate)
+    ws, n = _workspace(workspace)
+    _call(lib().moe_norm_residual_backward, dev, stream, _ptr(dr), _dt(dr), _ptr(y), _dt(y), T, H,
+          ctypes.byref(post.c), ctypes.byref(gate.c), pdt, _ptr(dy), _ptr(dweight), _ptr(dbias),
+          _ptr(dchannel), _ptr(dtoken), ws, n)

@@ -6,12 +6,6 @@
 
 namespace moe {
 
-// DPP controls (gfx9 encoding): quad permutations and row mirrors
-constexpr int kQuadXor1 = 0xB1;     // quad_perm [1,0,3,2]
-constexpr int kQuadXor2 = 0x4E;     // quad_perm [2,3,0,1]
-constexpr int kRowHalfMirror = 0x141;
-constexpr int kRowMirror = 0x140;
-
 template <int CTRL>
 __device__ __forceinline__ float dpp_max(float v) {
   const int o = __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false);

@@ -143,6 +143,13 @@ class MoELayer:
         """One pass; gate_up_events = (a, b): HIP events recorded on the current
         stream just before and after the grouped gate/up launch (the benchmark
         times the dominant kernel inside the pass with them)."""
+        self.experts(gate_up_events)
+        self.combine()
+        return self.out
+
+    def experts(self, gate_up_events=None):
+        """The pass up to its combine: y_pairs, topk_w and, with shared experts,
+        shared_out are ready on the current stream."""
         cur = torch.cuda.current_stream()
         if self.has_shared:
             fork = torch.cuda.Event()
@@ -170,8 +177,6 @@ class MoELayer:
         self.down()
         if self.has_shared:
             cur.wait_event(join)
-        self.combine()
-        return self.out
 
     def dense_fa(self):
         d = self.inputs
@@ -186,3 +191,40 @@ class MoELayer:
         B.dense_ffn_fa(self.inputs["x"], self.inputs["wpa13"], self.inputs["wpa2"], self.pa_ws,
                        self.pa_out, self.sched)
         return self.pa_out
+
+
+class MoEBlock:
+    """A MoELayer on a residual stream: r = x + gate * post(layer(pre(x))), and, with a
+    next norm, n = next_norm(r), the next block's input.  The layer's combine, the norm
+    after it, the gate, the residual sum and the next norm are one launch.
+
+    The layer's inputs["x"] is written by the pre norm.  router(tokens, logits), when
+    given, fills inputs["logits"] from it on the current stream (the router's product
+    is the caller's); without one they are there before each pass.  Buffers are
+    allocated once; a pass only enqueues work on the current stream."""
+
+    def __init__(self, layer, pre, post, gate=None, next_norm=None, router=None,
+                 stream_dtype=torch.bfloat16):
+        self.layer, self.pre, self.post, self.next_norm = layer, pre, post, next_norm
+        self.gate = gate if gate is not None else B.Gate()
+        self.router = router
+        x = layer.inputs["x"]
+        self.r = torch.empty(x.shape, dtype=stream_dtype, device=x.device)
+        self.n = torch.empty_like(x) if next_norm is not None else None
+
+    def forward(self, x):
+        """One pass over the residual stream x [T,H] (of stream_dtype); returns (r, n)."""
+        B.moe_norm(x, self.pre, self.layer.inputs["x"])
+        return self.normed(x)
+
+    def normed(self, x):
+        """forward(x) where the layer's inputs["x"] holds pre(x) already, as written by the
+        block before (its n is that tensor)."""
+        layer = self.layer
+        if self.router is not None:
+            self.router(layer.inputs["x"], layer.inputs["logits"])
+        layer.experts()
+        B.moe_combine_norm_residual(layer.y_pairs[:layer.T * layer.shape.topk], layer.topk_w, x,
+                                    self.post, self.gate, self.r, pre=self.next_norm, n=self.n,
+                                    shared=layer.shared_out if layer.has_shared else None)
+        return self.r, self.n

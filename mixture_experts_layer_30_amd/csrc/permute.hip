@@ -2,201 +2,271 @@
 // (what each computes: include/moe_layer.h).
 //
 // Everything here is bound by memory: a row element is moved once and takes at
-// most one multiply-add.  The kernels go by token, not by row: a token's row is
-// read once for its K copies (permute, unpermute_backward) and its K rows are
-// summed in slot order in registers (unpermute), so no sum needs atomics.  The
-// padding rows have no token; workgroups past the tokens' zero them, taking the
-// alignment's blocks one by one (each belongs to one expert, whose rows end at
-// offsets[e] + counts[e]).
+// most one multiply-add.  The kernels go by token or by pair, not by alignment
+// row: a token's row is read once for its K copies (permute), its K rows are
+// summed in slot order in registers (unpermute), and a pair's dot product stays
+// in one wavefront (unpermute_backward), so no sum needs atomics.  The padding
+// rows have no token; workgroups past the others' zero them, expert by expert.
+//
+// A unit of work is kLanes vectors of 16 bytes of one token's or pair's row, on
+// as many lanes: a wavefront where the row fills one (its row index and weight
+// then sit in scalar registers, and its loads take the row's address from them),
+// else the smallest power of two of lanes that holds the row, several rows to a
+// wavefront.
 #include "common.h"
 #include "kernels.h"
 
 namespace moe {
 
 constexpr int kThreads = 256;
-constexpr int kPadRows = 16;   // padding rows of one block that a workgroup zeroes at a time
+constexpr int kWaves = kThreads / kWave;
 
-// Zeroes the padding rows of work item `item`: rows sub * kPadRows .. of block
-// item / subs (rows of nv 16-byte vectors).
-__device__ __forceinline__ void zero_padding(int64_t item, int subs, int block_m, int E,
-                                             const int32_t* counts, const int32_t* offsets,
-                                             const int32_t* block_expert, int nv, u32x4* rows) {
-  const int64_t b = item / subs;
-  const int e = block_expert[b];
-  if (e < 0 || e >= E) return;
-  const int64_t lo = b * block_m + (item - b * subs) * kPadRows;
-  int64_t end = lo + kPadRows;
-  if (end > (b + 1) * block_m) end = (b + 1) * block_m;
-  int64_t r = (int64_t)offsets[e] + counts[e];
-  if (r < lo) r = lo;
-  const u32x4 z = {0, 0, 0, 0};
-  for (; r < end; ++r)
-    for (int v = threadIdx.x; v < nv; v += kThreads) rows[r * nv + v] = z;
+// The rows are streamed: a buffer of them is far larger than the caches, each
+// element is used once, and stores of whole lines that bypass them leave the
+// tokens, which are read K times over, in place.
+__device__ __forceinline__ u32x4 stream_load(const u32x4* p) {
+  return __builtin_nontemporal_load(p);
+}
+__device__ __forceinline__ void stream_store(u32x4* p, u32x4 v) {
+  __builtin_nontemporal_store(v, p);
 }
 
-// rows[inv_pos[t*K + k]] = x[t].  tx lanes (a power of two) share a token and
-// cover tx of its nv vectors; units = token groups x chunks of tx vectors.
+// The 16 / kBytes elements of a vector as fp32, and back.
+template <class S>
+struct Vec {
+  static constexpr int N = 16 / S::kBytes;
+};
+template <class S>
+__device__ __forceinline__ void unpack(u32x4 r, float* v) {
+  if constexpr (S::kBytes == 2) {
+    const uint32_t q[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(q[j] << 16);
+      v[2 * j + 1] = __uint_as_float(q[j] & 0xffff0000u);
+    }
+  } else {
+    const f32x4 a = __builtin_bit_cast(f32x4, r);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+}
+template <class S>
+__device__ __forceinline__ u32x4 pack(const float* v) {
+  if constexpr (S::kBytes == 2) {
+    u32x4 r;
+    r.x = pack_bf16x2(v[0], v[1]);
+    r.y = pack_bf16x2(v[2], v[3]);
+    r.z = pack_bf16x2(v[4], v[5]);
+    r.w = pack_bf16x2(v[6], v[7]);
+    return r;
+  } else {
+    return __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+  }
+}
+
+// N (4 or 8) consecutive elements of the tokens' own buffers, whose type may
+// differ from the rows'.
+template <class S, int N>
+__device__ __forceinline__ void load_n(const typename S::T* p, float* v) {
+  if constexpr (N == 8) {
+    load8f<S>(p, v);
+  } else if constexpr (S::kBytes == 4) {
+    unpack<F32>(*reinterpret_cast<const u32x4*>(p), v);
+  } else {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = __uint_as_float(q.x << 16);
+    v[1] = __uint_as_float(q.x & 0xffff0000u);
+    v[2] = __uint_as_float(q.y << 16);
+    v[3] = __uint_as_float(q.y & 0xffff0000u);
+  }
+}
+template <class S, int N>
+__device__ __forceinline__ void store_n(typename S::T* p, const float* v) {
+  if constexpr (N == 8) store8f<S>(p, v);
+  else store_out4<S>(p, f32x4{v[0], v[1], v[2], v[3]});
+}
+
+// Sum over the aligned group of kLanes lanes, in every lane of it.
+template <int kLanes>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (kLanes == 64) {
+    return wave_sum(v);
+  } else {
+    v = dpp_add<kQuadXor1>(v);
+    v = dpp_add<kQuadXor2>(v);
+    v = dpp_add<kRowHalfMirror>(v);
+    if constexpr (kLanes >= 16) v = dpp_add<kRowMirror>(v);
+    if constexpr (kLanes == 32)   // lane i and lane i ^ 16 (ds_swizzle, bit mode: xor mask 16)
+      v += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));
+    return v;
+  }
+}
+
+// The unit that this lane works on in workgroup b; scalar where it is the
+// wavefront's.
+template <int kLanes>
+__device__ __forceinline__ uint32_t unit_of(uint32_t b) {
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t first = (b * kWaves + wave) * (kWave / kLanes);
+  return kLanes == kWave ? first : first + (threadIdx.x & (kWave - 1)) / kLanes;
+}
+
+// The padding rows: expert e's are offsets[e] + counts[e] .. offsets[e + 1] - 1,
+// one run of memory, zeroed by `subs` workgroups.
+struct Padding {
+  const int32_t* counts;
+  const int32_t* offsets;
+  int subs;
+};
+
+// Zeroes share item % subs of the padding rows (of nv vectors) of expert item / subs.
+__device__ __forceinline__ void zero_padding(uint32_t item, const Padding& pad, int nv, int64_t cap,
+                                             u32x4* rows) {
+  const uint32_t e = item / (uint32_t)pad.subs;
+  int64_t first = (int64_t)pad.offsets[e] + pad.counts[e], end = pad.offsets[e + 1];
+  if (first < 0) first = 0;
+  if (end > cap) end = cap;
+  const u32x4 z = {0, 0, 0, 0};
+  const int64_t stride = (int64_t)pad.subs * kThreads;
+  for (int64_t i = first * nv + (item - e * pad.subs) * kThreads + threadIdx.x; i < end * nv;
+       i += stride)
+    stream_store(rows + i, z);
+}
+
+// rows[inv_pos[t*K + k]] = x[t] (rows of nv vectors; a token takes `chunks`
+// units), then the padding rows in `pads` items.
+template <int kLanes>
 __global__ __launch_bounds__(kThreads) void permute_kernel(
-    const u32x4* __restrict__ x, int64_t T, int K, int nv, int tx_log2, int chunks, int64_t units,
-    const int32_t* __restrict__ inv_pos, int64_t cap, u32x4* __restrict__ rows, int64_t pad_items,
-    int pad_subs, int block_m, int E, const int32_t* __restrict__ counts,
-    const int32_t* __restrict__ offsets, const int32_t* __restrict__ block_expert) {
-  const int tx = 1 << tx_log2;
-  const int ty = kThreads >> tx_log2;
-  for (int64_t u = blockIdx.x; u < units + pad_items; u += gridDim.x) {
-    if (u >= units) {
-      zero_padding(u - units, pad_subs, block_m, E, counts, offsets, block_expert, nv, rows);
+    const u32x4* __restrict__ x, uint32_t T, int K, int nv, uint32_t chunks, uint32_t groups,
+    const int32_t* __restrict__ inv_pos, int64_t cap, u32x4* __restrict__ rows, uint32_t pads,
+    Padding pad) {
+  for (uint32_t b = blockIdx.x; b < groups + pads; b += gridDim.x) {
+    if (b >= groups) {
+      zero_padding(b - groups, pad, nv, cap, rows);
       continue;
     }
-    const int64_t g = u / chunks;
-    const int v = (int)(u - g * chunks) * tx + (threadIdx.x & (tx - 1));
-    const int64_t t = g * ty + (threadIdx.x >> tx_log2);
+    const uint32_t u = unit_of<kLanes>(b);
+    const uint32_t t = u / chunks;
+    const int v = (u - t * chunks) * kLanes + threadIdx.x % kLanes;
     if (t >= T || v >= nv) continue;
-    const u32x4 d = x[t * nv + v];
+    const u32x4 d = x[(int64_t)t * nv + v];
+    const int32_t* pos = inv_pos + (int64_t)t * K;
     for (int k = 0; k < K; ++k) {
-      const int64_t r = inv_pos[t * K + k];
-      if (r >= 0 && r < cap) rows[r * nv + v] = d;
+      const int64_t r = pos[k];
+      if (r >= 0 && r < cap) stream_store(rows + r * nv + v, d);
     }
   }
 }
 
-constexpr int kSlots = 4;   // rows in flight per thread
+constexpr int kSlots = 4;   // rows in flight per lane
 
-// out[t] = sum_k w[t][k] rows[inv_pos[t*K + k]] (+ shared[t]): a thread owns 8
-// elements of a token.
-template <class SR, class SS, class SO, bool kWeighted>
+// out[t] = sum_k w[t][k] rows[inv_pos[t*K + k]] (+ shared[t]); w null: ones.
+template <class SR, class SS, class SO, int kLanes>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(
-    const typename SR::T* __restrict__ rows, const float* __restrict__ w,
-    const typename SS::T* __restrict__ shared, int64_t T, int K, int H, int tx_log2, int chunks,
-    int64_t units, const int32_t* __restrict__ inv_pos, int64_t cap,
+    const u32x4* __restrict__ rows, const float* __restrict__ w,
+    const typename SS::T* __restrict__ shared, uint32_t T, int K, int nv, uint32_t chunks,
+    uint32_t groups, const int32_t* __restrict__ inv_pos, int64_t cap,
     typename SO::T* __restrict__ out) {
-  const int tx = 1 << tx_log2;
-  const int ty = kThreads >> tx_log2;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
-    const int64_t g = u / chunks;
-    const int h = ((int)(u - g * chunks) * tx + (threadIdx.x & (tx - 1))) * 8;
-    const int64_t t = g * ty + (threadIdx.x >> tx_log2);
-    if (t >= T || h >= H) continue;
-    float acc[8];
+  constexpr int N = Vec<SR>::N;
+  for (uint32_t b = blockIdx.x; b < groups; b += gridDim.x) {
+    const uint32_t u = unit_of<kLanes>(b);
+    const uint32_t t = u / chunks;
+    const int v = (u - t * chunks) * kLanes + threadIdx.x % kLanes;
+    if (t >= T || v >= nv) continue;
+    const int32_t* pos = inv_pos + (int64_t)t * K;
+    float acc[N];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[j] = 0.0f;
+    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
     for (int k0 = 0; k0 < K; k0 += kSlots) {
-      float v[kSlots][8], wk[kSlots];
+      u32x4 d[kSlots];
+      float wk[kSlots];
       bool use[kSlots];
 #pragma unroll
       for (int j = 0; j < kSlots; ++j) {
         use[j] = false;
         if (k0 + j < K) {
-          const int64_t r = inv_pos[t * K + k0 + j];
-          wk[j] = kWeighted ? w[t * K + k0 + j] : 1.0f;
+          const int64_t r = pos[k0 + j];
+          wk[j] = w ? w[(int64_t)t * K + k0 + j] : 1.0f;
           use[j] = r >= 0 && r < cap && wk[j] != 0.0f;
-          if (use[j]) load8f<SR>(rows + r * H + h, v[j]);
+          if (use[j]) d[j] = stream_load(rows + r * nv + v);
         }
       }
 #pragma unroll
       for (int j = 0; j < kSlots; ++j)
         if (use[j]) {
+          float y[N];
+          unpack<SR>(d[j], y);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) acc[i] = fmaf(wk[j], v[j][i], acc[i]);
+          for (int i = 0; i < N; ++i) acc[i] = fmaf(wk[j], y[i], acc[i]);
         }
     }
+    const int64_t o = ((int64_t)t * nv + v) * N;
     if (shared) {
-      float v[8];
-      load8f<SS>(shared + t * H + h, v);
+      float s[N];
+      load_n<SS, N>(shared + o, s);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] += v[i];
+      for (int i = 0; i < N; ++i) acc[i] += s[i];
     }
-    store8f<SO>(out + t * H + h, acc);
+    store_n<SO, N>(out + o, acc);
   }
 }
 
-constexpr int kGradSlots = 8;   // slots whose dot products a pass over the token holds
 
-// drows[r] = w[t][k] dout[t] and dw[t][k] = <dout[t], rows[r]> for the rows r of
-// token t.  kWaves wavefronts share a token (its elements dealt 8 to a lane),
-// kThreads / 64 / kWaves tokens a workgroup; the dot products of up to 8 slots
-// run together, are summed over each wavefront and then in wavefront order.
-template <class S, int kWaves>
+// drows[r] = w[p] dout[t] and dw[p] = <dout[t], rows[r]> for the row r of pair p
+// = t*K + k, a unit each: dout's row is read K times over, from the caches.  A
+// lane reads an element of rows before it writes that of drows (they may be one
+// buffer).
+template <class S, int kLanes>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
-    const typename S::T* __restrict__ dout, const typename S::T* rows,
-    const float* __restrict__ w, int64_t T, int K, int H, int64_t units,
-    const int32_t* __restrict__ inv_pos, int64_t cap, typename S::T* drows,
-    float* __restrict__ dw, int64_t pad_items, int pad_subs, int block_m, int E,
-    const int32_t* __restrict__ counts, const int32_t* __restrict__ offsets,
-    const int32_t* __restrict__ block_expert) {
-  constexpr int kTokens = kThreads / kWave / kWaves;
-  __shared__ float part[kThreads / kWave][kGradSlots];
-  const int wave = threadIdx.x / kWave;
-  const int lane = threadIdx.x & (kWave - 1);
-  for (int64_t u = blockIdx.x; u < units + pad_items; u += gridDim.x) {
-    if (u >= units) {   // (only where drows is written)
-      zero_padding(u - units, pad_subs, block_m, E, counts, offsets, block_expert,
-                   H * S::kBytes / 16, reinterpret_cast<u32x4*>(drows));
+    const u32x4* __restrict__ dout, const u32x4* rows, const float* __restrict__ w,
+    uint32_t pairs, int K, int nv, uint32_t groups, const int32_t* __restrict__ inv_pos,
+    int64_t cap, u32x4* drows, float* __restrict__ dw, uint32_t pads, Padding pad) {
+  constexpr int N = Vec<S>::N;
+  constexpr int kSteps = kLanes == kWave ? 4 : 1;   // vectors of a row in flight per lane
+  for (uint32_t b = blockIdx.x; b < groups + pads; b += gridDim.x) {
+    if (b >= groups) {   // (there are none where drows is null)
+      zero_padding(b - groups, pad, nv, cap, drows);
       continue;
     }
-    const int64_t t = u * kTokens + wave / kWaves;
-    const bool live = t < T;
-    for (int k0 = 0; k0 < K; k0 += kGradSlots) {
-      int64_t r[kGradSlots];
-      float wk[kGradSlots], acc[kGradSlots];
+    const uint32_t p = unit_of<kLanes>(b);
+    const int lane = threadIdx.x % kLanes;
+    // (a group past the pairs keeps its lanes: they take part in the sums)
+    const int64_t r = p < pairs ? inv_pos[p] : -1;
+    const bool used = r >= 0 && r < cap;
+    const float wk = w && p < pairs ? w[p] : 1.0f;
+    float acc = 0.0f;
+    if (used) {
+      const u32x4* g0 = dout + (int64_t)(p / (uint32_t)K) * nv;
+      const int64_t r0 = r * nv;
+      for (int v0 = lane; v0 < nv; v0 += kSteps * kLanes) {
+        u32x4 dg[kSteps], dv[kSteps];
 #pragma unroll
-      for (int j = 0; j < kGradSlots; ++j) {
-        r[j] = -1;
-        wk[j] = 1.0f;
-        acc[j] = 0.0f;
-        if (live && k0 + j < K) {
-          r[j] = inv_pos[t * K + k0 + j];
-          if (r[j] >= cap) r[j] = -1;
-          if (w) wk[j] = w[t * K + k0 + j];
-        }
+        for (int i = 0; i < kSteps; ++i)
+          if (v0 + i * kLanes < nv) {
+            dg[i] = g0[v0 + i * kLanes];
+            if (dw) dv[i] = stream_load(rows + r0 + v0 + i * kLanes);
+          }
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i)
+          if (v0 + i * kLanes < nv) {
+            float g[N], y[N];
+            unpack<S>(dg[i], g);
+            if (dw) {
+              unpack<S>(dv[i], y);
+#pragma unroll
+              for (int j = 0; j < N; ++j) acc = fmaf(g[j], y[j], acc);
+            }
+            if (drows) {
+#pragma unroll
+              for (int j = 0; j < N; ++j) g[j] *= wk;
+              stream_store(drows + r0 + v0 + i * kLanes, pack<S>(g));
+            }
+          }
       }
-      if (live)
-        for (int h = ((wave % kWaves) * kWave + lane) * 8; h < H; h += kWaves * kWave * 8) {
-          float g[8];
-          load8f<S>(dout + t * H + h, g);
-          if (dw) {
-            float v[kGradSlots][8];
-#pragma unroll
-            for (int j = 0; j < kGradSlots; ++j)
-              if (r[j] >= 0) load8f<S>(rows + r[j] * H + h, v[j]);
-#pragma unroll
-            for (int j = 0; j < kGradSlots; ++j)
-              if (r[j] >= 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) acc[j] = fmaf(g[i], v[j][i], acc[j]);
-              }
-          }
-          if (drows) {
-#pragma unroll
-            for (int j = 0; j < kGradSlots; ++j)
-              if (r[j] >= 0) {
-                float s[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] = wk[j] * g[i];
-                store8f<S>(drows + r[j] * H + h, s);
-              }
-          }
-        }
-      if (dw) {
-#pragma unroll
-        for (int j = 0; j < kGradSlots; ++j) acc[j] = wave_sum(acc[j]);
-        if (kWaves == 1) {
-#pragma unroll
-          for (int j = 0; j < kGradSlots; ++j)
-            if (live && lane == j && k0 + j < K) dw[t * K + k0 + j] = acc[j];
-        } else {
-#pragma unroll
-          for (int j = 0; j < kGradSlots; ++j)
-            if (lane == j) part[wave][j] = acc[j];
-          __syncthreads();
-          if (live && wave % kWaves == 0 && lane < kGradSlots && k0 + lane < K) {
-            float sum = 0.0f;
-            for (int i = 0; i < kWaves; ++i) sum += part[wave + i][lane];
-            dw[t * K + k0 + lane] = sum;
-          }
-          __syncthreads();
-        }
-      }
+    }
+    if (dw) {
+      acc = lanes_sum<kLanes>(acc);
+      if (lane == 0 && p < pairs) dw[p] = acc;
     }
   }
 }
@@ -208,9 +278,8 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ w, const float* __restrict__ dw,
     int64_t T, int E, int K, float* __restrict__ dlogits) {
   const int lane = threadIdx.x & (kWave - 1);
-  const int64_t waves = (int64_t)gridDim.x * (kThreads / kWave);
-  for (int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; t < T;
-       t += waves) {
+  const int64_t waves = (int64_t)gridDim.x * kWaves;
+  for (int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave; t < T; t += waves) {
     // at most 256 slots: 4 a lane
     int id[4];
     float g[4], s = 0.0f;
@@ -249,36 +318,50 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
 
 namespace {
 
-// Lanes that share a token: the smallest power of two covering its nv vectors,
-// between 8 and the workgroup.
-int lanes_log2(int nv) {
-  int l = 3;
-  while (l < 8 && (1 << l) < nv) ++l;
-  return l;
-}
-
 constexpr int64_t kMaxGrid = 1 << 20;   // workgroups; the kernels loop past it
 
-unsigned grid_of(int64_t units) { return (unsigned)(units < kMaxGrid ? units : kMaxGrid); }
+unsigned grid_of(int64_t groups) { return (unsigned)(groups < kMaxGrid ? groups : kMaxGrid); }
 
-int pad_subs(int block_m) { return (block_m + kPadRows - 1) / kPadRows; }
+// f(lanes): the lanes of a unit as a constant, for rows of nv vectors.
+template <class F>
+hipError_t with_lanes(int nv, F f) {
+  if (nv > 32) f(std::integral_constant<int, 64>());
+  else if (nv > 16) f(std::integral_constant<int, 32>());
+  else if (nv > 8) f(std::integral_constant<int, 16>());
+  else f(std::integral_constant<int, 8>());
+  return hipGetLastError();
+}
+
+// Workgroups that `units` units of `lanes` lanes take.
+int64_t groups_of(int64_t units, int lanes) {
+  const int per = kThreads / lanes;
+  return (units + per - 1) / per;
+}
+
+// Up to kPadWorkgroups workgroups for an expert's padding: block-wise padding
+// leaves at most block_m - 1 rows.
+constexpr int kPadWorkgroups = 16;
+
+Padding padding_of(const RowMap& rm) {
+  const int most = rm.block_m - 1;
+  return Padding{rm.counts, rm.offsets, most < kPadWorkgroups ? most : kPadWorkgroups};
+}
 
 template <class SR, class SS, class SO>
 hipError_t launch_unpermute_t(const void* rows, const float* w, const void* shared, int64_t T,
                               int K, int H, const int32_t* inv_pos, int64_t cap, void* out,
                               hipStream_t s) {
-  const int l = lanes_log2(H / 8);
-  const int ty = kThreads >> l, chunks = (H / 8 + (1 << l) - 1) >> l;
-  const int64_t units = (T + ty - 1) / ty * chunks;
-  auto go = [&](auto kernel) {
-    hipLaunchKernelGGL(kernel, dim3(grid_of(units)), dim3(kThreads), 0, s,
-                       static_cast<const typename SR::T*>(rows), w,
-                       static_cast<const typename SS::T*>(shared), T, K, H, l, chunks, units,
-                       inv_pos, cap, static_cast<typename SO::T*>(out));
-  };
-  if (w) go(unpermute_kernel<SR, SS, SO, true>);
-  else go(unpermute_kernel<SR, SS, SO, false>);
-  return hipGetLastError();
+  const int nv = H / Vec<SR>::N;
+  return with_lanes(nv, [&](auto lanes) {
+    constexpr int kLanes = decltype(lanes)::value;
+    const int chunks = (nv + kLanes - 1) / kLanes;
+    const int64_t groups = groups_of(T * chunks, kLanes);
+    hipLaunchKernelGGL((unpermute_kernel<SR, SS, SO, kLanes>), dim3(grid_of(groups)),
+                       dim3(kThreads), 0, s, static_cast<const u32x4*>(rows), w,
+                       static_cast<const typename SS::T*>(shared), (uint32_t)T, K, nv,
+                       (uint32_t)chunks, (uint32_t)groups, inv_pos, cap,
+                       static_cast<typename SO::T*>(out));
+  });
 }
 
 template <class SR, class SS>
@@ -290,20 +373,40 @@ hipError_t unpermute_out(const void* rows, const float* w, const void* shared, i
              : launch_unpermute_t<SR, SS, BF16>(rows, w, shared, T, K, H, inv_pos, cap, out, s);
 }
 
+template <class S>
+hipError_t unpermute_backward_t(const void* dout, const void* rows, const float* w, int64_t T,
+                                int K, int H, const RowMap& rm, int E, int64_t cap, void* drows,
+                                float* dw, hipStream_t s) {
+  const int nv = H / Vec<S>::N;
+  const Padding pad = padding_of(rm);
+  const int64_t pads = drows ? E * pad.subs : 0;   // (blocks of one row leave none)
+  return with_lanes(nv, [&](auto lanes) {
+    constexpr int kLanes = decltype(lanes)::value;
+    const int64_t groups = groups_of(T * K, kLanes);
+    hipLaunchKernelGGL((unpermute_backward_kernel<S, kLanes>), dim3(grid_of(groups + pads)),
+                       dim3(kThreads), 0, s, static_cast<const u32x4*>(dout),
+                       static_cast<const u32x4*>(rows), w, (uint32_t)(T * K), K, nv,
+                       (uint32_t)groups, rm.inv_pos, cap, static_cast<u32x4*>(drows), dw,
+                       (uint32_t)pads, pad);
+  });
+}
+
 }  // namespace
 
 hipError_t launch_permute(const void* x, int dt, int64_t T, int K, int H, const RowMap& rm, int E,
                           int64_t cap, void* rows, hipStream_t s) {
-  const int nv = H / 8 * (dt == kDtF32 ? 2 : 1);
-  const int l = lanes_log2(nv);
-  const int ty = kThreads >> l, chunks = (nv + (1 << l) - 1) >> l;
-  const int64_t units = (T + ty - 1) / ty * chunks;
-  const int64_t pad = rm.block_m > 1 ? cap / rm.block_m * pad_subs(rm.block_m) : 0;
-  hipLaunchKernelGGL(permute_kernel, dim3(grid_of(units + pad)), dim3(kThreads), 0, s,
-                     static_cast<const u32x4*>(x), T, K, nv, l, chunks, units, rm.inv_pos, cap,
-                     static_cast<u32x4*>(rows), pad, pad_subs(rm.block_m), rm.block_m, E,
-                     rm.counts, rm.offsets, rm.block_expert);
-  return hipGetLastError();
+  const int nv = dt == kDtF32 ? H / 4 : H / 8;
+  const Padding pad = padding_of(rm);
+  const int64_t pads = E * pad.subs;   // (blocks of one row leave none)
+  return with_lanes(nv, [&](auto lanes) {
+    constexpr int kLanes = decltype(lanes)::value;
+    const int chunks = (nv + kLanes - 1) / kLanes;
+    const int64_t groups = groups_of(T * chunks, kLanes);
+    hipLaunchKernelGGL((permute_kernel<kLanes>), dim3(grid_of(groups + pads)), dim3(kThreads), 0,
+                       s, static_cast<const u32x4*>(x), (uint32_t)T, K, nv, (uint32_t)chunks,
+                       (uint32_t)groups, rm.inv_pos, cap, static_cast<u32x4*>(rows),
+                       (uint32_t)pads, pad);
+  });
 }
 
 hipError_t launch_unpermute(const void* rows, int rdt, const float* w, const void* shared, int sdt,
@@ -321,35 +424,15 @@ hipError_t launch_unpermute(const void* rows, int rdt, const float* w, const voi
 hipError_t launch_unpermute_backward(const void* dout, const void* rows, int dt, const float* w,
                                      int64_t T, int K, int H, const RowMap& rm, int E, int64_t cap,
                                      void* drows, float* dw, hipStream_t s) {
-  const int64_t pad =
-      drows && rm.block_m > 1 ? cap / rm.block_m * pad_subs(rm.block_m) : 0;
-  // one wavefront holds a token of up to 1024 elements in two steps; a longer one
-  // takes the workgroup
-  const bool one = H <= 1024;
-  const int64_t units = one ? (T + 3) / 4 : T;
-  auto go = [&](auto kernel, auto* type) {
-    typedef std::remove_pointer_t<decltype(type)> E_;
-    hipLaunchKernelGGL(kernel, dim3(grid_of(units + pad)), dim3(kThreads), 0, s,
-                       static_cast<const E_*>(dout), static_cast<const E_*>(rows), w, T, K, H,
-                       units, rm.inv_pos, cap, static_cast<E_*>(drows), dw, pad,
-                       pad_subs(rm.block_m), rm.block_m, E, rm.counts, rm.offsets,
-                       rm.block_expert);
-  };
-  if (dt == kDtF32) {
-    if (one) go(unpermute_backward_kernel<F32, 1>, (float*)nullptr);
-    else go(unpermute_backward_kernel<F32, 4>, (float*)nullptr);
-  } else {
-    if (one) go(unpermute_backward_kernel<BF16, 1>, (uint16_t*)nullptr);
-    else go(unpermute_backward_kernel<BF16, 4>, (uint16_t*)nullptr);
-  }
-  return hipGetLastError();
+  return dt == kDtF32 ? unpermute_backward_t<F32>(dout, rows, w, T, K, H, rm, E, cap, drows, dw, s)
+                      : unpermute_backward_t<BF16>(dout, rows, w, T, K, H, rm, E, cap, drows, dw,
+                                                   s);
 }
 
 hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw, int64_t T,
                                  int E, int K, float* dlogits, hipStream_t s) {
-  const int64_t units = (T + kThreads / kWave - 1) / (kThreads / kWave);
-  hipLaunchKernelGGL(route_backward_kernel, dim3(grid_of(units)), dim3(kThreads), 0, s, ids, w, dw,
-                     T, E, K, dlogits);
+  hipLaunchKernelGGL(route_backward_kernel, dim3(grid_of((T + kWaves - 1) / kWaves)),
+                     dim3(kThreads), 0, s, ids, w, dw, T, E, K, dlogits);
   return hipGetLastError();
 }
 

@@ -260,8 +260,10 @@ moe_status moe_norm_backward(const void* dn, moe_dtype odt, const void* x, moe_d
   }
   if (T > 0 && (!good(dn, 16) || !good(x, 16) || !good(dx, 16) || !optional(dres, 16)))
     return null_pointer(what);
-  return hip_status(moe::launch_norm_backward(dn, odt, x, xdt, dres, T, H, spec, pdt, dx, dweight,
-                                              dbias, (float*)workspace, (hipStream_t)stream),
+  const moe::GateSpec none{1.0f, nullptr, nullptr};
+  return hip_status(moe::launch_norm_backward(dn, odt, x, xdt, dres, T, H, spec, none, pdt, dx,
+                                              dweight, dbias, nullptr, nullptr, (float*)workspace,
+                                              (hipStream_t)stream),
                     what);
 }
 
@@ -348,9 +350,9 @@ moe_status moe_norm_residual_backward(const void* dr, moe_dtype xdt, const void*
     if (st) return st;
   }
   if (T > 0 && (!good(dr, 16) || !good(y, 16) || !good(dy, 16))) return null_pointer(what);
-  return hip_status(moe::launch_norm_residual_backward(dr, xdt, y, ydt, T, H, a, g, pdt, dy,
-                                                       dweight, dbias, dchannel, dtoken,
-                                                       (float*)workspace, (hipStream_t)stream),
+  return hip_status(moe::launch_norm_backward(dr, xdt, y, ydt, nullptr, T, H, a, g, pdt, dy,
+                                              dweight, dbias, dchannel, dtoken, (float*)workspace,
+                                              (hipStream_t)stream),
                     what);
 }
 

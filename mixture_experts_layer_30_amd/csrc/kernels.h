@@ -53,16 +53,14 @@ hipError_t launch_combine_norm_residual(const void* y, int ydt, const float* w, 
                                         int64_t T, int H, const NormSpec& post,
                                         const GateSpec& gate, int pdt, void* r,
                                         const NormSpec& pre, void* n, hipStream_t s);
-// fp32 partial sums of the two backward launches (all the parameter gradients)
+// fp32 partial sums of a backward launch (all the parameter gradients)
 int64_t norm_workspace_floats(int64_t T, int H);
-hipError_t launch_norm_backward(const void* dn, int odt, const void* x, int xdt, const void* dres,
-                                int64_t T, int H, const NormSpec& n, int pdt, void* dx,
-                                float* dweight, float* dbias, float* workspace, hipStream_t s);
-hipError_t launch_norm_residual_backward(const void* dr, int xdt, const void* y, int ydt,
-                                         int64_t T, int H, const NormSpec& post,
-                                         const GateSpec& gate, int pdt, void* dy, float* dweight,
-                                         float* dbias, float* dchannel, float* dtoken,
-                                         float* workspace, hipStream_t s);
+// From e, the gradient of gate * norm(v): dv (+ dres, null: none; as v), the
+// parameters' gradients and the gates', each where not null.
+hipError_t launch_norm_backward(const void* e, int edt, const void* v, int vdt, const void* dres,
+                                int64_t T, int H, const NormSpec& n, const GateSpec& gate, int pdt,
+                                void* dv, float* dweight, float* dbias, float* dchannel,
+                                float* dtoken, float* workspace, hipStream_t s);
 
 // Token rows of a grouped (or dense) GEMM.  Grouped: expert e owns the rows
 // offsets[e] .. offsets[e] + counts[e] - 1 of the alignment; row r holds pair

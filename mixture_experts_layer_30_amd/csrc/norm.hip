@@ -2,12 +2,18 @@
 // gate and residual scale, and their gradients (what each computes:
 // include/moe_layer.h).
 //
-// A workgroup holds one row at a time in registers, 8 elements of a lane's at a
-// stride of the workgroup (kVec of them): the statistics, the normed row and
-// the residual sum all come from one read.  Row sums go over the wavefront by
-// lane permutations, then over the wavefronts in order through LDS; a layer
-// norm sums the centred squares in a second pass over the registers, since the
-// difference of the two raw moments loses the variance of a row far from zero.
+// All of it is bound by memory.  A workgroup holds one row at a time in
+// registers, so that the statistics, the normed row, the residual sum and the
+// next norm come from one read, and asks for its next row before it works on
+// this one.  Row sums go over the wavefront by lane permutations, then over the
+// wavefronts in order through LDS; a layer norm sums the centred squares in a
+// second pass over the registers, since the difference of the two raw moments
+// loses the variance of a row far from zero.
+//
+// Rows are read and written through buffer descriptors of the row's length: a
+// lane past its end reads zeros and writes nothing, and a row that is not there
+// (no bias, a slot of weight 0) has length 0, so the kernels have no branches
+// around their loads and address rows from scalar registers.
 //
 // Parameter gradients are sums down the columns: each workgroup keeps those of
 // its rows in registers and writes one fp32 row of partial sums; a second
@@ -19,420 +25,660 @@ namespace moe {
 
 constexpr int kMaxWaves = 16;
 
-// Sums of kN values over the workgroup's `waves` wavefronts, in every lane.
-// buf [kMaxWaves * kN]; consecutive calls alternate between two buffers (a
-// wavefront may still read the last call's while another is in the next).
-template <int kN>
-__device__ __forceinline__ void block_sum(float (&v)[kN], int waves, float* buf) {
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = wave_sum(v[i]);
-  if (waves == 1) return;
-  const int lane = threadIdx.x & (kWave - 1);
-  const int wave = threadIdx.x / kWave;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) buf[wave * kN + i] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kN; ++i) {
-    float s = lane < waves ? buf[lane * kN + i] : 0.0f;   // (16 lanes at most hold one)
-    s = dpp_add<kQuadXor1>(s);
-    s = dpp_add<kQuadXor2>(s);
-    s = dpp_add<kRowHalfMirror>(s);
-    s = dpp_add<kRowMirror>(s);
-    v[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s), 0));
-  }
+typedef __amdgpu_buffer_rsrc_t Row;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+
+// Row t of the rows of `bytes` bytes at p (raw 32-bit elements, range checked);
+// a row that is not there where p is null.
+__device__ __forceinline__ Row row_at(const void* p, int64_t t, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<char*>(static_cast<const char*>(p) + t * (int64_t)bytes), 0, p ? bytes : 0,
+      0x00020000);
 }
 
-// 8 parameters from p + h, or `none` where there are none
-template <class SP>
-__device__ __forceinline__ void load_param(const void* p, int h, float none, float* v) {
-  if (p) {
-    load8f<SP>(static_cast<const typename SP::T*>(p) + h, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = none;
-  }
+constexpr int kCached = 0, kStreamed = 2;   // cache policy of a load or store: 2 non-temporal
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {   // v_cvt_pk_bf16_f32
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
 }
 
-// Elements of the row that this lane holds: vector j starts at h(j), in the row
-// where h(j) < H.
-template <int kVec>
-struct Slice {
-  int H;
-  __device__ int h(int j) const { return ((int)threadIdx.x + j * (int)blockDim.x) * 8; }
-  __device__ bool in(int j) const { return h(j) < H; }
+// N (4 or 8) consecutive elements as they are in memory, converted when they are
+// used, four at a time: a load in flight is waited for where its values are
+// needed, and the values that stay live are the shorter ones.
+template <class S, int N>
+struct Raw;
+template <int N>
+struct Raw<BF16, N> {
+  uint32_t q[N / 2];
+  template <int kPolicy>
+  __device__ __forceinline__ void load(Row r, uint32_t h) {
+    if constexpr (N == 8) {
+      const u32x4 a = __builtin_amdgcn_raw_buffer_load_b128(r, h * 2, 0, kPolicy);
+      q[0] = a.x; q[1] = a.y; q[2] = a.z; q[3] = a.w;
+    } else {
+      const u32x2 a = __builtin_amdgcn_raw_buffer_load_b64(r, h * 2, 0, kPolicy);
+      q[0] = a.x; q[1] = a.y;
+    }
+  }
+  __device__ __forceinline__ void fill(float f) {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) q[j] = pack2(f, f);
+  }
+  __device__ __forceinline__ void get4(int j, float* v) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[2 * i] = __uint_as_float(q[2 * j + i] << 16);
+      v[2 * i + 1] = __uint_as_float(q[2 * j + i] & 0xffff0000u);
+    }
+  }
+  // The values are converted anew after this, not kept in twice the registers.
+  __device__ __forceinline__ void keep() {
+#pragma unroll
+    for (int j = 0; j < N / 2; ++j) asm volatile("" : "+v"(q[j]));
+  }
+};
+template <int N>
+struct Raw<F32, N> {
+  u32x4 q[N / 4];
+  template <int kPolicy>
+  __device__ __forceinline__ void load(Row r, uint32_t h) {
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j)
+      q[j] = __builtin_amdgcn_raw_buffer_load_b128(r, h * 4 + 16 * j, 0, kPolicy);
+  }
+  __device__ __forceinline__ void fill(float f) {
+#pragma unroll
+    for (int j = 0; j < N / 4; ++j) q[j] = __builtin_bit_cast(u32x4, f32x4{f, f, f, f});
+  }
+  __device__ __forceinline__ void get4(int j, float* v) const {
+    const f32x4 a = __builtin_bit_cast(f32x4, q[j]);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  }
+  __device__ __forceinline__ void keep() {}
 };
 
-// Mean (0 for RMS) and 1 / deviation of the row in v (elements past H are 0).
-template <int kVec>
-__device__ __forceinline__ void row_stats(const float (&v)[kVec][8], const Slice<kVec>& sl,
-                                          const NormSpec& n, int waves, float* buf, int& parity,
-                                          float& mean, float& rstd) {
-  mean = 0.0f;
-  if (n.kind == kNormLayer) {
-    float s[1] = {0.0f};
+template <class S, int N, int kPolicy>
+__device__ __forceinline__ void put(Row r, uint32_t h, const float* v) {
+  if constexpr (S::kBytes == 4) {
 #pragma unroll
-    for (int j = 0; j < kVec; ++j)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[0] += v[j][i];
-    block_sum<1>(s, waves, buf + parity * kMaxWaves);
-    parity ^= 1;
-    mean = s[0] / (float)sl.H;
+    for (int j = 0; j < N / 4; ++j)
+      __builtin_amdgcn_raw_buffer_store_b128(
+          __builtin_bit_cast(u32x4, f32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]}), r,
+          h * 4 + 16 * j, 0, kPolicy);
+  } else if constexpr (N == 8) {
+    __builtin_amdgcn_raw_buffer_store_b128(
+        u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])}, r,
+        h * 2, 0, kPolicy);
+  } else {
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])}, r, h * 2, 0,
+                                          kPolicy);
   }
-  float q[1] = {0.0f};
+}
+
+// What a lane holds of a row: kV vectors of kN elements, a workgroup's lanes
+// apart; vector j starts at h(j).
+template <int kN, int kV>
+struct Slice {
+  static constexpr int N = kN, V = kV;
+  uint32_t H;
+  __device__ __forceinline__ uint32_t h(int j) const {
+    return (threadIdx.x + j * blockDim.x) * N;
+  }
+  __device__ __forceinline__ bool in(int j) const { return h(j) < H; }
+};
+
+// A lane's elements of a row, or of a parameter.
+template <class S, class L>
+struct Part {
+  Raw<S, L::N> q[L::V];
+  template <int kPolicy>
+  __device__ __forceinline__ void load(Row r, const L& sl) {
 #pragma unroll
-  for (int j = 0; j < kVec; ++j)
-    if (sl.in(j)) {
+    for (int j = 0; j < L::V; ++j) q[j].template load<kPolicy>(r, sl.h(j));
+  }
+  // Parameter p, or `none` for each element where there is none.
+  __device__ __forceinline__ void param(const void* p, float none, const L& sl) {
+    load<kCached>(row_at(p, 0, sl.H * S::kBytes), sl);
+    if (!p && none != 0.0f) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float d = v[j][i] - mean;
-        q[0] = fmaf(d, d, q[0]);
-      }
+      for (int j = 0; j < L::V; ++j) q[j].fill(none);
     }
-  block_sum<1>(q, waves, buf + parity * kMaxWaves);
-  parity ^= 1;
-  rstd = 1.0f / sqrtf(q[0] / (float)sl.H + n.eps);
-}
-
-template <class SP, int kVec>
-__device__ __forceinline__ void apply_norm(const float (&v)[kVec][8], const Slice<kVec>& sl,
-                                           const NormSpec& n, float mean, float rstd, int j,
-                                           float* out) {
-  float w[8], b[8];
-  load_param<SP>(n.weight, sl.h(j), 1.0f, w);
-  load_param<SP>(n.bias, sl.h(j), 0.0f, b);
+  }
+  __device__ __forceinline__ void keep() {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) out[i] = fmaf((v[j][i] - mean) * rstd, w[i], b[i]);
+    for (int j = 0; j < L::V; ++j) q[j].keep();
+  }
+};
+
+// f(j, q) for every group of four elements that a lane holds.
+template <class L, class F>
+__device__ __forceinline__ void each4(F f) {
+#pragma unroll
+  for (int j = 0; j < L::V; ++j)
+#pragma unroll
+    for (int q = 0; q < L::N / 4; ++q) f(j, q);
 }
 
-template <class SX, class SO, class SP, int kVec>
-__global__ __launch_bounds__(1024) void norm_kernel(const typename SX::T* x, int64_t T, int H,
-                                                    NormSpec n, typename SO::T* out) {
-  __shared__ float buf[2 * kMaxWaves];
+// Sum over the wavefront, in its last lane.
+__device__ __forceinline__ float wave_sum_last(float v) {
+  v = dpp_add<kQuadXor1>(v);
+  v = dpp_add<kQuadXor2>(v);
+  v = dpp_add<kRowHalfMirror>(v);
+  v = dpp_add<kRowMirror>(v);
+  // row_bcast:15 into rows 1 and 3, row_bcast:31 into rows 2 and 3
+  v += __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));
+  v += __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
+  return v;
+}
+
+// Sums of kN <= 4 values over the workgroup's `waves` wavefronts, in every lane.
+// Each wavefront leaves its sums in buf, one row of 16 per value; every wavefront
+// then adds up the rows, value i's on its lanes 16 i .. 16 i + 15.  Consecutive
+// calls alternate between two buffers (a wavefront may still read the last call's
+// while another is in the next).
+template <int kN>
+__device__ __forceinline__ void block_sum(float (&v)[kN], int waves, float* buf) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = wave_sum_last(v[i]);
+  if (waves == 1) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      v[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v[i]), kWave - 1));
+    return;
+  }
+  if (lane == kWave - 1) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) buf[i * kMaxWaves + threadIdx.x / kWave] = v[i];
+  }
+  __syncthreads();
+  float s = lane < kN * kMaxWaves && lane % kMaxWaves < waves ? buf[lane] : 0.0f;
+  s = dpp_add<kQuadXor1>(s);
+  s = dpp_add<kQuadXor2>(s);
+  s = dpp_add<kRowHalfMirror>(s);
+  s = dpp_add<kRowMirror>(s);
+#pragma unroll
+  for (int i = 0; i < kN; ++i)
+    v[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s), i * kMaxWaves));
+}
+
+// Two buffers of block_sum, taken in turn.
+template <int kN>
+struct SumBuffers {
+  float (*buf)[kN * kMaxWaves];
+  int next;
+  __device__ __forceinline__ float* take() {
+    next ^= 1;
+    return buf[next];
+  }
+};
+
+// 1 / deviation of the row in v, whose elements past the end are 0; for a layer
+// norm the row's mean is taken from it first.
+template <class L>
+__device__ __forceinline__ float center_and_rstd(float (&v)[L::V][L::N], const L& sl, int kind,
+                                                 float eps, float inv_h, int waves,
+                                                 SumBuffers<1>& buf) {
+  if (kind == kNormLayer) {
+    float m[1] = {0.0f};
+#pragma unroll
+    for (int j = 0; j < L::V; ++j)
+#pragma unroll
+      for (int i = 0; i < L::N; ++i) m[0] += v[j][i];
+    block_sum<1>(m, waves, buf.take());
+    const float mean = m[0] * inv_h;
+#pragma unroll
+    for (int j = 0; j < L::V; ++j) {
+      const float c = sl.in(j) ? mean : 0.0f;
+#pragma unroll
+      for (int i = 0; i < L::N; ++i) v[j][i] -= c;
+    }
+  }
+  float s[1] = {0.0f};
+#pragma unroll
+  for (int j = 0; j < L::V; ++j)
+#pragma unroll
+    for (int i = 0; i < L::N; ++i) s[0] = fmaf(v[j][i], v[j][i], s[0]);
+  block_sum<1>(s, waves, buf.take());
+  return rsqrtf(fmaf(s[0], inv_h, eps));
+}
+
+// v = v * rstd * weight + bias, element by element; `bias` as the norm has it.
+template <class SP, class L>
+__device__ __forceinline__ void scale_and_shift(float (&v)[L::V][L::N], const L& sl, float rstd,
+                                                const Part<SP, L>& weight, const void* bias) {
+  if (bias) {
+    Part<SP, L> pb;
+    pb.param(bias, 0.0f, sl);
+    each4<L>([&](int j, int q) {
+      float w[4], b[4];
+      weight.q[j].get4(q, w);
+      pb.q[j].get4(q, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][4 * q + i] = fmaf(v[j][4 * q + i] * rstd, w[i], b[i]);
+    });
+  } else {
+    each4<L>([&](int j, int q) {
+      float w[4];
+      weight.q[j].get4(q, w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[j][4 * q + i] *= rstd * w[i];
+    });
+  }
+}
+
+template <class S, class L>
+__device__ __forceinline__ void put_row(void* p, int64_t t, const L& sl,
+                                        const float (&v)[L::V][L::N]) {
+  const Row r = row_at(p, t, sl.H * S::kBytes);
+#pragma unroll
+  for (int j = 0; j < L::V; ++j) put<S, L::N, kStreamed>(r, sl.h(j), v[j]);
+}
+
+template <class SX, class SO, class SP, class L>
+__global__ __launch_bounds__(1024) void norm_kernel(const void* x, int64_t T, int H, NormSpec n,
+                                                    void* out) {
+  __shared__ float sums[2][kMaxWaves];
+  SumBuffers<1> buf{sums, 0};
   const int waves = blockDim.x / kWave;
-  const Slice<kVec> sl{H};
-  int parity = 0;
+  const L sl{(uint32_t)H};
+  const uint32_t xb = H * SX::kBytes;
+  const float inv_h = 1.0f / (float)H;
+  Part<SX, L> rx;
+  Part<SP, L> pw;
+  rx.template load<kCached>(row_at(x, blockIdx.x, xb), sl);
+  pw.param(n.weight, 1.0f, sl);
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    float v[kVec][8];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-      if (sl.in(j)) load8f<SX>(x + t * H + sl.h(j), v[j]);
-    }
-    float mean, rstd;
-    row_stats<kVec>(v, sl, n, waves, buf, parity, mean, rstd);
-#pragma unroll
-    for (int j = 0; j < kVec; ++j)
-      if (sl.in(j)) {
-        float o[8];
-        apply_norm<SP, kVec>(v, sl, n, mean, rstd, j, o);
-        store8f<SO>(out + t * H + sl.h(j), o);
-      }
+    float v[L::V][L::N];
+    each4<L>([&](int j, int q) { rx.q[j].get4(q, &v[j][4 * q]); });
+    if (t + gridDim.x < T) rx.template load<kCached>(row_at(x, t + gridDim.x, xb), sl);
+    pw.keep();
+    const float rstd = center_and_rstd(v, sl, n.kind, n.eps, inv_h, waves, buf);
+    scale_and_shift<SP>(v, sl, rstd, pw, n.bias);
+    put_row<SO>(out, t, sl, v);
   }
 }
-
-constexpr int kSlots = 4;   // pair rows in flight per lane
 
 // r = x + gate * post(y), n = pre(r).  kCombine: y[t] = sum_k w[t][k] y[t*K + k]
 // (+ shared[t]), in slot order as moe_combine sums it.
-template <class SY, class SS, class SX, class SP, int kVec, bool kCombine>
+template <class SY, class SS, class SX, class SP, class L, bool kCombine>
 __global__ __launch_bounds__(1024) void norm_residual_kernel(
-    const typename SY::T* y, const float* __restrict__ w, int K,
-    const typename SS::T* __restrict__ shared, const typename SX::T* x, int64_t T, int H,
-    NormSpec post, GateSpec gate, typename SX::T* r, NormSpec pre, typename SY::T* n) {
-  __shared__ float buf[2 * kMaxWaves];
+    const void* y, const float* __restrict__ w, int K, const void* shared, const void* x,
+    int64_t T, int H, NormSpec post, GateSpec gate, void* r, NormSpec pre, void* n) {
+  constexpr int N = L::N, V = L::V;
+  __shared__ float sums[2][kMaxWaves];
+  SumBuffers<1> buf{sums, 0};
   const int waves = blockDim.x / kWave;
-  const Slice<kVec> sl{H};
-  int parity = 0;
+  const L sl{(uint32_t)H};
+  const uint32_t xb = H * SX::kBytes, yb = H * SY::kBytes, sb = H * SS::kBytes;
+  const float inv_h = 1.0f / (float)H;
+  Part<SX, L> rx;
+  Part<SY, L> ry;
+  Part<SP, L> pw, qw;
+  if (!kCombine) {
+    rx.template load<kCached>(row_at(x, blockIdx.x, xb), sl);
+    ry.template load<kCached>(row_at(y, blockIdx.x, yb), sl);
+  }
+  pw.param(post.weight, 1.0f, sl);
+  qw.param(pre.weight, 1.0f, sl);
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    float v[kVec][8], xr[kVec][8];
+    float v[V][N];
+    Part<SX, L> cx;
+    if constexpr (kCombine) {
+      // pair rows in flight: 64 bytes a lane
+      constexpr int kSlots = N * V * SY::kBytes <= 16 ? 4 : N * V * SY::kBytes <= 32 ? 2 : 1;
+      Part<SS, L> rs;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
+      for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
-      if (!sl.in(j)) continue;
-      load8f<SX>(x + t * H + sl.h(j), xr[j]);
-      if (!kCombine) load8f<SY>(y + t * H + sl.h(j), v[j]);
-    }
-    if (kCombine) {
+        for (int i = 0; i < N; ++i) v[j][i] = 0.0f;
       for (int k0 = 0; k0 < K; k0 += kSlots) {
+        Part<SY, L> p[kSlots];
         float wk[kSlots];
 #pragma unroll
         for (int k = 0; k < kSlots; ++k) wk[k] = k0 + k < K ? w[t * K + k0 + k] : 0.0f;
+        // (a slot of weight 0: a row of no bytes, which reads zeros)
 #pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-          if (!sl.in(j)) continue;
-          float p[kSlots][8];
+        for (int k = 0; k < kSlots; ++k)
+          p[k].template load<kStreamed>(
+              wk[k] != 0.0f ? row_at(y, t * K + k0 + k, yb) : row_at(nullptr, 0, 0), sl);
 #pragma unroll
-          for (int k = 0; k < kSlots; ++k)
-            if (wk[k] != 0.0f) load8f<SY>(y + (t * K + k0 + k) * H + sl.h(j), p[k]);
+        for (int k = 0; k < kSlots; ++k)
+          each4<L>([&](int j, int q) {
+            float e[4];
+            p[k].q[j].get4(q, e);
 #pragma unroll
-          for (int k = 0; k < kSlots; ++k)
-            if (wk[k] != 0.0f) {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[j][i] = fmaf(wk[k], p[k][i], v[j][i]);
-            }
-        }
+            for (int i = 0; i < 4; ++i) v[j][4 * q + i] = fmaf(wk[k], e[i], v[j][4 * q + i]);
+          });
       }
-      if (shared) {
+      rs.template load<kCached>(row_at(shared, t, sb), sl);
+      cx.template load<kCached>(row_at(x, t, xb), sl);
+      if (shared)
+        each4<L>([&](int j, int q) {
+          float e[4];
+          rs.q[j].get4(q, e);
 #pragma unroll
-        for (int j = 0; j < kVec; ++j)
-          if (sl.in(j)) {
-            float s[8];
-            load8f<SS>(shared + t * H + sl.h(j), s);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[j][i] += s[i];
-          }
+          for (int i = 0; i < 4; ++i) v[j][4 * q + i] += e[i];
+        });
+    } else {
+      cx = rx;
+      each4<L>([&](int j, int q) { ry.q[j].get4(q, &v[j][4 * q]); });
+      if (t + gridDim.x < T) {
+        rx.template load<kCached>(row_at(x, t + gridDim.x, xb), sl);
+        ry.template load<kCached>(row_at(y, t + gridDim.x, yb), sl);
       }
     }
-    float mean = 0.0f, rstd = 1.0f;
-    if (post.kind != kNormNone) row_stats<kVec>(v, sl, post, waves, buf, parity, mean, rstd);
+    pw.keep();
+    qw.keep();
+    const float rstd =
+        post.kind != kNormNone
+            ? center_and_rstd(v, sl, post.kind, post.eps, inv_h, waves, buf)
+            : 1.0f;
     const float a = gate.token ? gate.alpha * gate.token[t] : gate.alpha;
+    if (post.bias || gate.channel) {
+      Part<SP, L> pb, pc;
+      pb.param(post.bias, 0.0f, sl);
+      pc.param(gate.channel, 1.0f, sl);
+      each4<L>([&](int j, int q) {
+        float w4[4], b4[4], c4[4], x4[4];
+        pw.q[j].get4(q, w4);
+        pb.q[j].get4(q, b4);
+        pc.q[j].get4(q, c4);
+        cx.q[j].get4(q, x4);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (!sl.in(j)) continue;
-      float u[8], c[8];
-      if (post.kind != kNormNone) {
-        apply_norm<SP, kVec>(v, sl, post, mean, rstd, j, u);
-      } else {
+        for (int i = 0; i < 4; ++i) {
+          float& e = v[j][4 * q + i];
+          e = fmaf(a * c4[i], fmaf(e * rstd, w4[i], b4[i]), x4[i]);
+        }
+      });
+    } else {
+      const float ar = a * rstd;
+      each4<L>([&](int j, int q) {
+        float w4[4], x4[4];
+        pw.q[j].get4(q, w4);
+        cx.q[j].get4(q, x4);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = v[j][i];
-      }
-      load_param<SP>(gate.channel, sl.h(j), 1.0f, c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = fmaf(a * c[i], u[i], xr[j][i]);
-      store8f<SX>(r + t * H + sl.h(j), v[j]);
+        for (int i = 0; i < 4; ++i) v[j][4 * q + i] = fmaf(v[j][4 * q + i] * ar, w4[i], x4[i]);
+      });
     }
+    put_row<SX>(r, t, sl, v);
     if (n) {
-      row_stats<kVec>(v, sl, pre, waves, buf, parity, mean, rstd);
-#pragma unroll
-      for (int j = 0; j < kVec; ++j)
-        if (sl.in(j)) {
-          float o[8];
-          apply_norm<SP, kVec>(v, sl, pre, mean, rstd, j, o);
-          store8f<SY>(n + t * H + sl.h(j), o);
-        }
+      const float rstd2 = center_and_rstd(v, sl, pre.kind, pre.eps, inv_h, waves, buf);
+      scale_and_shift<SP>(v, sl, rstd2, qw, pre.bias);
+      put_row<SY>(n, t, sl, v);
     }
   }
 }
 
-// With xh the normalised x and g = dn * weight:
-//   dx = rstd (g - [LAYER] mean(g) - xh mean(g xh)) + dres,
-//   dweight = sum_t dn xh, dbias = sum_t dn (partial sums of this workgroup's rows
-//   to part_w, part_b [gridDim.x][H], where given).
-template <class SO, class SX, class SP, int kVec>
+// Gradients of v -> gate * norm(v) and of its parameters, from the gradient e of
+// the result: with a = alpha * token[t], f = channel * weight, xh the normalised
+// row and g = f e,
+//   dv = a rstd (g - [LAYER] mean(g) - xh mean(g xh)) (+ dres),
+//   dtoken[t] = alpha sum_h e channel (xh weight + bias)
+//             = alpha (sum_h g xh + sum_h e channel bias),
+// and down the columns only two sums are needed,
+//   S1 = sum_t a e xh,  S0 = sum_t a e:
+//   dweight = channel S1,  dbias = channel S0,  dchannel = weight S1 + bias S0.
+// Partial sums of this workgroup's rows go to part1, part0 [gridDim.x][H] where
+// given.  One reduction a row (the sums are of the centred row), two for a layer
+// norm.  The norm before a block is the case without gates, with dres.
+template <class SE, class SV, class SP, class L, bool kDres, bool kSum0>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(
-    const typename SO::T* dn, const typename SX::T* x, const typename SX::T* dres, int64_t T,
-    int H, NormSpec n, typename SX::T* dx, float* __restrict__ part_w,
-    float* __restrict__ part_b) {
-  __shared__ float buf[2 * kMaxWaves * 2];
+    const void* e, const void* v, const void* dres, int64_t T, int H, NormSpec n, GateSpec gate,
+    void* dv, float* part1, float* part0, float* __restrict__ dtoken) {
+  constexpr int N = L::N, V = L::V;
+  __shared__ float sums4[2][kMaxWaves * 4];
+  __shared__ float sums1[2][kMaxWaves];
+  SumBuffers<4> buf{sums4, 0};
+  SumBuffers<1> buf1{sums1, 0};
   const int waves = blockDim.x / kWave;
-  const Slice<kVec> sl{H};
-  int parity = 0;
+  const L sl{(uint32_t)H};
+  const uint32_t vb = H * SV::kBytes, eb = H * SE::kBytes;
   const float inv_h = 1.0f / (float)H;
-  float aw[kVec][8], ab[kVec][8];
+  const bool layer = n.kind == kNormLayer;
+  const bool bias_sum = dtoken && n.bias;
+  // (16 elements a lane leave no registers for the next row's)
+  constexpr bool kAhead = N * V <= 8;
+  float s1[V][N], s0[kSum0 ? V : 1][N], f[V][N];
+  Part<SV, L> rv, rr;
+  Part<SE, L> re;
+  auto fetch = [&](int64_t t) {
+    rv.template load<kCached>(row_at(v, t, vb), sl);
+    re.template load<kCached>(row_at(e, t, eb), sl);
+    if (kDres) rr.template load<kCached>(row_at(dres, t, vb), sl);
+  };
+  if (kAhead) fetch(blockIdx.x);
+  {
+    Part<SP, L> pw, pc;
+    pw.param(n.weight, 1.0f, sl);
+    pc.param(gate.channel, 1.0f, sl);
 #pragma unroll
-  for (int j = 0; j < kVec; ++j)
+    for (int j = 0; j < V; ++j)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) aw[j][i] = ab[j][i] = 0.0f;
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    float v[kVec][8], g[kVec][8], d[kVec][8];
+      for (int q = 0; q < N / 4; ++q) {
+        float w[4], c[4];
+        pw.q[j].get4(q, w);
+        pc.q[j].get4(q, c);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = d[j][i] = 0.0f;
-      if (!sl.in(j)) continue;
-      load8f<SX>(x + t * H + sl.h(j), v[j]);
-      load8f<SO>(dn + t * H + sl.h(j), d[j]);
-    }
-    float mean, rstd;
-    row_stats<kVec>(v, sl, n, waves, buf + 2 * kMaxWaves, parity, mean, rstd);
-    float s[2] = {0.0f, 0.0f};
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      float w[8];
-      if (!sl.in(j)) continue;
-      load_param<SP>(n.weight, sl.h(j), 1.0f, w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[j][i] = (v[j][i] - mean) * rstd;
-        g[j][i] = d[j][i] * w[i];
-        s[0] = fmaf(g[j][i], v[j][i], s[0]);
-        s[1] += g[j][i];
-        aw[j][i] = fmaf(d[j][i], v[j][i], aw[j][i]);
-        ab[j][i] += d[j][i];
+        for (int i = 0; i < 4; ++i) {
+          f[j][4 * q + i] = w[i] * c[i];
+          s1[j][4 * q + i] = 0.0f;
+          if (kSum0) s0[j][4 * q + i] = 0.0f;
+        }
       }
-    }
-    block_sum<2>(s, waves, buf);
-    const float mgx = s[0] * inv_h, mg = n.kind == kNormLayer ? s[1] * inv_h : 0.0f;
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (!sl.in(j)) continue;
-      float o[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = rstd * (g[j][i] - mg - v[j][i] * mgx);
-      if (dres) {
-        float e[8];
-        load8f<SX>(dres + t * H + sl.h(j), e);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] += e[i];
-      }
-      store8f<SX>(dx + t * H + sl.h(j), o);
-    }
   }
-#pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    if (!sl.in(j)) continue;
-    if (part_w) store8f<F32>(part_w + (int64_t)blockIdx.x * H + sl.h(j), aw[j]);
-    if (part_b) store8f<F32>(part_b + (int64_t)blockIdx.x * H + sl.h(j), ab[j]);
-  }
-}
-
-// From dr: with u = post(y), a = alpha * token[t] and du = a * channel * dr:
-//   dy from du as above (du itself without a norm), dweight, dbias likewise,
-//   dchannel = sum_t a dr u,   dtoken[t] = sum_h alpha channel dr u.
-template <class SX, class SY, class SP, int kVec>
-__global__ __launch_bounds__(1024) void norm_residual_backward_kernel(
-    const typename SX::T* dr, const typename SY::T* y, int64_t T, int H, NormSpec n,
-    GateSpec gate, typename SY::T* dy, float* __restrict__ part_w, float* __restrict__ part_b,
-    float* __restrict__ part_c, float* __restrict__ dtoken) {
-  __shared__ float buf[2 * kMaxWaves + kMaxWaves * 3];
-  const int waves = blockDim.x / kWave;
-  const Slice<kVec> sl{H};
-  int parity = 0;
-  const float inv_h = 1.0f / (float)H;
-  float aw[kVec][8], ab[kVec][8], ac[kVec][8];
-#pragma unroll
-  for (int j = 0; j < kVec; ++j)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) aw[j][i] = ab[j][i] = ac[j][i] = 0.0f;
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    float v[kVec][8], g[kVec][8];
-#pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[j][i] = g[j][i] = 0.0f;
-      if (!sl.in(j)) continue;
-      load8f<SY>(y + t * H + sl.h(j), v[j]);
-      load8f<SX>(dr + t * H + sl.h(j), g[j]);
-    }
-    float mean = 0.0f, rstd = 1.0f;
-    if (n.kind != kNormNone)
-      row_stats<kVec>(v, sl, n, waves, buf + 3 * kMaxWaves, parity, mean, rstd);
+    if (!kAhead) fetch(t);
+    Part<SV, L> cv = rv, cr = rr;
+    Part<SE, L> ce = re;
+    if (kAhead && t + gridDim.x < T) fetch(t + gridDim.x);
     const float a = gate.token ? gate.alpha * gate.token[t] : gate.alpha;
-    // over the row: sums of g xh and g (without the factor a) and of channel dr u
-    float s[3] = {0.0f, 0.0f, 0.0f};
+    float mean = 0.0f;
+    if (layer) {
+      float m[1] = {0.0f};
+      each4<L>([&](int j, int q) {
+        float x[4];
+        cv.q[j].get4(q, x);
+        m[0] += (x[0] + x[1]) + (x[2] + x[3]);
+      });
+      cv.keep();
+      block_sum<1>(m, waves, buf1.take());
+      mean = m[0] * inv_h;
+    }
+    // of the centred squares, g times the centred row, g, and e channel bias
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    each4<L>([&](int j, int q) {
+      float x[4], d[4];
+      cv.q[j].get4(q, x);
+      ce.q[j].get4(q, d);
+      if (layer) {
+        const float c = sl.in(j) ? mean : 0.0f;
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (!sl.in(j)) continue;
-      float w[8], b[8], c[8];
-      load_param<SP>(n.weight, sl.h(j), 1.0f, w);
-      load_param<SP>(n.bias, sl.h(j), 0.0f, b);
-      load_param<SP>(gate.channel, sl.h(j), 1.0f, c);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float xh = (v[j][i] - mean) * rstd;
-        const float u = fmaf(xh, w[i], b[i]);
-        const float e = g[j][i];
-        const float ce = c[i] * e;
-        ac[j][i] = fmaf(a * e, u, ac[j][i]);
-        aw[j][i] = fmaf(a * ce, xh, aw[j][i]);
-        ab[j][i] = fmaf(a, ce, ab[j][i]);
-        const float gw = ce * w[i];
-        s[0] = fmaf(gw, xh, s[0]);
-        s[1] += gw;
-        s[2] = fmaf(ce, u, s[2]);
-        v[j][i] = xh;
-        g[j][i] = gw;
+        for (int i = 0; i < 4; ++i) {
+          x[i] -= c;
+          s[2] = fmaf(d[i], f[j][4 * q + i], s[2]);
+        }
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[0] = fmaf(x[i], x[i], s[0]);
+        s[1] = fmaf(d[i] * f[j][4 * q + i], x[i], s[1]);
+      }
+    });
+    if (bias_sum) {
+      Part<SP, L> pb, pc;
+      pb.param(n.bias, 0.0f, sl);
+      pc.param(gate.channel, 1.0f, sl);
+      each4<L>([&](int j, int q) {
+        float b[4], c[4], d[4];
+        pb.q[j].get4(q, b);
+        pc.q[j].get4(q, c);
+        ce.q[j].get4(q, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[3] = fmaf(d[i], c[i] * b[i], s[3]);
+      });
     }
-    block_sum<3>(s, waves, buf);
-    if (dtoken && threadIdx.x == 0) dtoken[t] = gate.alpha * s[2];
-    const float mgx = n.kind != kNormNone ? s[0] * inv_h : 0.0f;
-    const float mg = n.kind == kNormLayer ? s[1] * inv_h : 0.0f;
+    cv.keep();
+    ce.keep();
+    block_sum<4>(s, waves, buf.take());
+    const float rstd = n.kind != kNormNone ? rsqrtf(fmaf(s[0], inv_h, n.eps)) : 1.0f;
+    if (dtoken && threadIdx.x == 0) dtoken[t] = gate.alpha * fmaf(s[1], rstd, s[3]);
+    // dv = (ar e) f - ag - (x - mean) agx
     const float ar = a * rstd;
+    const float agx = n.kind != kNormNone ? ar * rstd * rstd * (s[1] * inv_h) : 0.0f;
+    const float ag = layer ? ar * (s[2] * inv_h) : 0.0f;
+    const Row out = row_at(dv, t, vb);
 #pragma unroll
-    for (int j = 0; j < kVec; ++j) {
-      if (!sl.in(j)) continue;
-      float o[8];
+    for (int j = 0; j < V; ++j) {
+      float o[N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = ar * (g[j][i] - mg - v[j][i] * mgx);
-      store8f<SY>(dy + t * H + sl.h(j), o);
+      for (int q = 0; q < N / 4; ++q) {
+        float x[4], d[4];
+        cv.q[j].get4(q, x);
+        ce.q[j].get4(q, d);
+        float* oq = o + 4 * q;
+        if (kDres) {
+          cr.q[j].get4(q, oq);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) oq[i] = 0.0f;
+        }
+        if (layer) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] -= mean;
+            oq[i] -= ag;
+          }
+        }
+        if (kSum0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s0[j][4 * q + i] = fmaf(a, d[i], s0[j][4 * q + i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = 4 * q + i;
+          const float er = ar * d[i];
+          s1[j][k] = fmaf(er, x[i], s1[j][k]);
+          oq[i] = fmaf(er, f[j][k], fmaf(-agx, x[i], oq[i]));
+        }
+      }
+      put<SV, N, kStreamed>(out, sl.h(j), o);
     }
-    __syncthreads();   // buf is written again by the next row's sums
   }
+  const Row r1 = row_at(part1, blockIdx.x, H * 4), r0 = row_at(part0, blockIdx.x, H * 4);
 #pragma unroll
-  for (int j = 0; j < kVec; ++j) {
-    if (!sl.in(j)) continue;
-    const int64_t o = (int64_t)blockIdx.x * H + sl.h(j);
-    if (part_w) store8f<F32>(part_w + o, aw[j]);
-    if (part_b) store8f<F32>(part_b + o, ab[j]);
-    if (part_c) store8f<F32>(part_c + o, ac[j]);
+  for (int j = 0; j < V; ++j) {
+    put<F32, N, kCached>(r1, sl.h(j), s1[j]);
+    if (kSum0) put<F32, N, kCached>(r0, sl.h(j), s0[j]);
   }
 }
 
-// out[i][h] = sum over g < G, in order, of part[i][g][h]; zeros for G = 0.
-// 16 lanes hold 64 columns, 16 groups of them G / 16 rows each.
-struct ColumnSums {
-  const float* part[3];
-  float* out[3];
+// The parameters' gradients from the partial sums [G][H] of S1 and S0 (null: not
+// asked for), added in a fixed order; zeros for G = 0.  A workgroup takes 32
+// columns: 8 lanes of 4 columns, 32 groups of lanes with every 32nd row each, then
+// the groups in order.
+struct ParamGrads {
+  const float *part1, *part0;
+  const void *weight, *bias, *channel;
+  float *dweight, *dbias, *dchannel;
 };
-__global__ __launch_bounds__(256) void column_sum_kernel(ColumnSums c, int G, int H) {
-  __shared__ f32x4 buf[16][16];
-  const int lane = threadIdx.x & 15, grp = threadIdx.x >> 4;
-  const int h = blockIdx.x * 64 + lane * 4;
-  const float* part = c.part[blockIdx.y];
-  float* out = c.out[blockIdx.y];
-  const int per = (G + 15) / 16;
-  f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (h < H)
-    for (int g = grp * per; g < G && g < (grp + 1) * per; ++g)
-      s += *reinterpret_cast<const f32x4*>(part + (int64_t)g * H + h);
-  buf[grp][lane] = s;
+constexpr int kSumLanes = 8, kSumGroups = 32;
+template <class SP>
+__global__ __launch_bounds__(kSumLanes* kSumGroups) void param_grads_kernel(ParamGrads p, int G,
+                                                                            int H) {
+  __shared__ f32x4 buf[2][kSumGroups][kSumLanes];
+  const int lane = threadIdx.x % kSumLanes, grp = threadIdx.x / kSumLanes;
+  const int h = (blockIdx.x * kSumLanes + lane) * 4;
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  f32x4 s1 = zero, s0 = zero;
+  auto param = [&](const void* q, float none, float* o) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = none;
+    if (q && h < H) {
+      Raw<SP, 4> r;
+      r.template load<kCached>(row_at(q, 0, H * SP::kBytes), h);
+      r.get4(0, o);
+    }
+  };
+  float w[4], b[4], c[4];
+  param(p.weight, 1.0f, w);
+  param(p.bias, 0.0f, b);
+  param(p.channel, 1.0f, c);
+  if (h < H) {
+    if (p.part1) {
+#pragma unroll 8
+      for (int g = grp; g < G; g += kSumGroups)
+        s1 += *reinterpret_cast<const f32x4*>(p.part1 + (int64_t)g * H + h);
+    }
+    if (p.part0) {
+#pragma unroll 8
+      for (int g = grp; g < G; g += kSumGroups)
+        s0 += *reinterpret_cast<const f32x4*>(p.part0 + (int64_t)g * H + h);
+    }
+  }
+  buf[0][grp][lane] = s1;
+  buf[1][grp][lane] = s0;
   __syncthreads();
-  if (grp == 0 && h < H) {
-    f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int g = 0; g < 16; ++g) o += buf[g][lane];
-    *reinterpret_cast<f32x4*>(out + h) = o;
+  if (grp != 0 || h >= H) return;
+  s1 = s0 = zero;
+#pragma unroll 4
+  for (int g = 0; g < kSumGroups; ++g) {
+    s1 += buf[0][g][lane];
+    s0 += buf[1][g][lane];
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (p.dweight) p.dweight[h + i] = c[i] * s1[i];
+    if (p.dbias) p.dbias[h + i] = c[i] * s0[i];
+    if (p.dchannel) p.dchannel[h + i] = fmaf(b[i], s0[i], w[i] * s1[i]);
   }
 }
 
 namespace {
 
-struct Launch {
-  int vec, threads;
-};
+// Lanes of a workgroup that hold `elements` of a row each.
+int threads_for(int H, int elements) {
+  return ((H + elements - 1) / elements + kWave - 1) / kWave * kWave;
+}
 
-// Vectors of 8 elements a lane holds (1 up to 8192 elements, where 1024 lanes
-// cover the row) and the lanes.
-Launch launch_for(int H, int vec) {
-  const int nv = H / 8;
-  if (nv > kMaxWaves * kWave) vec = 2;
-  const int lanes = (nv + vec - 1) / vec;
-  return {vec, (lanes + kWave - 1) / kWave * kWave};
+// Elements of a lane: 8 while 1024 lanes cover the row, else 16.
+int lane_elements(int H) { return H > 8 * kMaxWaves * kWave ? 16 : 8; }
+
+// Workgroups of a forward launch: 32 wavefronts a CU, each looping over its rows.
+unsigned forward_groups(int64_t T, int threads) {
+  const int waves = threads / kWave;
+  const int64_t most = 256 * (32 / waves);
+  return (unsigned)(T < most ? T : most);
 }
 
 // Workgroups of a backward launch: each writes a row of partial sums per
-// parameter, so it takes 16 rows or more once there are 256 of them.
+// parameter, so it takes 8 rows or more once there are 256 of them, and no more
+// than two a CU, or 16 wavefronts of them.
 int backward_groups(int64_t T, int H) {
-  const int waves = launch_for(H, 2).threads / kWave;
-  int64_t g = T / 16;
-  const int64_t most = 256 * (waves < 16 ? 16 / waves : 1);
+  const int waves = threads_for(H, lane_elements(H)) / kWave;
+  const int64_t most = lane_elements(H) > 8 ? 256 : 256 * (waves < 8 ? 16 / waves : 2);
+  int64_t g = T / 8;
   if (g > most) g = most;
   if (g < 256) g = 256;
   return (int)(g < T ? g : T);
 }
 
-unsigned rows_grid(int64_t T) { return (unsigned)(T < (1 << 20) ? T : (1 << 20)); }
-
+// f(a, b, c, layout): the types and how a lane's `elements` lie -- vectors of 16
+// bytes of the wider of the row types, a and b.
 template <class F>
-hipError_t with_types(int a, int b, int c, F f) {
+hipError_t with_types(int a, int b, int c, int elements, F f) {
+  auto layout = [&](auto sa, auto sb, auto sc) {
+    constexpr int N = decltype(sa)::kBytes == 2 && decltype(sb)::kBytes == 2 ? 8 : 4;
+    if (elements == 8) f(sa, sb, sc, Slice<N, 8 / N>());
+    else f(sa, sb, sc, Slice<N, 16 / N>());
+  };
   auto third = [&](auto sa, auto sb) {
-    if (c == kDtF32) f(sa, sb, F32());
-    else f(sa, sb, BF16());
+    if (c == kDtF32) layout(sa, sb, F32());
+    else layout(sa, sb, BF16());
   };
   auto second = [&](auto sa) {
     if (b == kDtF32) third(sa, F32());
@@ -443,67 +689,36 @@ hipError_t with_types(int a, int b, int c, F f) {
   return hipGetLastError();
 }
 
-hipError_t column_sums(const ColumnSums& c, int n, int G, int H, hipStream_t s) {
-  if (n == 0) return hipSuccess;
-  hipLaunchKernelGGL(column_sum_kernel, dim3((H + 63) / 64, n), dim3(256), 0, s, c, G, H);
-  return hipGetLastError();
-}
-
-// The partial sums of the gradients asked for (out[i] not null), in `workspace`.
-struct Partials {
-  ColumnSums sums;
-  int n;
-  float* part[3];
-  Partials(float* const* out, int count, float* workspace, int G, int H) : n(0) {
-    for (int i = 0; i < count; ++i) {
-      part[i] = out[i] ? workspace + (int64_t)n * G * H : nullptr;
-      if (out[i]) {
-        sums.part[n] = part[i];
-        sums.out[n++] = out[i];
-      }
-    }
-  }
-};
-
 }  // namespace
 
 int64_t norm_workspace_floats(int64_t T, int H) {
-  return 3 * (int64_t)backward_groups(T, H) * H;
+  return 2 * (int64_t)backward_groups(T, H) * H;
 }
 
 hipError_t launch_norm(const void* x, int xdt, int64_t T, int H, const NormSpec& n, int pdt,
                        void* out, int odt, hipStream_t s) {
-  const Launch l = launch_for(H, 1);
-  return with_types(xdt, odt, pdt, [&](auto sx, auto so, auto sp) {
-    typedef decltype(sx) SX;
-    typedef decltype(so) SO;
-    typedef decltype(sp) SP;
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3(rows_grid(T)), dim3(l.threads), 0, s,
-                         static_cast<const typename SX::T*>(x), T, H, n,
-                         static_cast<typename SO::T*>(out));
-    };
-    if (l.vec == 1) go(norm_kernel<SX, SO, SP, 1>);
-    else go(norm_kernel<SX, SO, SP, 2>);
+  const int e = lane_elements(H), threads = threads_for(H, e);
+  return with_types(xdt, odt, pdt, e, [&](auto sx, auto so, auto sp, auto layout) {
+    hipLaunchKernelGGL(
+        (norm_kernel<decltype(sx), decltype(so), decltype(sp), decltype(layout)>),
+        dim3(forward_groups(T, threads)), dim3(threads), 0, s, x, T, H, n, out);
   });
 }
 
 hipError_t launch_norm_residual(const void* y, int ydt, const void* x, int xdt, int64_t T, int H,
                                 const NormSpec& post, const GateSpec& gate, int pdt, void* r,
                                 const NormSpec& pre, void* n, hipStream_t s) {
-  const Launch l = launch_for(H, 1);
-  return with_types(ydt, xdt, pdt, [&](auto sy, auto sx, auto sp) {
+  // bf16 rows of more than 4096 on half the lanes: two workgroups fit a CU (7168 of
+  // them: 14 wavefronts of 65 registers do not share one, 7 of 110 do; 8192 rows
+  // 96.6 -> 85.2 us, one row 3.38 -> 3.25)
+  const int e = ydt == kDtBF16 && xdt == kDtBF16 && H > 4096 ? 16 : lane_elements(H);
+  const int threads = threads_for(H, e);
+  return with_types(ydt, xdt, pdt, e, [&](auto sy, auto sx, auto sp, auto layout) {
     typedef decltype(sy) SY;
-    typedef decltype(sx) SX;
-    typedef decltype(sp) SP;
-    auto go = [&](auto kernel) {
-      hipLaunchKernelGGL(kernel, dim3(rows_grid(T)), dim3(l.threads), 0, s,
-                         static_cast<const typename SY::T*>(y), nullptr, 0, nullptr,
-                         static_cast<const typename SX::T*>(x), T, H, post, gate,
-                         static_cast<typename SX::T*>(r), pre, static_cast<typename SY::T*>(n));
-    };
-    if (l.vec == 1) go(norm_residual_kernel<SY, SY, SX, SP, 1, false>);
-    else go(norm_residual_kernel<SY, SY, SX, SP, 2, false>);
+    hipLaunchKernelGGL(
+        (norm_residual_kernel<SY, SY, decltype(sx), decltype(sp), decltype(layout), false>),
+        dim3(forward_groups(T, threads)), dim3(threads), 0, s, y, nullptr, 0, nullptr, x, T, H,
+        post, gate, r, pre, n);
   });
 }
 
@@ -512,74 +727,52 @@ hipError_t launch_combine_norm_residual(const void* y, int ydt, const float* w, 
                                         int64_t T, int H, const NormSpec& post,
                                         const GateSpec& gate, int pdt, void* r,
                                         const NormSpec& pre, void* n, hipStream_t s) {
-  const Launch l = launch_for(H, 1);
-  return with_types(ydt, xdt, pdt, [&](auto sy, auto sx, auto sp) {
-    typedef decltype(sy) SY;
-    typedef decltype(sx) SX;
-    typedef decltype(sp) SP;
-    auto shared_type = [&](auto ss) {
-      typedef decltype(ss) SS;
-      auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(rows_grid(T)), dim3(l.threads), 0, s,
-                           static_cast<const typename SY::T*>(y), w, K,
-                           static_cast<const typename SS::T*>(shared),
-                           static_cast<const typename SX::T*>(x), T, H, post, gate,
-                           static_cast<typename SX::T*>(r), pre, static_cast<typename SY::T*>(n));
-      };
-      if (l.vec == 1) go(norm_residual_kernel<SY, SS, SX, SP, 1, true>);
-      else go(norm_residual_kernel<SY, SS, SX, SP, 2, true>);
+  const int e = lane_elements(H), threads = threads_for(H, e);
+  return with_types(ydt, xdt, pdt, e, [&](auto sy, auto sx, auto sp, auto layout) {
+    auto go = [&](auto ss) {
+      hipLaunchKernelGGL((norm_residual_kernel<decltype(sy), decltype(ss), decltype(sx),
+                                               decltype(sp), decltype(layout), true>),
+                         dim3(forward_groups(T, threads)), dim3(threads), 0, s, y, w, K, shared,
+                         x, T, H, post, gate, r, pre, n);
     };
-    if (sdt == kDtF32) shared_type(F32());
-    else shared_type(BF16());
+    if (sdt == kDtF32) go(F32());
+    else go(BF16());
   });
 }
 
-hipError_t launch_norm_backward(const void* dn, int odt, const void* x, int xdt, const void* dres,
-                                int64_t T, int H, const NormSpec& n, int pdt, void* dx,
-                                float* dweight, float* dbias, float* workspace, hipStream_t s) {
-  const Launch l = launch_for(H, 2);
+hipError_t launch_norm_backward(const void* e, int edt, const void* v, int vdt, const void* dres,
+                                int64_t T, int H, const NormSpec& n, const GateSpec& gate, int pdt,
+                                void* dv, float* dweight, float* dbias, float* dchannel,
+                                float* dtoken, float* workspace, hipStream_t s) {
   const int G = backward_groups(T, H);
-  float* const out[2] = {dweight, dbias};
-  const Partials p(out, 2, workspace, G, H);
+  const int elements = lane_elements(H);
+  ParamGrads p{nullptr, nullptr, n.weight, n.bias, gate.channel, dweight, dbias, dchannel};
+  float* part1 = dweight || dchannel ? workspace : nullptr;
+  float* part0 = dbias || (dchannel && n.bias) ? workspace + (int64_t)G * H : nullptr;
+  p.part1 = part1;
+  p.part0 = part0;
   if (T > 0) {
-    const hipError_t e = with_types(odt, xdt, pdt, [&](auto so, auto sx, auto sp) {
-      typedef decltype(so) SO;
-      typedef decltype(sx) SX;
+    const hipError_t st = with_types(edt, vdt, pdt, elements, [&](auto se, auto sv, auto sp, auto layout) {
+      auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(G), dim3(threads_for(H, elements)), 0, s, e, v, dres, T, H, n, gate,
+                           dv, part1, part0, dtoken);
+      };
+      typedef decltype(se) SE;
+      typedef decltype(sv) SV;
       typedef decltype(sp) SP;
-      hipLaunchKernelGGL((norm_backward_kernel<SO, SX, SP, 2>), dim3(G), dim3(l.threads), 0, s,
-                         static_cast<const typename SO::T*>(dn),
-                         static_cast<const typename SX::T*>(x),
-                         static_cast<const typename SX::T*>(dres), T, H, n,
-                         static_cast<typename SX::T*>(dx), p.part[0], p.part[1]);
+      typedef decltype(layout) L;
+      if (dres && part0) go(norm_backward_kernel<SE, SV, SP, L, true, true>);
+      else if (dres) go(norm_backward_kernel<SE, SV, SP, L, true, false>);
+      else if (part0) go(norm_backward_kernel<SE, SV, SP, L, false, true>);
+      else go(norm_backward_kernel<SE, SV, SP, L, false, false>);
     });
-    if (e != hipSuccess) return e;
+    if (st != hipSuccess) return st;
   }
-  return column_sums(p.sums, p.n, G, H, s);
-}
-
-hipError_t launch_norm_residual_backward(const void* dr, int xdt, const void* y, int ydt,
-                                         int64_t T, int H, const NormSpec& post,
-                                         const GateSpec& gate, int pdt, void* dy, float* dweight,
-                                         float* dbias, float* dchannel, float* dtoken,
-                                         float* workspace, hipStream_t s) {
-  const Launch l = launch_for(H, 2);
-  const int G = backward_groups(T, H);
-  float* const out[3] = {dweight, dbias, dchannel};
-  const Partials p(out, 3, workspace, G, H);
-  if (T > 0) {
-    const hipError_t e = with_types(xdt, ydt, pdt, [&](auto sx, auto sy, auto sp) {
-      typedef decltype(sx) SX;
-      typedef decltype(sy) SY;
-      typedef decltype(sp) SP;
-      hipLaunchKernelGGL((norm_residual_backward_kernel<SX, SY, SP, 2>), dim3(G),
-                         dim3(l.threads), 0, s, static_cast<const typename SX::T*>(dr),
-                         static_cast<const typename SY::T*>(y), T, H, post, gate,
-                         static_cast<typename SY::T*>(dy), p.part[0], p.part[1], p.part[2],
-                         dtoken);
-    });
-    if (e != hipSuccess) return e;
-  }
-  return column_sums(p.sums, p.n, G, H, s);
+  if (!dweight && !dbias && !dchannel) return hipSuccess;
+  const dim3 grid((H + 4 * kSumLanes - 1) / (4 * kSumLanes)), block(kSumLanes * kSumGroups);
+  if (pdt == kDtF32) hipLaunchKernelGGL(param_grads_kernel<F32>, grid, block, 0, s, p, G, H);
+  else hipLaunchKernelGGL(param_grads_kernel<BF16>, grid, block, 0, s, p, G, H);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -494,14 +494,19 @@ def test_combine_norm_residual(T, H, ydt, xdt, pdt, kind, channel, token, alpha,
     r = torch.full((T, H), float("nan"), dtype=DT[xdt], device=DEV)
     n = torch.full((T, H), float("nan"), dtype=DT[ydt], device=DEV) if pre else None
     B.moe_combine_norm_residual(y, w, x, post, gate, r, pre=pre, n=n, shared=sh)
-    # the combine in fp32, then the norm and residual sum from it: the fp32 rows are the
-    # same, so the results are, where y's type has no part in them
+    # the combine in fp32 (the same sums bit for bit), then the norm and residual sum from it
     c = torch.empty(T, H, device=DEV)
     B.moe_combine(y, w, c, shared=sh)
-    check_residual(r, n, reference(c, post), x, gate, pre, T)
+    ref = reference(c, post)
+    check_residual(r, n, ref, x, gate, pre, T)
+    # the two calls one after the other, to the same bound: the statistics are sums over the
+    # row in an order that goes by the types (a lane holds 8 neighbours of bf16 rows, 4 of
+    # fp32 ones), so the bits agree only where y is fp32 in both
     r2 = torch.empty_like(r)
     B.moe_norm_residual(c, x, post, gate, r2)
-    assert torch.equal(r, r2)
+    check_residual(r2, None, ref, x, gate, None, T)
+    if ydt == "f32":
+        assert torch.equal(r, r2)
 
 
 @pytest.mark.parametrize("T,H,ydt,xdt,pdt,kind,channel,token,alpha,pre_kind", RESIDUALS)
@@ -804,10 +809,4 @@ def test_block_pass(T, shared, stream_dtype):
         layer.forward()   # the layer's own pass on the tokens and logits the block left
         c = torch.empty(T, H, device=DEV)
         B.moe_combine(layer.y_pairs, layer.topk_w, c, layer.shared_out if layer.has_shared else None)
-        want = torch.empty(T, H, dtype=stream_dtype, device=DEV)
-        B.moe_norm_residual(c, xin, post, gt, want)
-        assert torch.equal(r, want)
-        if nxt is not None:
-            ref = torch.empty(T, H, device=DEV)
-            B.moe_norm_residual(c, xin, post, gt, want, pre=nxt, n=ref)
-            assert torch.equal(n, ref.to(n.dtype))
+        check_residual(r, n, reference(c, post), xin, gt, nxt, T)

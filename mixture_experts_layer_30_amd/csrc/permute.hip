@@ -338,13 +338,15 @@ int64_t groups_of(int64_t units, int lanes) {
   return (units + per - 1) / per;
 }
 
-// Up to kPadWorkgroups workgroups for an expert's padding: block-wise padding
-// leaves at most block_m - 1 rows.
-constexpr int kPadWorkgroups = 16;
-
-Padding padding_of(const RowMap& rm) {
-  const int most = rm.block_m - 1;
-  return Padding{rm.counts, rm.offsets, most < kPadWorkgroups ? most : kPadWorkgroups};
+// Workgroups for an expert's padding, 8 stores a lane each if every row that the
+// plan has room for beyond its pairs were padding: up to 16 (1024 in all where
+// there are few experts, whose max-padded slots may be long).  Block-wise padding
+// leaves at most block_m - 1 rows an expert, max padding any number.
+Padding padding_of(const RowMap& rm, int E, int64_t cap, int64_t pairs, int nv) {
+  const int64_t rows = (cap - pairs + E - 1) / E;
+  const int64_t want = (rows * nv + 8 * kThreads - 1) / (8 * kThreads);
+  const int64_t most = 1024 / E > 16 ? 1024 / E : 16;
+  return Padding{rm.counts, rm.offsets, (int)(want < 1 ? 1 : want < most ? want : most)};
 }
 
 template <class SR, class SS, class SO>
@@ -378,8 +380,8 @@ hipError_t unpermute_backward_t(const void* dout, const void* rows, const float*
                                 int K, int H, const RowMap& rm, int E, int64_t cap, void* drows,
                                 float* dw, hipStream_t s) {
   const int nv = H / Vec<S>::N;
-  const Padding pad = padding_of(rm);
-  const int64_t pads = drows ? E * pad.subs : 0;   // (blocks of one row leave none)
+  const Padding pad = padding_of(rm, E, cap, T * K, nv);
+  const int64_t pads = drows ? E * pad.subs : 0;
   return with_lanes(nv, [&](auto lanes) {
     constexpr int kLanes = decltype(lanes)::value;
     const int64_t groups = groups_of(T * K, kLanes);
@@ -396,8 +398,8 @@ hipError_t unpermute_backward_t(const void* dout, const void* rows, const float*
 hipError_t launch_permute(const void* x, int dt, int64_t T, int K, int H, const RowMap& rm, int E,
                           int64_t cap, void* rows, hipStream_t s) {
   const int nv = dt == kDtF32 ? H / 4 : H / 8;
-  const Padding pad = padding_of(rm);
-  const int64_t pads = E * pad.subs;   // (blocks of one row leave none)
+  const Padding pad = padding_of(rm, E, cap, T * K, nv);
+  const int64_t pads = E * pad.subs;
   return with_lanes(nv, [&](auto lanes) {
     constexpr int kLanes = decltype(lanes)::value;
     const int chunks = (nv + kLanes - 1) / kLanes;

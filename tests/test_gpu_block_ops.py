@@ -85,6 +85,8 @@ SORTED = [
     (257, 3584, 64, 8, 1, B.PAD_BLOCK, "f32", True, False),
     (300, 1032, 256, 13, 1000, B.PAD_BLOCK, "bf16", False, False),
     (33, 16392, 5, 3, 16, B.PAD_MAX, "bf16", True, False),
+    (70, 136, 9, 2, 1, B.PAD_MAX, "bf16", False, False),     # blocks of one row, and padding all the same
+    (900, 1024, 4, 1, 128, B.PAD_MAX, "f32", False, True),   # one expert's rows, three slots of padding
 ]
 
 
@@ -374,6 +376,9 @@ def test_norm(T, H, xdt, odt, pdt, weight, bias, kind):
     B.moe_norm(x, n, o)
     ref = reference(x, n)
     close(o, ref.out, ref.e_out)
+    if xdt == odt:   # in place
+        B.moe_norm(x, n, x)
+        assert torch.equal(x, o)
 
 
 @pytest.mark.parametrize("kind", [B.NORM_RMS, B.NORM_LAYER])
@@ -595,6 +600,19 @@ def test_values_that_are_not_finite_stay_in_their_row():
     keep = [0, 1, 3, 5]
     assert torch.equal(r[keep], r2[keep]) and torch.equal(o[keep], o2[keep])
     assert torch.isnan(r2[2]).all() and torch.isnan(r2[4, 0])
+
+
+def test_a_missing_norm_or_gate_is_refused():
+    x = torch.zeros(2, 64, device=DEV)
+    for f in (lambda: B.moe_norm(x, None, x), lambda: B.moe_norm_backward(x, x, None, x),
+              lambda: B.moe_norm_residual(x, x, None, B.Gate(), x),
+              lambda: B.moe_norm_residual(x, x, B.Norm(), None, x),
+              lambda: B.moe_norm(x, B.Norm(), torch.zeros(2, 64)),
+              lambda: B.moe_norm(x, B.Norm(weight=torch.ones(64)), x)):
+        with pytest.raises(B.MoEError) as e:
+            f()
+        assert e.value.status == B.MOE_EINVAL
+    assert (x == 0).all()
 
 
 def test_empty_batches():

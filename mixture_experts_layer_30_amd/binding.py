@@ -149,7 +149,7 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         # the current stream's handle alone: building torch's Stream object around it
-        # takes 2.5 us of a call's 9 (MI355X, one token's norm: 9.2 -> 6.4 us a call)
+        # takes 2.5 us (measured on MI355X: one token's norm 9.2 -> 7.2 us a call)
         return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return ctypes.c_void_p(stream.cuda_stream)
 
@@ -336,24 +336,41 @@ def _shaped(t, shape, what, dtype=None):
         _refuse(f"{what} must be contiguous")
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _call(fn, device, stream, *args):
-    """fn(*args, stream) with the tensors' GPU current: on `stream`, or that GPU's current one."""
-    if device.type != "cuda":
-        _refuse(f"tensors must be on a GPU, got {device}")
-    if stream is not None and stream.device != device:
-        _refuse(f"a stream of {stream.device} for tensors on {device}")
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream(stream)))
+    """fn(*args, stream) with GPU `device` (an index) current: on `stream`, or that GPU's
+    current one."""
+    if device < 0:
+        _refuse("tensors must be on a GPU")
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(device)   # (see _stream)
+    elif stream.device.index != device:
+        _refuse(f"a stream of {stream.device} for tensors on GPU {device}")
+    else:
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        status = fn(*args, stream)
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream(stream)))
+            status = fn(*args, stream)
+    if status != MOE_OK:
+        _check(status)
 
 
 def _one_device(first, *rest):
+    """The index of the GPU that holds every tensor given; -1: none does."""
+    dev = first.get_device()
     for t in rest:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             _refuse(f"tensors on {first.device} and {t.device}")
-    return first.device
+    return dev
+
+
+def _ref(o):
+    return None if o is None else ctypes.byref(o.c)
 
 
 class Norm:
@@ -365,10 +382,7 @@ class Norm:
 
     @property
     def c(self):
-        return moe_norm_params(self.kind, self.eps, _ptr(self.weight), _ptr(self.bias))
-
-    def tensors(self):
-        return self.weight, self.bias
+        return moe_norm_params(self.kind, self.eps, _addr(self.weight), _addr(self.bias))
 
 
 class Gate:
@@ -380,33 +394,30 @@ class Gate:
 
     @property
     def c(self):
-        return moe_gate_params(self.alpha, _ptr(self.channel), _ptr(self.token))
+        return moe_gate_params(self.alpha, _addr(self.channel), _addr(self.token))
 
 
 def _params(T, H, device, norms, gate=None):
     """Checks the parameters of a call; returns their type."""
     dt = None
-    named = [(t, w) for n in norms if n is not None for t, w in zip(n.tensors(), ("weight", "bias"))]
+    named = [(t, w) for n in norms if n is not None
+             for t, w in ((n.weight, "weight"), (n.bias, "bias")) if t is not None]
     if gate is not None:
-        named.append((gate.channel, "channel"))
+        if gate.channel is not None:
+            named.append((gate.channel, "channel"))
         if gate.token is not None:
             _shaped(gate.token, (T,), "token", torch.float32)
+            if gate.token.get_device() != device:
+                _refuse(f"token on {gate.token.device}, the tokens on another")
     for t, what in named:
-        if t is None:
-            continue
         _shaped(t, (H,), what)
-        if dt is not None and t.dtype != dt:
+        if dt is None:
+            dt = t.dtype
+        elif t.dtype != dt:
             raise MoEError(MOE_EUNSUPPORTED, f"parameters of {dt} and {t.dtype} in one call")
-        dt = t.dtype
-        if t.device != device:
-            _refuse(f"{what} on {t.device}, the tokens on {device}")
-    if gate is not None and gate.token is not None and gate.token.device != device:
-        _refuse(f"token on {gate.token.device}, the tokens on {device}")
-    if dt is None or dt == torch.float32:
-        return MOE_F32
-    if dt == torch.bfloat16:
-        return MOE_BF16
-    raise MoEError(MOE_EUNSUPPORTED, f"parameter dtype {dt}")
+        if t.get_device() != device:
+            _refuse(f"{what} on {t.device}, the tokens on another")
+    return MOE_F32 if dt is None else _dt(t)
 
 
 def _rows(t, plan, H, what, dtype=None):
@@ -439,8 +450,8 @@ def moe_permute(x, plan, rows, stream=None):
     T, H = _planned(x, plan, "x")
     _rows(rows, plan, H, "rows", x.dtype)
     dev = _one_device(x, rows, plan.inv_pos)
-    _call(lib().moe_permute, dev, stream, _ptr(x), _dt(x), T, H, plan.E, plan.K,
-          ctypes.byref(plan.c), _ptr(rows))
+    _call(lib().moe_permute, dev, stream, _addr(x), _dt(x), T, H, plan.E, plan.K,
+          ctypes.byref(plan.c), _addr(rows))
 
 
 def moe_permute_backward(drows, plan, dx, stream=None):
@@ -448,8 +459,8 @@ def moe_permute_backward(drows, plan, dx, stream=None):
     T, H = _planned(dx, plan, "dx")
     _rows(drows, plan, H, "drows", dx.dtype)
     dev = _one_device(dx, drows, plan.inv_pos)
-    _call(lib().moe_permute_backward, dev, stream, _ptr(drows), _dt(dx), T, H, plan.E, plan.K,
-          ctypes.byref(plan.c), _ptr(dx))
+    _call(lib().moe_permute_backward, dev, stream, _addr(drows), _dt(dx), T, H, plan.E, plan.K,
+          ctypes.byref(plan.c), _addr(dx))
 
 
 def moe_unpermute(rows, topk_w, plan, out, shared=None, stream=None):
@@ -461,9 +472,9 @@ def moe_unpermute(rows, topk_w, plan, out, shared=None, stream=None):
     if shared is not None:
         _shaped(shared, (T, H), "shared")
     dev = _one_device(out, rows, topk_w, shared, plan.inv_pos)
-    _call(lib().moe_unpermute, dev, stream, _ptr(rows), _dt(rows), _ptr(topk_w), _ptr(shared),
+    _call(lib().moe_unpermute, dev, stream, _addr(rows), _dt(rows), _addr(topk_w), _addr(shared),
           _dt(shared) if shared is not None else MOE_F32, T, H, plan.E, plan.K,
-          ctypes.byref(plan.c), _ptr(out), _dt(out))
+          ctypes.byref(plan.c), _addr(out), _dt(out))
 
 
 def moe_unpermute_backward(dout, rows, topk_w, plan, drows=None, dw=None, stream=None):
@@ -477,8 +488,8 @@ def moe_unpermute_backward(dout, rows, topk_w, plan, drows=None, dw=None, stream
         if t is not None:
             _shaped(t, (T, plan.K), what, torch.float32)
     dev = _one_device(dout, rows, topk_w, drows, dw, plan.inv_pos)
-    _call(lib().moe_unpermute_backward, dev, stream, _ptr(dout), _ptr(rows), _dt(dout),
-          _ptr(topk_w), T, H, plan.E, plan.K, ctypes.byref(plan.c), _ptr(drows), _ptr(dw))
+    _call(lib().moe_unpermute_backward, dev, stream, _addr(dout), _addr(rows), _dt(dout),
+          _addr(topk_w), T, H, plan.E, plan.K, ctypes.byref(plan.c), _addr(drows), _addr(dw))
 
 
 def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None):
@@ -492,8 +503,8 @@ def moe_route_backward(topk_ids, topk_w, dw, dlogits, stream=None):
     _shaped(dw, (T, K), "dw", torch.float32)
     _shaped(dlogits, (T, E), "dlogits", torch.float32)
     dev = _one_device(topk_ids, topk_w, dw, dlogits)
-    _call(lib().moe_route_backward, dev, stream, _ptr(topk_ids), _ptr(topk_w), _ptr(dw), T, E, K,
-          _ptr(dlogits))
+    _call(lib().moe_route_backward, dev, stream, _addr(topk_ids), _addr(topk_w), _addr(dw), T, E, K,
+          _addr(dlogits))
 
 
 def moe_norm_workspace_bytes(T, H):
@@ -505,7 +516,7 @@ def _workspace(t):
         return None, 0
     if not t.is_contiguous():
         _refuse("workspace must be contiguous")
-    return _ptr(t), t.numel() * t.element_size()
+    return _addr(t), t.numel() * t.element_size()
 
 
 def _optional(H, **named):
@@ -520,7 +531,7 @@ def moe_norm(x, norm, out, stream=None):
     _shaped(out, (T, H), "out")
     dev = _one_device(x, out)
     pdt = _params(T, H, dev, (norm,))
-    _call(lib().moe_norm, dev, stream, _ptr(x), _dt(x), T, H, ctypes.byref(norm.c), pdt, _ptr(out),
+    _call(lib().moe_norm, dev, stream, _addr(x), _dt(x), T, H, _ref(norm), pdt, _addr(out),
           _dt(out))
 
 
@@ -537,14 +548,14 @@ def moe_norm_backward(dout, x, norm, dx, workspace=None, dres=None, dweight=None
     dev = _one_device(x, dout, dx, dres, dweight, dbias, workspace)
     pdt = _params(T, H, dev, (norm,))
     ws, n = _workspace(workspace)
-    _call(lib().moe_norm_backward, dev, stream, _ptr(dout), _dt(dout), _ptr(x), _dt(x), _ptr(dres),
-          T, H, ctypes.byref(norm.c), pdt, _ptr(dx), _ptr(dweight), _ptr(dbias), ws, n)
+    _call(lib().moe_norm_backward, dev, stream, _addr(dout), _dt(dout), _addr(x), _dt(x), _addr(dres),
+          T, H, _ref(norm), pdt, _addr(dx), _addr(dweight), _addr(dbias), ws, n)
 
 
 def _next_norm(pre, n, T, H, dtype):
     if n is not None:
         _shaped(n, (T, H), "n", dtype)
-    return ctypes.byref(pre.c) if pre is not None else None
+    return _ref(pre)
 
 
 def moe_norm_residual(y, x, post, gate, r, pre=None, n=None, stream=None):
@@ -555,8 +566,8 @@ def moe_norm_residual(y, x, post, gate, r, pre=None, n=None, stream=None):
     nx = _next_norm(pre, n, T, H, y.dtype)
     dev = _one_device(x, y, r, n)
     pdt = _params(T, H, dev, (post, pre), gate)
-    _call(lib().moe_norm_residual, dev, stream, _ptr(y), _dt(y), _ptr(x), _dt(x), T, H,
-          ctypes.byref(post.c), ctypes.byref(gate.c), pdt, _ptr(r), nx, _ptr(n))
+    _call(lib().moe_norm_residual, dev, stream, _addr(y), _dt(y), _addr(x), _dt(x), T, H,
+          _ref(post), _ref(gate), pdt, _addr(r), nx, _addr(n))
 
 
 def moe_combine_norm_residual(y_pairs, topk_w, x, post, gate, r, pre=None, n=None, shared=None,
@@ -576,9 +587,9 @@ def moe_combine_norm_residual(y_pairs, topk_w, x, post, gate, r, pre=None, n=Non
     nx = _next_norm(pre, n, T, H, y_pairs.dtype)
     dev = _one_device(x, y_pairs, topk_w, shared, r, n)
     pdt = _params(T, H, dev, (post, pre), gate)
-    _call(lib().moe_combine_norm_residual, dev, stream, _ptr(y_pairs), _dt(y_pairs), _ptr(topk_w),
-          _ptr(shared), _dt(shared) if shared is not None else MOE_F32, _ptr(x), _dt(x), T, K, H,
-          ctypes.byref(post.c), ctypes.byref(gate.c), pdt, _ptr(r), nx, _ptr(n))
+    _call(lib().moe_combine_norm_residual, dev, stream, _addr(y_pairs), _dt(y_pairs), _addr(topk_w),
+          _addr(shared), _dt(shared) if shared is not None else MOE_F32, _addr(x), _dt(x), T, K, H,
+          _ref(post), _ref(gate), pdt, _addr(r), nx, _addr(n))
 
 
 def moe_norm_residual_backward(dr, y, post, gate, dy, workspace=None, dweight=None, dbias=None,
@@ -594,6 +605,6 @@ def moe_norm_residual_backward(dr, y, post, gate, dy, workspace=None, dweight=No
     dev = _one_device(y, dr, dy, dweight, dbias, dchannel, dtoken, workspace)
     pdt = _params(T, H, dev, (post,), gate)
     ws, n = _workspace(workspace)
-    _call(lib().moe_norm_residual_backward, dev, stream, _ptr(dr), _dt(dr), _ptr(y), _dt(y), T, H,
-          ctypes.byref(post.c), ctypes.byref(gate.c), pdt, _ptr(dy), _ptr(dweight), _ptr(dbias),
-          _ptr(dchannel), _ptr(dtoken), ws, n)
+    _call(lib().moe_norm_residual_backward, dev, stream, _addr(dr), _dt(dr), _addr(y), _dt(y), T, H,
+          _ref(post), _ref(gate), pdt, _addr(dy), _addr(dweight), _addr(dbias),
+          _addr(dchannel), _addr(dtoken), ws, n)

@@ -30,13 +30,14 @@ bool optional(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0
 
 bool valid_dtype(int dt) { return dt == MOE_F32 || dt == MOE_BF16; }
 
-// H elements of either type are whole 16-byte vectors; a row tensor's elements
-// are counted in 63 bits
+// H elements of either type are whole 16-byte vectors; the kernels count a
+// token tensor's pieces of 256 elements, and a row's last one, in 32 bits
 moe_status check_rows(const char* what, int64_t T, int H) {
   if (T < 0) return fail(MOE_EINVAL, "%s: T = %lld < 0", what, (long long)T);
   if (T >= (int64_t)1 << 31) return fail(MOE_EUNSUPPORTED, "%s: T must be < 2^31", what);
   if (H < 8 || H % 8 != 0)
     return fail(MOE_EUNSUPPORTED, "%s: H = %d must be a positive multiple of 8", what, H);
+  if (T * H >= (int64_t)1 << 39) return fail(MOE_EUNSUPPORTED, "%s: T*H must be < 2^39", what);
   return MOE_OK;
 }
 

@@ -39,7 +39,7 @@ def expect(fn, good, table):
         assert fn.__name__.encode() in B.lib().moe_last_error(), bad
 
 
-SORT = [(INV, dict(T=-1)), (UNS, dict(T=1 << 31)), (UNS, dict(H=100)), (UNS, dict(H=0)), (INV, dict(K=0)),
+SORT = [(INV, dict(T=-1)), (UNS, dict(T=1 << 31)), (UNS, dict(T=1 << 24, H=1 << 15)), (UNS, dict(H=100)), (UNS, dict(H=0)), (INV, dict(K=0)),
         (INV, dict(K=257)), (UNS, dict(E=257)), (INV, dict(plan=None)), (INV, dict(plan=plan(ptr=0))),
         (INV, dict(plan=plan(ptr=FAKE + 2))), (INV, dict(plan=plan(cap=4865))),
         (UNS, dict(plan=plan(block_m=0))), (CAP, dict(plan=plan(cap=1024)))]

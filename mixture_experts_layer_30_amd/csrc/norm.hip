@@ -579,14 +579,15 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
 
 // The parameters' gradients from the partial sums [G][H] of S1 and S0 (null: not
 // asked for), added in a fixed order; zeros for G = 0.  A workgroup takes 32
-// columns: 8 lanes of 4 columns, 32 groups of lanes with every 32nd row each, then
-// the groups in order.
+// columns: 8 lanes of 4 columns, kSumGroups groups of lanes with every
+// kSumGroups-th row each; then 8 groups add up a run of those sums each, and one
+// the 8.
 struct ParamGrads {
   const float *part1, *part0;
   const void *weight, *bias, *channel;
   float *dweight, *dbias, *dchannel;
 };
-constexpr int kSumLanes = 8, kSumGroups = 32;
+constexpr int kSumLanes = 8, kSumGroups = 64;
 template <class SP>
 __global__ __launch_bounds__(kSumLanes* kSumGroups) void param_grads_kernel(ParamGrads p, int G,
                                                                             int H) {
@@ -594,11 +595,10 @@ __global__ __launch_bounds__(kSumLanes* kSumGroups) void param_grads_kernel(Para
   const int lane = threadIdx.x % kSumLanes, grp = threadIdx.x / kSumLanes;
   const int h = (blockIdx.x * kSumLanes + lane) * 4;
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-  f32x4 s1 = zero, s0 = zero;
   auto param = [&](const void* q, float none, float* o) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = none;
-    if (q && h < H) {
+    if (q && grp == 0 && h < H) {
       Raw<SP, 4> r;
       r.template load<kCached>(row_at(q, 0, H * SP::kBytes), h);
       r.get4(0, o);
@@ -608,33 +608,39 @@ __global__ __launch_bounds__(kSumLanes* kSumGroups) void param_grads_kernel(Para
   param(p.weight, 1.0f, w);
   param(p.bias, 0.0f, b);
   param(p.channel, 1.0f, c);
-  if (h < H) {
-    if (p.part1) {
-#pragma unroll 8
+  f32x4 s[2] = {zero, zero};
+  const float* part[2] = {p.part1, p.part0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+    if (part[k] && h < H) {
+#pragma unroll 4
       for (int g = grp; g < G; g += kSumGroups)
-        s1 += *reinterpret_cast<const f32x4*>(p.part1 + (int64_t)g * H + h);
+        s[k] += *reinterpret_cast<const f32x4*>(part[k] + (int64_t)g * H + h);
     }
-    if (p.part0) {
-#pragma unroll 8
-      for (int g = grp; g < G; g += kSumGroups)
-        s0 += *reinterpret_cast<const f32x4*>(p.part0 + (int64_t)g * H + h);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) buf[k][grp][lane] = s[k];
+  __syncthreads();
+  constexpr int kRun = kSumGroups / 8;
+  if (grp < 8) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      s[k] = buf[k][grp * kRun][lane];
+#pragma unroll
+      for (int g = 1; g < kRun; ++g) s[k] += buf[k][grp * kRun + g][lane];
+      buf[k][grp * kRun][lane] = s[k];   // (read by this lane alone)
     }
   }
-  buf[0][grp][lane] = s1;
-  buf[1][grp][lane] = s0;
   __syncthreads();
   if (grp != 0 || h >= H) return;
-  s1 = s0 = zero;
-#pragma unroll 4
-  for (int g = 0; g < kSumGroups; ++g) {
-    s1 += buf[0][g][lane];
-    s0 += buf[1][g][lane];
-  }
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int g = 1; g < 8; ++g) s[k] += buf[k][g * kRun][lane];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (p.dweight) p.dweight[h + i] = c[i] * s1[i];
-    if (p.dbias) p.dbias[h + i] = c[i] * s0[i];
-    if (p.dchannel) p.dchannel[h + i] = fmaf(b[i], s0[i], w[i] * s1[i]);
+    if (p.dweight) p.dweight[h + i] = c[i] * s[0][i];
+    if (p.dbias) p.dbias[h + i] = c[i] * s[1][i];
+    if (p.dchannel) p.dchannel[h + i] = fmaf(b[i], s[1][i], w[i] * s[0][i]);
   }
 }
 

@@ -272,46 +272,46 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
 }
 
 // dlogits[t][e] = sum over the slots j with id e of w_j (dw_j - sum_i w_i dw_i).
-// One wavefront a token, its slots held 64 to a register; each lane owns every
-// 64th expert and looks the slots through in order.
+// One wavefront a token, its slots held 64 to a register (kSlotRegs of them); each
+// lane owns every 64th expert (kOutRegs) and looks the slots through in order.
+template <int kSlotRegs, int kOutRegs>
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const int32_t* __restrict__ ids, const float* __restrict__ w, const float* __restrict__ dw,
     int64_t T, int E, int K, float* __restrict__ dlogits) {
   const int lane = threadIdx.x & (kWave - 1);
-  const int64_t waves = (int64_t)gridDim.x * kWaves;
-  for (int64_t t = (int64_t)blockIdx.x * kWaves + threadIdx.x / kWave; t < T; t += waves) {
-    // at most 256 slots: 4 a lane
-    int id[4];
-    float g[4], s = 0.0f;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < T; t += (int64_t)gridDim.x * kWaves) {
+    int id[kSlotRegs];
+    float g[kSlotRegs], d[kSlotRegs], s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < kSlotRegs; ++j) {
       const int k = j * kWave + lane;
-      id[j] = k < K ? ids[t * K + k] : -1;
-      const bool used = id[j] >= 0 && id[j] < E;
-      const float wk = used ? w[t * K + k] : 0.0f, d = used ? dw[t * K + k] : 0.0f;
-      s = fmaf(wk, d, s);
-      g[j] = wk;
-      // (held until s is known)
-      id[j] = used ? id[j] : -1;
+      const bool there = k < K;
+      id[j] = there ? ids[t * K + k] : -1;
+      g[j] = there ? w[t * K + k] : 0.0f;
+      d[j] = there ? dw[t * K + k] : 0.0f;
+      if (id[j] < 0 || id[j] >= E) {   // unused: whatever its weight and gradient hold
+        id[j] = -1;
+        g[j] = d[j] = 0.0f;
+      }
+      s = fmaf(g[j], d[j], s);
     }
     s = wave_sum(s);
-    float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int k = j * kWave + lane;
-      g[j] = id[j] >= 0 ? g[j] * (dw[t * K + k] - s) : 0.0f;
-    }
+    for (int j = 0; j < kSlotRegs; ++j) g[j] *= d[j] - s;
+    float o[kOutRegs];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int i = 0; i < kOutRegs; ++i) o[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < kSlotRegs; ++j)
       for (int l = 0; l < kWave && j * kWave + l < K; ++l) {
         const int e = __builtin_amdgcn_readlane(id[j], l);
         const float ge = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(g[j]), l));
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (e == i * kWave + lane) o[i] += ge;
+        for (int i = 0; i < kOutRegs; ++i) o[i] += e == i * kWave + lane ? ge : 0.0f;
       }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kOutRegs; ++i)
       if (i * kWave + lane < E) dlogits[t * E + i * kWave + lane] = o[i];
   }
 }
@@ -433,8 +433,14 @@ hipError_t launch_unpermute_backward(const void* dout, const void* rows, int dt,
 
 hipError_t launch_route_backward(const int32_t* ids, const float* w, const float* dw, int64_t T,
                                  int E, int K, float* dlogits, hipStream_t s) {
-  hipLaunchKernelGGL(route_backward_kernel, dim3(grid_of((T + kWaves - 1) / kWaves)),
-                     dim3(kThreads), 0, s, ids, w, dw, T, E, K, dlogits);
+  auto go = [&](auto kernel) {
+    hipLaunchKernelGGL(kernel, dim3(grid_of((T + kWaves - 1) / kWaves)), dim3(kThreads), 0, s, ids,
+                       w, dw, T, E, K, dlogits);
+  };
+  // (K <= E <= 256)
+  if (E <= kWave) go(route_backward_kernel<1, 1>);
+  else if (K <= kWave) go(route_backward_kernel<1, 4>);
+  else go(route_backward_kernel<4, 4>);
   return hipGetLastError();
 }
 

@@ -360,8 +360,8 @@ moe_status dense_ffn_fa(const void *x, moe_dtype dt, int64_t T, int H, int I_fa,
  * every result is the same on every run.
  * x, dx [T][H] dt; rows, drows [plan->cap][H] dt / rdt; dout, out [T][H] odt;
  * shared [T][H] sdt; topk_w, dw [T][K] fp32.  dout and rows have the same type.
- * Limits: H a multiple of 8.  Row indices of the plan outside [0, plan->cap)
- * are taken as unused slots.
+ * Limits: H a multiple of 8, T*H < 2^39.  Row indices of the plan outside
+ * [0, plan->cap) are taken as unused slots.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED (H, dtype), MOE_ECAPACITY (a plan whose
  * cap is below what either padding may need).
  */
@@ -432,17 +432,23 @@ typedef struct {
  *
  * n is computed from r before r is rounded.  pdt is the type of every weight,
  * bias and channel gate of the call.  x, r, dx, dres and dr are of type xdt; y,
- * dy and moe_norm_residual's n of type ydt; moe_norm's n and dn of type odt.
+ * dy and the n of the two residual calls of type ydt; moe_norm's n and dn of
+ * type odt.
  * Parameter gradients are fp32 [H] (dtoken fp32 [T]), overwritten, summed over
- * the tokens in a fixed order: the same on every run.  Each may be NULL; one of
- * a parameter that the call has not (a NULL weight's is that of ones) is refused
- * for the gates and for MOE_NORM_NONE.  r may be x, n may be y, dx may be dn or
- * dres, and dy may be dr or y where the types agree; other overlaps are not
- * allowed.
- * workspace: >= moe_norm_workspace_bytes(T, H) bytes for the partial sums, needed
- * only where a gradient of weight, bias or channel is asked for (else may be
- * NULL).  T = 0 writes zeros to those gradients and does nothing else.
- * Limits: H a multiple of 8, at most 16384.
+ * the tokens in a fixed order: the same on every run.  Each may be NULL.  A NULL
+ * weight's or bias's gradient is that of the ones or zeros it stands for; that
+ * of a gate that is not there, or of MOE_NORM_NONE's parameters, is refused.
+ * In place, where the types agree: moe_norm's n may be x, r may be x,
+ * moe_norm_residual's n may be y, dx may be dn or dres, and dy may be dr or y;
+ * other overlaps are not allowed.
+ * workspace: >= moe_norm_workspace_bytes(T, H) bytes for partial sums, 16-byte
+ * aligned, needed only where a gradient of weight, bias or channel is asked for
+ * (else it may be NULL), with no contents to keep before or after the call;
+ * calls that may overlap need one each.  T = 0 writes zeros to those gradients
+ * and does nothing else.
+ * Squares are summed in fp32: rows whose sum of squares overflows it normalise
+ * to zeros, and a row of zeros with eps = 0 to NaN.
+ * Limits: H a multiple of 8, at most 16384; T*H < 2^39.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY (workspace).
  */
 int64_t moe_norm_workspace_bytes(int64_t T, int H);   /* -1 on bad arguments */

@@ -328,12 +328,13 @@ def _refuse(what):
 
 def _shaped(t, shape, what, dtype=None):
     """t is a tensor of this shape (and type), its elements in row-major order."""
+    if t.shape == shape and (dtype is None or t.dtype is dtype) and t.is_contiguous():
+        return
     if t.shape != shape:
         _refuse(f"{what} must have shape {list(shape)}, got {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise MoEError(MOE_EUNSUPPORTED, f"{what} must be {dtype}, got {t.dtype}")
-    if not t.is_contiguous():
-        _refuse(f"{what} must be contiguous")
+    _refuse(f"{what} must be contiguous")
 
 
 def _addr(t):
@@ -370,7 +371,8 @@ def _one_device(first, *rest):
 
 
 def _ref(o):
-    return None if o is None else ctypes.byref(o.c)
+    """The C struct of a Norm or Gate by reference, as the object is now; None: NULL."""
+    return None if o is None else o.ref()
 
 
 class Norm:
@@ -379,10 +381,14 @@ class Norm:
 
     def __init__(self, kind=NORM_RMS, eps=1e-6, weight=None, bias=None):
         self.kind, self.eps, self.weight, self.bias = kind, eps, weight, bias
+        self._c = moe_norm_params()
+        self._ref = ctypes.byref(self._c)
 
-    @property
-    def c(self):
-        return moe_norm_params(self.kind, self.eps, _addr(self.weight), _addr(self.bias))
+    def ref(self):
+        c = self._c
+        c.kind, c.eps = self.kind, self.eps
+        c.weight, c.bias = _addr(self.weight), _addr(self.bias)
+        return self._ref
 
 
 class Gate:
@@ -391,33 +397,46 @@ class Gate:
 
     def __init__(self, alpha=1.0, channel=None, token=None):
         self.alpha, self.channel, self.token = alpha, channel, token
+        self._c = moe_gate_params()
+        self._ref = ctypes.byref(self._c)
 
-    @property
-    def c(self):
-        return moe_gate_params(self.alpha, _addr(self.channel), _addr(self.token))
+    def ref(self):
+        c = self._c
+        c.alpha, c.channel, c.token = self.alpha, _addr(self.channel), _addr(self.token)
+        return self._ref
 
 
-def _params(T, H, device, norms, gate=None):
+def _param(t, H, dt, device, what):
+    """Checks a parameter (None: absent) against those before it, of type dt; the type since."""
+    if t is None:
+        return dt
+    _shaped(t, (H,), what)
+    if dt is not None and t.dtype is not dt:
+        raise MoEError(MOE_EUNSUPPORTED, f"parameters of {dt} and {t.dtype} in one call")
+    if t.get_device() != device:
+        _refuse(f"{what} on {t.device}, the tokens on another")
+    return t.dtype
+
+
+def _params(T, H, device, norm, gate=None, next_norm=None):
     """Checks the parameters of a call; returns their type."""
     dt = None
-    named = [(t, w) for n in norms if n is not None
-             for t, w in ((n.weight, "weight"), (n.bias, "bias")) if t is not None]
+    if norm is not None:
+        dt = _param(norm.bias, H, _param(norm.weight, H, dt, device, "weight"), device, "bias")
+    if next_norm is not None:
+        dt = _param(next_norm.bias, H, _param(next_norm.weight, H, dt, device, "weight"), device,
+                    "bias")
     if gate is not None:
-        if gate.channel is not None:
-            named.append((gate.channel, "channel"))
+        dt = _param(gate.channel, H, dt, device, "channel")
         if gate.token is not None:
             _shaped(gate.token, (T,), "token", torch.float32)
             if gate.token.get_device() != device:
                 _refuse(f"token on {gate.token.device}, the tokens on another")
-    for t, what in named:
-        _shaped(t, (H,), what)
-        if dt is None:
-            dt = t.dtype
-        elif t.dtype != dt:
-            raise MoEError(MOE_EUNSUPPORTED, f"parameters of {dt} and {t.dtype} in one call")
-        if t.get_device() != device:
-            _refuse(f"{what} on {t.device}, the tokens on another")
-    return MOE_F32 if dt is None else _dt(t)
+    if dt is None or dt is torch.float32:
+        return MOE_F32
+    if dt is torch.bfloat16:
+        return MOE_BF16
+    raise MoEError(MOE_EUNSUPPORTED, f"parameter dtype {dt}")
 
 
 def _rows(t, plan, H, what, dtype=None):
@@ -530,7 +549,7 @@ def moe_norm(x, norm, out, stream=None):
     T, H = _tokens(x, "x")
     _shaped(out, (T, H), "out")
     dev = _one_device(x, out)
-    pdt = _params(T, H, dev, (norm,))
+    pdt = _params(T, H, dev, norm)
     _call(lib().moe_norm, dev, stream, _addr(x), _dt(x), T, H, _ref(norm), pdt, _addr(out),
           _dt(out))
 
@@ -546,7 +565,7 @@ def moe_norm_backward(dout, x, norm, dx, workspace=None, dres=None, dweight=None
         _shaped(dres, (T, H), "dres", x.dtype)
     _optional(H, dweight=dweight, dbias=dbias)
     dev = _one_device(x, dout, dx, dres, dweight, dbias, workspace)
-    pdt = _params(T, H, dev, (norm,))
+    pdt = _params(T, H, dev, norm)
     ws, n = _workspace(workspace)
     _call(lib().moe_norm_backward, dev, stream, _addr(dout), _dt(dout), _addr(x), _dt(x), _addr(dres),
           T, H, _ref(norm), pdt, _addr(dx), _addr(dweight), _addr(dbias), ws, n)
@@ -565,7 +584,7 @@ def moe_norm_residual(y, x, post, gate, r, pre=None, n=None, stream=None):
     _shaped(r, (T, H), "r", x.dtype)
     nx = _next_norm(pre, n, T, H, y.dtype)
     dev = _one_device(x, y, r, n)
-    pdt = _params(T, H, dev, (post, pre), gate)
+    pdt = _params(T, H, dev, post, gate, pre)
     _call(lib().moe_norm_residual, dev, stream, _addr(y), _dt(y), _addr(x), _dt(x), T, H,
           _ref(post), _ref(gate), pdt, _addr(r), nx, _addr(n))
 
@@ -586,7 +605,7 @@ def moe_combine_norm_residual(y_pairs, topk_w, x, post, gate, r, pre=None, n=Non
         _shaped(shared, (T, H), "shared")
     nx = _next_norm(pre, n, T, H, y_pairs.dtype)
     dev = _one_device(x, y_pairs, topk_w, shared, r, n)
-    pdt = _params(T, H, dev, (post, pre), gate)
+    pdt = _params(T, H, dev, post, gate, pre)
     _call(lib().moe_combine_norm_residual, dev, stream, _addr(y_pairs), _dt(y_pairs), _addr(topk_w),
           _addr(shared), _dt(shared) if shared is not None else MOE_F32, _addr(x), _dt(x), T, K, H,
           _ref(post), _ref(gate), pdt, _addr(r), nx, _addr(n))
@@ -603,7 +622,7 @@ def moe_norm_residual_backward(dr, y, post, gate, dy, workspace=None, dweight=No
     if dtoken is not None:
         _shaped(dtoken, (T,), "dtoken", torch.float32)
     dev = _one_device(y, dr, dy, dweight, dbias, dchannel, dtoken, workspace)
-    pdt = _params(T, H, dev, (post,), gate)
+    pdt = _params(T, H, dev, post, gate)
     ws, n = _workspace(workspace)
     _call(lib().moe_norm_residual_backward, dev, stream, _addr(dr), _dt(dr), _addr(y), _dt(y), T, H,
           _ref(post), _ref(gate), pdt, _addr(dy), _addr(dweight), _addr(dbias),

@@ -12,7 +12,15 @@
 // as many lanes: a wavefront where the row fills one (its row index and weight
 // then sit in scalar registers, and its loads take the row's address from them),
 // else the smallest power of two of lanes that holds the row, several rows to a
-// wavefront.
+// wavefront (16384 tokens of 64, 8 experts each: permute 4.9 us, with a wavefront a
+// row 16; unpermute 8.1 and 15; of 256: unpermute 14.5 and 20).
+//
+// Measured on MI355X, inputs that no cache holds (a copy of 1 GB runs at 5.1 TB/s):
+// 16384 tokens of 3584 bf16 to 8 experts each 211 us (1.09 GB with the padding, 5.1
+// TB/s); the tokens' gradient from 32768 rows of 7168 90 us (5.9 TB/s); the gradients
+// of 65536 rows of 7168 with 16 thousand padding rows 409 us (2.3 GB, 5.7 TB/s).  Units
+// by alignment row, so that the rows are read and written in order and the tokens
+// gathered, run the last one in 470 us.
 #include "common.h"
 #include "kernels.h"
 
@@ -21,9 +29,10 @@ namespace moe {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 
-// The rows are streamed: a buffer of them is far larger than the caches, each
-// element is used once, and stores of whole lines that bypass them leave the
-// tokens, which are read K times over, in place.
+// The rows are streamed: a buffer of them is larger than the caches, each element
+// is used once, and the tokens, which gradients read K times over, stay in place
+// (weighted sums of 5003 tokens with budgets 52 -> 47 us, 32768 rows of 7168 102 ->
+// 90; stores: the gradients above 430 -> 415).
 __device__ __forceinline__ u32x4 stream_load(const u32x4* p) {
   return __builtin_nontemporal_load(p);
 }
@@ -158,7 +167,7 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(
   }
 }
 
-constexpr int kSlots = 4;   // rows in flight per lane
+constexpr int kSlots = 4;   // rows in flight per lane (8: 98 us for 89 at 32768 rows of 7168)
 
 // out[t] = sum_k w[t][k] rows[inv_pos[t*K + k]] (+ shared[t]); w null: ones.
 template <class SR, class SS, class SO, int kLanes>
@@ -222,7 +231,9 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
     uint32_t pairs, int K, int nv, uint32_t groups, const int32_t* __restrict__ inv_pos,
     int64_t cap, u32x4* drows, float* __restrict__ dw, uint32_t pads, Padding pad) {
   constexpr int N = Vec<S>::N;
-  constexpr int kSteps = kLanes == kWave ? 4 : 1;   // vectors of a row in flight per lane
+  // vectors of a row in flight per lane (16384 x 8 rows of 1032: 1 149 us, 2 141, 4 131;
+  // a row on part of a wavefront has one)
+  constexpr int kSteps = kLanes == kWave ? 4 : 1;
   for (uint32_t b = blockIdx.x; b < groups + pads; b += gridDim.x) {
     if (b >= groups) {   // (there are none where drows is null)
       zero_padding(b - groups, pad, nv, cap, drows);

@@ -446,8 +446,8 @@ typedef struct {
  * (else it may be NULL), with no contents to keep before or after the call;
  * calls that may overlap need one each.  T = 0 writes zeros to those gradients
  * and does nothing else.
- * Squares are summed in fp32: rows whose sum of squares overflows it normalise
- * to zeros, and a row of zeros with eps = 0 to NaN.
+ * Squares are summed in fp32: with eps = 0 a row of zeros, or one whose squares
+ * underflow, has no norm (NaN), and elements past 1e19 overflow it.
  * Limits: H a multiple of 8, at most 16384; T*H < 2^39.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY (workspace).
  */

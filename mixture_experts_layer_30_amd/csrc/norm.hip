@@ -540,9 +540,10 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
     block_sum<4>(s, waves, buf.take());
     const float rstd = n.kind != kNormNone ? rsqrtf(fmaf(s[0], inv_h, n.eps)) : 1.0f;
     if (dtoken && threadIdx.x == 0) dtoken[t] = gate.alpha * fmaf(s[1], rstd, s[3]);
-    // dv = (ar e) f - ag - (x - mean) agx
+    // dv = (ar e) f - ag - ((x - mean) rstd) agx  (rstd by itself: its cube overflows
+    // for rows as small as 1e-13)
     const float ar = a * rstd;
-    const float agx = n.kind != kNormNone ? ar * rstd * rstd * (s[1] * inv_h) : 0.0f;
+    const float agx = n.kind != kNormNone ? ar * (rstd * (s[1] * inv_h)) : 0.0f;
     const float ag = layer ? ar * (s[2] * inv_h) : 0.0f;
     const Row out = row_at(dv, t, vb);
 #pragma unroll
@@ -576,7 +577,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
           const int k = 4 * q + i;
           const float er = ar * d[i];
           s1[j][k] = fmaf(er, x[i], s1[j][k]);
-          oq[i] = fmaf(er, f[j][k], fmaf(-agx, x[i], oq[i]));
+          oq[i] = fmaf(er, f[j][k], fmaf(-agx, x[i] * rstd, oq[i]));
         }
       }
       put<SV, N, kStreamed>(out, sl.h(j), o);

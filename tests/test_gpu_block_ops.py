@@ -539,12 +539,17 @@ def test_norm_residual_backward(T, H, ydt, xdt, pdt, kind, channel, token, alpha
     if norm:
         close(dw, *columns(du * ref.xh, du.abs() * (ref.e_xh + 4 * E24 * ref.xh.abs())))
         close(db, *columns(du, 4 * E24 * du.abs()))
+    # u = xh w + b: both sums are taken of the two terms apart and put together at the end
+    # (w sum(..xh) + b sum(..)), so their roundings go by the terms' magnitudes
     u, eu = ref.out, ref.e_out
+    mag = (ref.xh * ref.w).abs() + ref.b.abs()
     if channel:
-        close(dc, *columns(a * d * u, (a * d).abs() * (eu + 3 * E24 * u.abs())))
+        ad = a * d
+        err = (ad.abs() * (eu + 3 * E24 * mag)).sum(0) + (tchain(T) + 2) * E24 * (ad.abs() * mag).sum(0)
+        close(dc, (ad * u).sum(0), err)
     if token:
         v = float(np.float32(alpha)) * c * d
-        close(dq, (v * u).sum(1), (v.abs() * (eu + (hchain(H) + 4) * E24 * u.abs())).sum(1))
+        close(dq, (v * u).sum(1), (v.abs() * (eu + (hchain(H) + 4) * E24 * mag)).sum(1))
     # without parameter gradients, in place
     if norm or not (channel or token):
         y2 = y.clone()
@@ -554,6 +559,62 @@ def test_norm_residual_backward(T, H, ydt, xdt, pdt, kind, channel, token, alpha
         d2 = dr.clone()
         B.moe_norm_residual_backward(d2, y, post, gate, d2)
         assert torch.equal(d2, dy)
+
+
+@pytest.mark.parametrize("kind", [B.NORM_RMS, B.NORM_LAYER])
+def test_rows_of_tiny_values_without_eps(kind):
+    """Rows of 1e-15: their deviation's reciprocal cubed is past fp32."""
+    T, H = 3, 264
+    g = gen(23)
+    x, dn = randn(g, T, H) * 1e-15, randn(g, T, H) * 1e-15
+    n = B.Norm(kind, 0.0, randn(g, H, mean=1.0))
+    o, dx = torch.empty_like(x), torch.empty_like(x)
+    B.moe_norm(x, n, o)
+    ref = Ref(x, kind, n.weight, None, 0.0)
+    close(o, ref.out, ref.e_out)
+    B.moe_norm_backward(dn, x, n, dx)
+    gw = dn.double() * ref.w
+    close(dx, *ref.backward(gw, E24 * gw.abs()))
+
+
+def test_norms_past_32_bit_offsets():
+    """Token buffers of more than 2^32 bytes and 2^31 elements: the rows at both ends, and
+    the sums over all of them."""
+    T, H = 300007, 7168
+    assert T * H > 2 ** 31
+    g = gen(24)
+    x = torch.empty(T, H, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    n, gate = params(g, H, "f32", B.NORM_RMS), gates(g, T, H, "f32", True, True, 0.5)
+    o, r = torch.empty_like(x), torch.empty_like(x)
+    ws = torch.empty(B.moe_norm_workspace_bytes(T, H), dtype=torch.uint8, device=DEV)
+    dw, db, dc = (torch.empty(H, device=DEV) for _ in range(3))
+    dq = torch.empty(T, device=DEV)
+    B.moe_norm(x, n, o)
+    B.moe_norm_residual(o, x, n, gate, r)
+    some = torch.cat([torch.arange(40), torch.arange(T - 40, T)]).to(DEV)
+    ref = reference(x[some], n)
+    close(o[some], ref.out, ref.e_out)
+    part = B.Gate(gate.alpha, gate.channel, gate.token[some])
+    check_residual(r[some], None, reference(o[some], n), x[some], part, None, some.numel())
+    B.moe_norm_residual_backward(x, o, n, gate, r, ws, dw, db, dc, dq)   # x for the gradient
+    ref = reference(o[some], n)
+    a, c = gate_factors(part, some.numel())
+    gw = a * c * x[some].double() * ref.w
+    close(r[some], *ref.backward(gw, 4 * E24 * gw.abs()))
+    sums = torch.zeros(2, H, dtype=torch.float64, device=DEV)
+    mags = torch.zeros(2, H, dtype=torch.float64, device=DEV)
+    for lo in range(0, T, 8192):
+        ref = reference(o[lo:lo + 8192], n)
+        ad = gate_factors(B.Gate(gate.alpha, None, gate.token[lo:lo + 8192]), ref.xh.shape[0])[0] * x[lo:lo + 8192].double()
+        for i, v in enumerate((ad * ref.xh, ad)):
+            sums[i] += v.sum(0)
+            mags[i] += v.abs().sum(0)
+    # a row's xh is right to hchain(H) roundings, a sum over the tokens to tchain(T) more
+    err = (hchain(H) + tchain(T)) * E24 * mags
+    ch, w, b = gate.channel.double(), n.weight.double(), n.bias.double()
+    close(dw, ch * sums[0], ch.abs() * err[0])
+    close(db, ch * sums[1], ch.abs() * err[1])
+    close(dc, w * sums[0] + b * sums[1], w.abs() * err[0] + b.abs() * err[1])
 
 
 @pytest.mark.parametrize("kind", [B.NORM_RMS, B.NORM_LAYER])
@@ -828,3 +889,37 @@ def test_block_pass(T, shared, stream_dtype):
         c = torch.empty(T, H, device=DEV)
         B.moe_combine(layer.y_pairs, layer.topk_w, c, layer.shared_out if layer.has_shared else None)
         check_residual(r, n, reference(c, post), xin, gt, nxt, T)
+
+
+def test_block_pass_captured_in_a_graph():
+    """A block with shared experts (a second stream inside the layer), captured and replayed
+    on new tokens, eager passes of another block between the replays."""
+    shape = LayerShape("block", hidden=256, inter=192, experts=16, topk=4, shared_inter=128,
+                       dtype="bf16", tokens=(20,), routing=("uniform",))
+    g = gen(37)
+    T, H = 20, shape.hidden
+
+    def block(seed):
+        layer = MoELayer(shape, synth.layer_inputs(shape, T, seed=seed, device=DEV, dense=False))
+        return MoEBlock(layer, params(g, H, "f32", B.NORM_RMS), params(g, H, "f32", B.NORM_LAYER),
+                        gates(g, T, H, "f32", True, True, 0.5), next_norm=params(g, H, "f32", B.NORM_RMS))
+    one, other = block(1), block(2)
+    xs = [randn(g, T, H, dt="bf16") for _ in range(4)]
+    want = [tuple(t.clone() for t in one.forward(x)) for x in xs]
+    x = xs[0].clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        one.forward(x)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r, n = one.forward(x)
+    for i in (1, 2, 3, 0):
+        x.copy_(xs[i])
+        r.zero_()
+        n.zero_()
+        graph.replay()
+        other.forward(xs[0])
+        torch.cuda.synchronize()
+        assert torch.equal(r, want[i][0]) and torch.equal(n, want[i][1]), i

@@ -29,15 +29,15 @@ namespace moe {
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 
-// The rows are streamed: a buffer of them is larger than the caches, each element
-// is used once, and the tokens, which gradients read K times over, stay in place
-// (weighted sums of 5003 tokens with budgets 52 -> 47 us, 32768 rows of 7168 102 ->
-// 90; stores: the gradients above 430 -> 415).
-__device__ __forceinline__ u32x4 stream_load(const u32x4* p) {
-  return __builtin_nontemporal_load(p);
+// Row loads and stores, past the caches (non-temporal) where kStream says so.
+template <bool kStream>
+__device__ __forceinline__ u32x4 row_load(const u32x4* p) {
+  return kStream ? __builtin_nontemporal_load(p) : *p;
 }
-__device__ __forceinline__ void stream_store(u32x4* p, u32x4 v) {
-  __builtin_nontemporal_store(v, p);
+template <bool kStream>
+__device__ __forceinline__ void row_store(u32x4* p, u32x4 v) {
+  if constexpr (kStream) __builtin_nontemporal_store(v, p);
+  else *p = v;
 }
 
 // The 16 / kBytes elements of a vector as fp32, and back.
@@ -139,12 +139,12 @@ __device__ __forceinline__ void zero_padding(uint32_t item, const Padding& pad, 
   const int64_t stride = (int64_t)pad.subs * kThreads;
   for (int64_t i = first * nv + (item - e * pad.subs) * kThreads + threadIdx.x; i < end * nv;
        i += stride)
-    stream_store(rows + i, z);
+    row_store<true>(rows + i, z);
 }
 
 // rows[inv_pos[t*K + k]] = x[t] (rows of nv vectors; a token takes `chunks`
 // units), then the padding rows in `pads` items.
-template <int kLanes>
+template <int kLanes, bool kStream>
 __global__ __launch_bounds__(kThreads) void permute_kernel(
     const u32x4* __restrict__ x, uint32_t T, int K, int nv, uint32_t chunks, uint32_t groups,
     const int32_t* __restrict__ inv_pos, int64_t cap, u32x4* __restrict__ rows, uint32_t pads,
@@ -162,7 +162,7 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(
     const int32_t* pos = inv_pos + (int64_t)t * K;
     for (int k = 0; k < K; ++k) {
       const int64_t r = pos[k];
-      if (r >= 0 && r < cap) stream_store(rows + r * nv + v, d);
+      if (r >= 0 && r < cap) row_store<kStream>(rows + r * nv + v, d);
     }
   }
 }
@@ -170,7 +170,7 @@ __global__ __launch_bounds__(kThreads) void permute_kernel(
 constexpr int kSlots = 4;   // rows in flight per lane (8: 98 us for 89 at 32768 rows of 7168)
 
 // out[t] = sum_k w[t][k] rows[inv_pos[t*K + k]] (+ shared[t]); w null: ones.
-template <class SR, class SS, class SO, int kLanes>
+template <class SR, class SS, class SO, int kLanes, bool kStream>
 __global__ __launch_bounds__(kThreads) void unpermute_kernel(
     const u32x4* __restrict__ rows, const float* __restrict__ w,
     const typename SS::T* __restrict__ shared, uint32_t T, int K, int nv, uint32_t chunks,
@@ -197,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(
           const int64_t r = pos[k0 + j];
           wk[j] = w ? w[(int64_t)t * K + k0 + j] : 1.0f;
           use[j] = r >= 0 && r < cap && wk[j] != 0.0f;
-          if (use[j]) d[j] = stream_load(rows + r * nv + v);
+          if (use[j]) d[j] = row_load<kStream>(rows + r * nv + v);
         }
       }
 #pragma unroll
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_kernel(
 // = t*K + k, a unit each: dout's row is read K times over, from the caches.  A
 // lane reads an element of rows before it writes that of drows (they may be one
 // buffer).
-template <class S, int kLanes>
+template <class S, int kLanes, bool kStream>
 __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
     const u32x4* __restrict__ dout, const u32x4* rows, const float* __restrict__ w,
     uint32_t pairs, int K, int nv, uint32_t groups, const int32_t* __restrict__ inv_pos,
@@ -255,7 +255,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
         for (int i = 0; i < kSteps; ++i)
           if (v0 + i * kLanes < nv) {
             dg[i] = g0[v0 + i * kLanes];
-            if (dw) dv[i] = stream_load(rows + r0 + v0 + i * kLanes);
+            if (dw) dv[i] = row_load<kStream>(rows + r0 + v0 + i * kLanes);
           }
 #pragma unroll
         for (int i = 0; i < kSteps; ++i)
@@ -270,7 +270,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
             if (drows) {
 #pragma unroll
               for (int j = 0; j < N; ++j) g[j] *= wk;
-              stream_store(drows + r0 + v0 + i * kLanes, pack<S>(g));
+              row_store<true>(drows + r0 + v0 + i * kLanes, pack<S>(g));
             }
           }
       }
@@ -333,6 +333,24 @@ constexpr int64_t kMaxGrid = 1 << 20;   // workgroups; the kernels loop past it
 
 unsigned grid_of(int64_t groups) { return (unsigned)(groups < kMaxGrid ? groups : kMaxGrid); }
 
+// When rows go past the caches.  Loads: where the pairs' rows are more than 96 MB,
+// of which a last-level cache of 256 MB keeps little until they are read (MI355X, sums
+// over 8 rows of 3584 a token: 1024 tokens, 59 MB, cached 11.5 us, past the caches
+// 12.2; 2048 tokens 29.4 and 25.1).  Stores of the tokens' copies: where rows are whole
+// 128-byte lines, since a line that two rows share is otherwise written twice in part
+// (16384 tokens to 8 rows of 1024 bf16 each: cached 62 us, past the caches 53; of 1032
+// 79 and 94).  Stores of the gradients, whose rows each wavefront also reads: always (8
+// rows of 1024 a token, 16384 tokens: cached 116 us, so 104; of 1032, 4096 tokens 38
+// and 30).
+bool many(int64_t pairs, int nv) { return pairs * nv > (int64_t)96 << 16; }
+bool whole_lines(int nv) { return nv % 8 == 0; }
+
+template <class F>
+void with_flag(bool flag, F f) {
+  if (flag) f(std::integral_constant<bool, true>());
+  else f(std::integral_constant<bool, false>());
+}
+
 // f(lanes): the lanes of a unit as a constant, for rows of nv vectors.
 template <class F>
 hipError_t with_lanes(int nv, F f) {
@@ -369,11 +387,14 @@ hipError_t launch_unpermute_t(const void* rows, const float* w, const void* shar
     constexpr int kLanes = decltype(lanes)::value;
     const int chunks = (nv + kLanes - 1) / kLanes;
     const int64_t groups = groups_of(T * chunks, kLanes);
-    hipLaunchKernelGGL((unpermute_kernel<SR, SS, SO, kLanes>), dim3(grid_of(groups)),
-                       dim3(kThreads), 0, s, static_cast<const u32x4*>(rows), w,
-                       static_cast<const typename SS::T*>(shared), (uint32_t)T, K, nv,
-                       (uint32_t)chunks, (uint32_t)groups, inv_pos, cap,
-                       static_cast<typename SO::T*>(out));
+    with_flag(many(T * K, nv), [&](auto stream) {
+      hipLaunchKernelGGL((unpermute_kernel<SR, SS, SO, kLanes, decltype(stream)::value>),
+                         dim3(grid_of(groups)), dim3(kThreads), 0, s,
+                         static_cast<const u32x4*>(rows), w,
+                         static_cast<const typename SS::T*>(shared), (uint32_t)T, K, nv,
+                         (uint32_t)chunks, (uint32_t)groups, inv_pos, cap,
+                         static_cast<typename SO::T*>(out));
+    });
   });
 }
 
@@ -396,11 +417,13 @@ hipError_t unpermute_backward_t(const void* dout, const void* rows, const float*
   return with_lanes(nv, [&](auto lanes) {
     constexpr int kLanes = decltype(lanes)::value;
     const int64_t groups = groups_of(T * K, kLanes);
-    hipLaunchKernelGGL((unpermute_backward_kernel<S, kLanes>), dim3(grid_of(groups + pads)),
-                       dim3(kThreads), 0, s, static_cast<const u32x4*>(dout),
-                       static_cast<const u32x4*>(rows), w, (uint32_t)(T * K), K, nv,
-                       (uint32_t)groups, rm.inv_pos, cap, static_cast<u32x4*>(drows), dw,
-                       (uint32_t)pads, pad);
+    with_flag(many(T * K, nv), [&](auto stream) {
+      hipLaunchKernelGGL((unpermute_backward_kernel<S, kLanes, decltype(stream)::value>),
+                         dim3(grid_of(groups + pads)), dim3(kThreads), 0, s,
+                         static_cast<const u32x4*>(dout), static_cast<const u32x4*>(rows), w,
+                         (uint32_t)(T * K), K, nv, (uint32_t)groups, rm.inv_pos, cap,
+                         static_cast<u32x4*>(drows), dw, (uint32_t)pads, pad);
+    });
   });
 }
 
@@ -415,10 +438,13 @@ hipError_t launch_permute(const void* x, int dt, int64_t T, int K, int H, const 
     constexpr int kLanes = decltype(lanes)::value;
     const int chunks = (nv + kLanes - 1) / kLanes;
     const int64_t groups = groups_of(T * chunks, kLanes);
-    hipLaunchKernelGGL((permute_kernel<kLanes>), dim3(grid_of(groups + pads)), dim3(kThreads), 0,
-                       s, static_cast<const u32x4*>(x), (uint32_t)T, K, nv, (uint32_t)chunks,
-                       (uint32_t)groups, rm.inv_pos, cap, static_cast<u32x4*>(rows),
-                       (uint32_t)pads, pad);
+    with_flag(whole_lines(nv), [&](auto stream) {
+      hipLaunchKernelGGL((permute_kernel<kLanes, decltype(stream)::value>),
+                         dim3(grid_of(groups + pads)), dim3(kThreads), 0, s,
+                         static_cast<const u32x4*>(x), (uint32_t)T, K, nv, (uint32_t)chunks,
+                         (uint32_t)groups, rm.inv_pos, cap, static_cast<u32x4*>(rows),
+                         (uint32_t)pads, pad);
+    });
   });
 }
 

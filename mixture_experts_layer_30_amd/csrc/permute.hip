@@ -245,7 +245,10 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
     const int64_t r = p < pairs ? inv_pos[p] : -1;
     const bool used = r >= 0 && r < cap;
     const float wk = w && p < pairs ? w[p] : 1.0f;
-    float acc = 0.0f;
+    // one sum per vector in flight: shorter chains of additions, and closer to the product
+    float acc[kSteps];
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) acc[i] = 0.0f;
     if (used) {
       const u32x4* g0 = dout + (int64_t)(p / (uint32_t)K) * nv;
       const int64_t r0 = r * nv;
@@ -265,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
             if (dw) {
               unpack<S>(dv[i], y);
 #pragma unroll
-              for (int j = 0; j < N; ++j) acc = fmaf(g[j], y[j], acc);
+              for (int j = 0; j < N; ++j) acc[i] = fmaf(g[j], y[j], acc[i]);
             }
             if (drows) {
 #pragma unroll
@@ -276,8 +279,12 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
       }
     }
     if (dw) {
-      acc = lanes_sum<kLanes>(acc);
-      if (lane == 0 && p < pairs) dw[p] = acc;
+#pragma unroll
+      for (int i = kSteps / 2; i > 0; i /= 2)
+#pragma unroll
+        for (int j = 0; j < i; ++j) acc[j] += acc[j + i];
+      const float dot = lanes_sum<kLanes>(acc[0]);
+      if (lane == 0 && p < pairs) dw[p] = dot;
     }
   }
 }
@@ -293,7 +300,7 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   for (int64_t t = (int64_t)blockIdx.x * kWaves + wave; t < T; t += (int64_t)gridDim.x * kWaves) {
     int id[kSlotRegs];
-    float g[kSlotRegs], d[kSlotRegs], s = 0.0f;
+    float g[kSlotRegs], d[kSlotRegs];
 #pragma unroll
     for (int j = 0; j < kSlotRegs; ++j) {
       const int k = j * kWave + lane;
@@ -305,11 +312,16 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
         id[j] = -1;
         g[j] = d[j] = 0.0f;
       }
-      s = fmaf(g[j], d[j], s);
     }
-    s = wave_sum(s);
+    // in 64 bits: with one weight near 1, its dw less the sum is what the others leave
+    double s = 0.0;
 #pragma unroll
-    for (int j = 0; j < kSlotRegs; ++j) g[j] *= d[j] - s;
+    for (int j = 0; j < kSlotRegs; ++j)
+      for (int l = 0; l < kWave && j * kWave + l < K; ++l)
+        s = fma((double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(g[j]), l)),
+                (double)__int_as_float(__builtin_amdgcn_readlane(__float_as_int(d[j]), l)), s);
+#pragma unroll
+    for (int j = 0; j < kSlotRegs; ++j) g[j] = (float)((double)g[j] * ((double)d[j] - s));
     float o[kOutRegs];
 #pragma unroll
     for (int i = 0; i < kOutRegs; ++i) o[i] = 0.0f;

@@ -228,6 +228,18 @@ def test_route_backward_sums_an_expert_listed_twice():
     close(o, ref, 12 * E24 * mag)
 
 
+def test_route_backward_next_to_a_weight_of_one():
+    """One expert's weight 1 - 2^-20: its gradient is the small rest of two near-equal numbers,
+    right to its own rounding and not to that of the numbers."""
+    ids = torch.tensor([[2, 0]], dtype=torch.int32, device=DEV)
+    w = torch.tensor([[1 - 2.0 ** -20, 2.0 ** -20]], device=DEV)
+    dw = torch.tensor([[1.2345678, -0.7654321]], device=DEV)
+    o = torch.empty(1, 3, device=DEV)
+    B.moe_route_backward(ids, w, dw, o)
+    ref, _ = softmax_grad(ids, w, dw, 3)
+    close(o, ref, 2 * 2.0 ** -52 * (w * dw).double().abs().sum())
+
+
 def test_route_backward_against_differences():
     """The gradient of sum(c * weights) along a direction, against the central
     difference of the routing weights' definition (fixed experts) in 64 bits."""

@@ -135,10 +135,10 @@ def _check(status):
 
 
 def _dt(t):
-    if t.dtype == torch.float32:
-        return MOE_F32
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return MOE_BF16
+    if t.dtype is torch.float32:
+        return MOE_F32
     raise MoEError(MOE_EUNSUPPORTED, f"dtype {t.dtype}")
 
 
@@ -385,9 +385,11 @@ class Norm:
         self._ref = ctypes.byref(self._c)
 
     def ref(self):
-        c = self._c
-        c.kind, c.eps = self.kind, self.eps
-        c.weight, c.bias = _addr(self.weight), _addr(self.bias)
+        c, w, b = self._c, self.weight, self.bias
+        c.kind = self.kind
+        c.eps = self.eps
+        c.weight = None if w is None else w.data_ptr()
+        c.bias = None if b is None else b.data_ptr()
         return self._ref
 
 
@@ -401,33 +403,37 @@ class Gate:
         self._ref = ctypes.byref(self._c)
 
     def ref(self):
-        c = self._c
-        c.alpha, c.channel, c.token = self.alpha, _addr(self.channel), _addr(self.token)
+        c, ch, tok = self._c, self.channel, self.token
+        c.alpha = self.alpha
+        c.channel = None if ch is None else ch.data_ptr()
+        c.token = None if tok is None else tok.data_ptr()
         return self._ref
 
 
-def _param(t, H, dt, device, what):
-    """Checks a parameter (None: absent) against those before it, of type dt; the type since."""
-    if t is None:
-        return dt
-    _shaped(t, (H,), what)
-    if dt is not None and t.dtype is not dt:
-        raise MoEError(MOE_EUNSUPPORTED, f"parameters of {dt} and {t.dtype} in one call")
+def _param(t, shape, dt, device, what):
+    """Checks a parameter against those before it, of type dt (None: any); returns its type."""
+    dtype = t.dtype
+    if t.shape != shape or not t.is_contiguous():
+        _shaped(t, shape, what)
+    if dt is not None and dtype is not dt:
+        raise MoEError(MOE_EUNSUPPORTED, f"parameters of {dt} and {dtype} in one call")
     if t.get_device() != device:
         _refuse(f"{what} on {t.device}, the tokens on another")
-    return t.dtype
+    return dtype
 
 
 def _params(T, H, device, norm, gate=None, next_norm=None):
     """Checks the parameters of a call; returns their type."""
-    dt = None
-    if norm is not None:
-        dt = _param(norm.bias, H, _param(norm.weight, H, dt, device, "weight"), device, "bias")
-    if next_norm is not None:
-        dt = _param(next_norm.bias, H, _param(next_norm.weight, H, dt, device, "weight"), device,
-                    "bias")
+    dt, shape = None, (H,)
+    for n in (norm, next_norm):
+        if n is not None:
+            if n.weight is not None:
+                dt = _param(n.weight, shape, dt, device, "weight")
+            if n.bias is not None:
+                dt = _param(n.bias, shape, dt, device, "bias")
     if gate is not None:
-        dt = _param(gate.channel, H, dt, device, "channel")
+        if gate.channel is not None:
+            dt = _param(gate.channel, shape, dt, device, "channel")
         if gate.token is not None:
             _shaped(gate.token, (T,), "token", torch.float32)
             if gate.token.get_device() != device:

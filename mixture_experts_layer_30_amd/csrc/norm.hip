@@ -456,7 +456,10 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
   const bool bias_sum = dtoken && n.bias;
   // (16 elements a lane leave no registers for the next row's)
   constexpr bool kAhead = N * V <= 8;
-  float s1[V][N], s0[kSum0 ? V : 1][N], f[V][N];
+  // channel bias, which every row of a token gradient takes: loaded with each row 31.4
+  // us instead of 28.7 (4099 x 3584, layer norm, all gates)
+  constexpr bool kHeld = kSum0 && kAhead;
+  float s1[V][N], s0[kSum0 ? V : 1][N], f[V][N], cb[kHeld ? V : 1][N];
   Part<SV, L> rv, rr;
   Part<SE, L> re;
   auto fetch = [&](int64_t t) {
@@ -466,18 +469,21 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
   };
   if (kAhead) fetch(blockIdx.x);
   {
-    Part<SP, L> pw, pc;
+    Part<SP, L> pw, pb, pc;
     pw.param(n.weight, 1.0f, sl);
+    if (kHeld) pb.param(n.bias, 0.0f, sl);
     pc.param(gate.channel, 1.0f, sl);
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
       for (int q = 0; q < N / 4; ++q) {
-        float w[4], c[4];
+        float w[4], b[4], c[4];
         pw.q[j].get4(q, w);
+        if (kHeld) pb.q[j].get4(q, b);
         pc.q[j].get4(q, c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          if (kHeld) cb[j][4 * q + i] = c[i] * b[i];
           f[j][4 * q + i] = w[i] * c[i];
           s1[j][4 * q + i] = 0.0f;
           if (kSum0) s0[j][4 * q + i] = 0.0f;
@@ -522,7 +528,14 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
         s[1] = fmaf(d[i] * f[j][4 * q + i], x[i], s[1]);
       }
     });
-    if (bias_sum) {
+    if (bias_sum && kHeld) {
+      each4<L>([&](int j, int q) {
+        float d[4];
+        ce.q[j].get4(q, d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[3] = fmaf(d[i], cb[j][4 * q + i], s[3]);
+      });
+    } else if (bias_sum) {
       Part<SP, L> pb, pc;
       pb.param(n.bias, 0.0f, sl);
       pc.param(gate.channel, 1.0f, sl);

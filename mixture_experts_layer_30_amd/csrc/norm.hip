@@ -130,15 +130,13 @@ __device__ __forceinline__ void put(Row r, uint32_t h, const float* v) {
   }
 }
 
-// What a lane holds of a row: kV vectors of kN elements, a workgroup's lanes
-// apart; vector j starts at h(j).
+// What a lane, one of `lanes`, holds of a row: kV vectors of kN elements, `lanes`
+// vectors apart; vector j starts at h(j).
 template <int kN, int kV>
 struct Slice {
   static constexpr int N = kN, V = kV;
-  uint32_t H;
-  __device__ __forceinline__ uint32_t h(int j) const {
-    return (threadIdx.x + j * blockDim.x) * N;
-  }
+  uint32_t H, lane, lanes;
+  __device__ __forceinline__ uint32_t h(int j) const { return (lane + j * lanes) * N; }
   __device__ __forceinline__ bool in(int j) const { return h(j) < H; }
 };
 
@@ -188,13 +186,13 @@ __device__ __forceinline__ float wave_sum_last(float v) {
   return v;
 }
 
-// Sums of kN <= 4 values over the workgroup's `waves` wavefronts, in every lane.
-// Each wavefront leaves its sums in buf, one row of 16 per value; every wavefront
-// then adds up the rows, value i's on its lanes 16 i .. 16 i + 15.  Consecutive
-// calls alternate between two buffers (a wavefront may still read the last call's
-// while another is in the next).
+// Sums of kN <= 4 values over the row's `waves` wavefronts, the workgroup's from
+// `first` on, in every lane.  Each wavefront leaves its sums in buf, one row of 16
+// per value; every wavefront then adds up its part of the rows, value i's on its
+// lanes 16 i .. 16 i + 15.  Consecutive calls alternate between two buffers (a
+// wavefront may still read the last call's while another is in the next).
 template <int kN>
-__device__ __forceinline__ void block_sum(float (&v)[kN], int waves, float* buf) {
+__device__ __forceinline__ void block_sum(float (&v)[kN], int waves, float* buf, int first = 0) {
   const int lane = threadIdx.x & (kWave - 1);
 #pragma unroll
   for (int i = 0; i < kN; ++i) v[i] = wave_sum_last(v[i]);
@@ -209,7 +207,8 @@ __device__ __forceinline__ void block_sum(float (&v)[kN], int waves, float* buf)
     for (int i = 0; i < kN; ++i) buf[i * kMaxWaves + threadIdx.x / kWave] = v[i];
   }
   __syncthreads();
-  float s = lane < kN * kMaxWaves && lane % kMaxWaves < waves ? buf[lane] : 0.0f;
+  const uint32_t col = (uint32_t)(lane % kMaxWaves - first);
+  float s = lane < kN * kMaxWaves && col < (uint32_t)waves ? buf[lane] : 0.0f;
   s = dpp_add<kQuadXor1>(s);
   s = dpp_add<kQuadXor2>(s);
   s = dpp_add<kRowHalfMirror>(s);
@@ -298,7 +297,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(const void* x, int64_t T, in
   __shared__ float sums[2][kMaxWaves];
   SumBuffers<1> buf{sums, 0};
   const int waves = blockDim.x / kWave;
-  const L sl{(uint32_t)H};
+  const L sl{(uint32_t)H, threadIdx.x, blockDim.x};
   const uint32_t xb = H * SX::kBytes;
   const float inv_h = 1.0f / (float)H;
   Part<SX, L> rx;
@@ -326,7 +325,7 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
   __shared__ float sums[2][kMaxWaves];
   SumBuffers<1> buf{sums, 0};
   const int waves = blockDim.x / kWave;
-  const L sl{(uint32_t)H};
+  const L sl{(uint32_t)H, threadIdx.x, blockDim.x};
   const uint32_t xb = H * SX::kBytes, yb = H * SY::kBytes, sb = H * SS::kBytes;
   const float inv_h = 1.0f / (float)H;
   Part<SX, L> rx;
@@ -436,20 +435,25 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
 // and down the columns only two sums are needed,
 //   S1 = sum_t a e xh,  S0 = sum_t a e:
 //   dweight = channel S1,  dbias = channel S0,  dchannel = weight S1 + bias S0.
-// Partial sums of this workgroup's rows go to part1, part0 [gridDim.x][H] where
-// given.  One reduction a row (the sums are of the centred row), two for a layer
-// norm.  The norm before a block is the case without gates, with dres.
+// A workgroup takes `rows` rows at a time, each on `waves` wavefronts, and adds their
+// sums up at the end; the partial sums go to part1, part0 [gridDim.x][H] where given.
+// One reduction a row (the sums are of the centred row), two for a layer norm.  The
+// norm before a block is the case without gates, with dres.
 template <class SE, class SV, class SP, class L, bool kDres, bool kSum0>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(
-    const void* e, const void* v, const void* dres, int64_t T, int H, NormSpec n, GateSpec gate,
-    void* dv, float* part1, float* part0, float* __restrict__ dtoken) {
+    const void* e, const void* v, const void* dres, int64_t T, int H, int waves, int rows,
+    NormSpec n, GateSpec gate, void* dv, float* part1, float* part0, float* __restrict__ dtoken) {
   constexpr int N = L::N, V = L::V;
   __shared__ float sums4[2][kMaxWaves * 4];
   __shared__ float sums1[2][kMaxWaves];
   SumBuffers<4> buf{sums4, 0};
   SumBuffers<1> buf1{sums1, 0};
-  const int waves = blockDim.x / kWave;
-  const L sl{(uint32_t)H};
+  extern __shared__ f32x4 staged[];
+  // the row of the workgroup's `rows` at a time that this wavefront works on
+  const int row = rows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWave / waves) : 0;
+  const int first = row * waves;
+  const L sl{(uint32_t)H, threadIdx.x - first * kWave, (uint32_t)waves * kWave};
+  const int64_t step = (int64_t)gridDim.x * rows;
   const uint32_t vb = H * SV::kBytes, eb = H * SE::kBytes;
   const float inv_h = 1.0f / (float)H;
   const bool layer = n.kind == kNormLayer;
@@ -462,12 +466,22 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
   float s1[V][N], s0[kSum0 ? V : 1][N], f[V][N], cb[kHeld ? V : 1][N];
   Part<SV, L> rv, rr;
   Part<SE, L> re;
-  auto fetch = [&](int64_t t) {
-    rv.template load<kCached>(row_at(v, t, vb), sl);
-    re.template load<kCached>(row_at(e, t, eb), sl);
-    if (kDres) rr.template load<kCached>(row_at(dres, t, vb), sl);
+  // (rows past the last: of no bytes, they read zeros and store nothing)
+  auto at = [&](const void* p, int64_t t, uint32_t bytes) {
+    return t < T ? row_at(p, t, bytes) : row_at(nullptr, 0, 0);
   };
-  if (kAhead) fetch(blockIdx.x);
+  // The token's gate comes with the row: loaded after the next row's loads, it waits
+  // for them (8192 x 3584, layer norm, all gates, 45.2 us instead of 43.1).
+  float token = 0.0f;
+  auto fetch = [&](int64_t t) {
+    if (gate.token)
+      token = __int_as_float(
+          __builtin_amdgcn_raw_buffer_load_b32(at(gate.token, t, 4), 0, 0, kCached));
+    rv.template load<kCached>(at(v, t, vb), sl);
+    re.template load<kCached>(at(e, t, eb), sl);
+    if (kDres) rr.template load<kCached>(at(dres, t, vb), sl);
+  };
+  if (kAhead) fetch((int64_t)blockIdx.x * rows + row);
   {
     Part<SP, L> pw, pb, pc;
     pw.param(n.weight, 1.0f, sl);
@@ -490,12 +504,18 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
         }
       }
   }
-  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+  // vmcnt(0), once: with loads from before the loop still open, the wait for a row in
+  // the loop has to cover both ways into it, and takes the last row's stores too (that
+  // size 51.9 us instead of 43.7).
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  for (int64_t t0 = (int64_t)blockIdx.x * rows; t0 < T; t0 += step) {
+    const int64_t t = t0 + row;
+    const bool live = t < T;
     if (!kAhead) fetch(t);
     Part<SV, L> cv = rv, cr = rr;
     Part<SE, L> ce = re;
-    if (kAhead && t + gridDim.x < T) fetch(t + gridDim.x);
-    const float a = gate.token ? gate.alpha * gate.token[t] : gate.alpha;
+    const float a = !live ? 0.0f : gate.token ? gate.alpha * token : gate.alpha;
+    if (kAhead && t0 + step < T) fetch(t + step);
     float mean = 0.0f;
     if (layer) {
       float m[1] = {0.0f};
@@ -505,7 +525,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
         m[0] += (x[0] + x[1]) + (x[2] + x[3]);
       });
       cv.keep();
-      block_sum<1>(m, waves, buf1.take());
+      block_sum<1>(m, waves, buf1.take(), first);
       mean = m[0] * inv_h;
     }
     // of the centred squares, g times the centred row, g, and e channel bias
@@ -550,15 +570,16 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
     }
     cv.keep();
     ce.keep();
-    block_sum<4>(s, waves, buf.take());
-    const float rstd = n.kind != kNormNone ? rsqrtf(fmaf(s[0], inv_h, n.eps)) : 1.0f;
-    if (dtoken && threadIdx.x == 0) dtoken[t] = gate.alpha * fmaf(s[1], rstd, s[3]);
+    block_sum<4>(s, waves, buf.take(), first);
+    const float rstd =
+        n.kind == kNormNone ? 1.0f : live ? rsqrtf(fmaf(s[0], inv_h, n.eps)) : 0.0f;
+    if (dtoken && live && sl.lane == 0) dtoken[t] = gate.alpha * fmaf(s[1], rstd, s[3]);
     // dv = (ar e) f - ag - ((x - mean) rstd) agx  (rstd by itself: its cube overflows
     // for rows as small as 1e-13)
     const float ar = a * rstd;
     const float agx = n.kind != kNormNone ? ar * (rstd * (s[1] * inv_h)) : 0.0f;
     const float ag = layer ? ar * (s[2] * inv_h) : 0.0f;
-    const Row out = row_at(dv, t, vb);
+    const Row out = at(dv, t, vb);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
       float o[N];
@@ -595,6 +616,29 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
       }
       put<SV, N, kStreamed>(out, sl.h(j), o);
     }
+  }
+  // The rows' sums into those of the first: its wavefronts add the others' in order.
+  auto join = [&](float (&s)[V][N]) {
+    if (row > 0)
+      each4<L>([&](int j, int q) {
+        const float* p = &s[j][4 * q];
+        staged[((row - 1) * (V * N / 4) + j * (N / 4) + q) * sl.lanes + sl.lane] =
+            f32x4{p[0], p[1], p[2], p[3]};
+      });
+    __syncthreads();
+    if (row == 0)
+      for (int r = 1; r < rows; ++r)
+        each4<L>([&](int j, int q) {
+          const f32x4 d = staged[((r - 1) * (V * N / 4) + j * (N / 4) + q) * sl.lanes + sl.lane];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[j][4 * q + i] += d[i];
+        });
+    __syncthreads();
+  };
+  if (rows > 1) {
+    if (part1) join(s1);
+    if constexpr (kSum0) join(s0);
+    if (row > 0) return;
   }
   const Row r1 = row_at(part1, blockIdx.x, H * 4), r0 = row_at(part0, blockIdx.x, H * 4);
 #pragma unroll
@@ -691,17 +735,30 @@ unsigned forward_groups(int64_t T, int threads, int per_cu) {
   return (unsigned)(T < most ? T : most);
 }
 
-// Workgroups of a backward launch: each writes a row of partial sums per
-// parameter, so it takes 8 rows or more once there are 256 of them (4099 x 3584: 8
-// rows 32 us, 16 rows 39), and no more than two a CU, or 16 wavefronts of them (16384
-// x 128: 4 rows a workgroup 18.6 us, 8 rows 15.2).
-int backward_groups(int64_t T, int H) {
-  const int waves = threads_for(H, lane_elements(H)) / kWave;
-  const int64_t most = lane_elements(H) > 8 ? 256 : 256 * (waves < 8 ? 16 / waves : 2);
-  int64_t g = T / 8;
-  if (g > most) g = most;
-  if (g < 256) g = 256;
-  return (int)(g < T ? g : T);
+// A backward launch: `groups` workgroups of `rows` rows at a time, `waves` wavefronts
+// each.
+struct BackwardShape {
+  int waves, rows, groups;
+};
+
+// Each workgroup writes a row of partial sums per parameter, so there are few and
+// large ones: 16 wavefronts a CU, its registers' worth, in one workgroup of as many
+// rows as they hold, no more than give every CU one (16384 x 128 11.6 us, a workgroup
+// to each row and 16 wavefronts of them a CU 14.4; 16384 x 1024 20.8, so 25.2; 16384 x
+// 4096 75.5, so 77.9; 4099 x 3584, layer norm and all gates, 26.2, so 25.8).  Rows of
+// more than 8 wavefronts: a workgroup to each, 8 rows or more once there are 256 of
+// them, two a CU where the lanes hold 8 elements.
+BackwardShape backward_shape(int64_t T, int H) {
+  const int elements = lane_elements(H), waves = threads_for(H, elements) / kWave;
+  const int64_t each = (T + 255) / 256;
+  int64_t rows = kMaxWaves / waves, groups = 256;
+  if (rows > each) rows = each > 1 ? each : 1;
+  if (waves > kMaxWaves / 2) {
+    const int64_t most = elements > 8 ? 256 : 512;
+    if (T / 8 > groups) groups = T / 8 < most ? T / 8 : most;
+  }
+  const int64_t turns = (T + rows - 1) / rows;
+  return {waves, (int)rows, (int)(turns < groups ? turns : groups)};
 }
 
 // f(a, b, c, layout): the types and how a lane's `elements` lie -- vectors of 16
@@ -731,7 +788,7 @@ hipError_t with_types(int a, int b, int c, int elements, F f) {
 }  // namespace
 
 int64_t norm_workspace_floats(int64_t T, int H) {
-  return 2 * (int64_t)backward_groups(T, H) * H;
+  return 2 * (int64_t)backward_shape(T, H).groups * H;
 }
 
 hipError_t launch_norm(const void* x, int xdt, int64_t T, int H, const NormSpec& n, int pdt,
@@ -784,8 +841,10 @@ hipError_t launch_norm_backward(const void* e, int edt, const void* v, int vdt, 
                                 int64_t T, int H, const NormSpec& n, const GateSpec& gate, int pdt,
                                 void* dv, float* dweight, float* dbias, float* dchannel,
                                 float* dtoken, float* workspace, hipStream_t s) {
-  const int G = backward_groups(T, H);
+  const BackwardShape shape = backward_shape(T, H);
+  const int G = shape.groups, threads = shape.waves * shape.rows * kWave;
   const int elements = lane_elements(H);
+  const int staged = (threads - shape.waves * kWave) * elements * 4;
   ParamGrads p{nullptr, nullptr, n.weight, n.bias, gate.channel, dweight, dbias, dchannel};
   float* part1 = dweight || dchannel ? workspace : nullptr;
   float* part0 = dbias || (dchannel && n.bias) ? workspace + (int64_t)G * H : nullptr;
@@ -794,8 +853,8 @@ hipError_t launch_norm_backward(const void* e, int edt, const void* v, int vdt, 
   if (T > 0) {
     const hipError_t st = with_types(edt, vdt, pdt, elements, [&](auto se, auto sv, auto sp, auto layout) {
       auto go = [&](auto kernel) {
-        hipLaunchKernelGGL(kernel, dim3(G), dim3(threads_for(H, elements)), 0, s, e, v, dres, T, H, n, gate,
-                           dv, part1, part0, dtoken);
+        hipLaunchKernelGGL(kernel, dim3(G), dim3(threads), staged, s, e, v, dres, T, H, shape.waves,
+                           shape.rows, n, gate, dv, part1, part0, dtoken);
       };
       typedef decltype(se) SE;
       typedef decltype(sv) SV;

@@ -935,3 +935,49 @@ def test_block_pass_captured_in_a_graph():
         other.forward(xs[0])
         torch.cuda.synchronize()
         assert torch.equal(r, want[i][0]) and torch.equal(n, want[i][1]), i
+
+
+@pytest.mark.parametrize("kind", [B.NORM_RMS, B.NORM_LAYER, B.NORM_NONE])
+@pytest.mark.parametrize("T,H", [(257, 8), (515, 520), (4099, 512), (769, 1032), (1025, 2048),
+                                 (300, 3584), (4100, 128), (641, 4096)])
+def test_gradients_of_rows_taken_together(T, H, kind):
+    """Several rows to a workgroup, and a last turn that has too few: without eps, so that a
+    row that is not there would turn up in the sums as a NaN."""
+    g = gen(T + H + 31)
+    y, dr, dres = (randn(g, T, H, dt="bf16") for _ in range(3))
+    w, b, c = (randn(g, H, mean=1.0) for _ in range(3))
+    none = kind == B.NORM_NONE
+    post = B.Norm(kind, 0.0, None if none else w, None if none else b)
+    gate = B.Gate(0.75, c, randn(g, T))
+    dy = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    ws = torch.full((B.moe_norm_workspace_bytes(T, H),), 255, dtype=torch.uint8, device=DEV)
+    nan = lambda *s: torch.full(s, float("nan"), device=DEV)  # noqa: E731
+    dw, db = (None, None) if none else (nan(H), nan(H))
+    dc, dq = nan(H), nan(T)
+    B.moe_norm_residual_backward(dr, y, post, gate, dy, ws, dw, db, dc, dq)
+    ref = reference(y, post)
+    a, ch = gate_factors(gate, T)
+    du = a * ch * dr.double()
+    gw = du * ref.w
+    close(dy, *ref.backward(gw, 4 * E24 * gw.abs()))
+    mag = (ref.xh * ref.w).abs() + ref.b.abs()
+    if not none:
+        close(dw, *columns(du * ref.xh, du.abs() * (ref.e_xh + 4 * E24 * ref.xh.abs())))
+        close(db, *columns(du, 4 * E24 * du.abs()))
+    ad = a * dr.double()
+    err = (ad.abs() * (ref.e_out + 3 * E24 * mag)).sum(0)
+    close(dc, (ad * ref.out).sum(0), err + (tchain(T) + 2) * E24 * (ad.abs() * mag).sum(0))
+    v = 0.75 * ch * dr.double()
+    close(dq, (v * ref.out).sum(1), (v.abs() * (ref.e_out + (hchain(H) + 4) * E24 * mag)).sum(1))
+    if none:
+        return
+    # the norm before a block: its gradient onto the residual's, without a bias
+    pre = B.Norm(kind, 0.0, w)
+    dx, dw2 = torch.empty_like(dy), nan(H)
+    B.moe_norm_backward(dr, y, pre, dx, ws, dweight=dw2, dres=dres)
+    ref = reference(y, pre)
+    d = dr.double()
+    gw = d * ref.w
+    want, err = ref.backward(gw, 4 * E24 * gw.abs())
+    close(dx, want + dres.double(), err + E24 * (want.abs() + dres.double().abs()))
+    close(dw2, *columns(d * ref.xh, d.abs() * (ref.e_xh + 4 * E24 * ref.xh.abs())))

@@ -259,13 +259,15 @@ __device__ __forceinline__ float center_and_rstd(float (&v)[L::V][L::N], const L
   return rsqrtf(fmaf(s[0], inv_h, eps));
 }
 
-// v = v * rstd * weight + bias, element by element; `bias` as the norm has it.
-template <class SP, class L>
+// v = v * rstd * weight + bias, element by element; `bias` as the norm has it, kHeld:
+// loaded already, in pb.
+template <bool kHeld, class SP, class L>
 __device__ __forceinline__ void scale_and_shift(float (&v)[L::V][L::N], const L& sl, float rstd,
-                                                const Part<SP, L>& weight, const void* bias) {
+                                                const Part<SP, L>& weight, const void* bias,
+                                                Part<SP, L>& pb) {
   if (bias) {
-    Part<SP, L> pb;
-    pb.param(bias, 0.0f, sl);
+    if (kHeld) pb.keep();
+    else pb.param(bias, 0.0f, sl);
     each4<L>([&](int j, int q) {
       float w[4], b[4];
       weight.q[j].get4(q, w);
@@ -291,7 +293,7 @@ __device__ __forceinline__ void put_row(void* p, int64_t t, const L& sl,
   for (int j = 0; j < L::V; ++j) put<S, L::N, kStreamed>(r, sl.h(j), v[j]);
 }
 
-template <class SX, class SO, class SP, class L>
+template <class SX, class SO, class SP, class L, bool kHeld>
 __global__ __launch_bounds__(1024) void norm_kernel(const void* x, int64_t T, int H, NormSpec n,
                                                     void* out) {
   __shared__ float sums[2][kMaxWaves];
@@ -301,23 +303,26 @@ __global__ __launch_bounds__(1024) void norm_kernel(const void* x, int64_t T, in
   const uint32_t xb = H * SX::kBytes;
   const float inv_h = 1.0f / (float)H;
   Part<SX, L> rx;
-  Part<SP, L> pw;
+  Part<SP, L> pw, pb;
   rx.template load<kCached>(row_at(x, blockIdx.x, xb), sl);
   pw.param(n.weight, 1.0f, sl);
+  if (kHeld) pb.param(n.bias, 0.0f, sl);
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
     float v[L::V][L::N];
     each4<L>([&](int j, int q) { rx.q[j].get4(q, &v[j][4 * q]); });
     if (t + gridDim.x < T) rx.template load<kCached>(row_at(x, t + gridDim.x, xb), sl);
     pw.keep();
     const float rstd = center_and_rstd(v, sl, n.kind, n.eps, inv_h, waves, buf);
-    scale_and_shift<SP>(v, sl, rstd, pw, n.bias);
+    scale_and_shift<kHeld>(v, sl, rstd, pw, n.bias, pb);
     put_row<SO>(out, t, sl, v);
   }
 }
 
 // r = x + gate * post(y), n = pre(r).  kCombine: y[t] = sum_k w[t][k] y[t*K + k]
-// (+ shared[t]), in slot order as moe_combine sums it.
-template <class SY, class SS, class SX, class SP, class L, bool kCombine>
+// (+ shared[t]), in slot order as moe_combine sums it.  kHeld: biases, channel and the
+// token's gate are loaded ahead of the next row, where otherwise a load in the row's
+// turn, issued after the next row's loads, waits for those too.
+template <class SY, class SS, class SX, class SP, class L, bool kCombine, bool kHeld>
 __global__ __launch_bounds__(1024) void norm_residual_kernel(
     const void* y, const float* __restrict__ w, int K, const void* shared, const void* x,
     int64_t T, int H, NormSpec post, GateSpec gate, void* r, NormSpec pre, void* n) {
@@ -330,20 +335,33 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
   const float inv_h = 1.0f / (float)H;
   Part<SX, L> rx;
   Part<SY, L> ry;
-  Part<SP, L> pw, qw;
+  Part<SP, L> pw, qw, pb, pc, qb;
+  float token = 0.0f;
+  auto fetch_token = [&](int64_t t) {
+    if (kHeld && gate.token)
+      token = __int_as_float(
+          __builtin_amdgcn_raw_buffer_load_b32(row_at(gate.token, t, 4), 0, 0, kCached));
+  };
   if (!kCombine) {
+    fetch_token(blockIdx.x);
     rx.template load<kCached>(row_at(x, blockIdx.x, xb), sl);
     ry.template load<kCached>(row_at(y, blockIdx.x, yb), sl);
   }
   pw.param(post.weight, 1.0f, sl);
   qw.param(pre.weight, 1.0f, sl);
+  if (kHeld) {
+    pb.param(post.bias, 0.0f, sl);
+    pc.param(gate.channel, 1.0f, sl);
+    qb.param(pre.bias, 0.0f, sl);
+  }
   for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
-    float v[V][N];
+    float v[V][N], g = 1.0f;
     Part<SX, L> cx;
     if constexpr (kCombine) {
       // pair rows in flight: 64 bytes a lane
       constexpr int kSlots = N * V * SY::kBytes <= 16 ? 4 : N * V * SY::kBytes <= 32 ? 2 : 1;
       Part<SS, L> rs;
+      fetch_token(t);
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
@@ -378,8 +396,10 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
         });
     } else {
       cx = rx;
+      g = token;
       each4<L>([&](int j, int q) { ry.q[j].get4(q, &v[j][4 * q]); });
       if (t + gridDim.x < T) {
+        fetch_token(t + gridDim.x);
         rx.template load<kCached>(row_at(x, t + gridDim.x, xb), sl);
         ry.template load<kCached>(row_at(y, t + gridDim.x, yb), sl);
       }
@@ -390,11 +410,16 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
         post.kind != kNormNone
             ? center_and_rstd(v, sl, post.kind, post.eps, inv_h, waves, buf)
             : 1.0f;
-    const float a = gate.token ? gate.alpha * gate.token[t] : gate.alpha;
+    const float a =
+        gate.token ? gate.alpha * (!kHeld ? gate.token[t] : kCombine ? token : g) : gate.alpha;
     if (post.bias || gate.channel) {
-      Part<SP, L> pb, pc;
-      pb.param(post.bias, 0.0f, sl);
-      pc.param(gate.channel, 1.0f, sl);
+      if (kHeld) {
+        pb.keep();
+        pc.keep();
+      } else {
+        pb.param(post.bias, 0.0f, sl);
+        pc.param(gate.channel, 1.0f, sl);
+      }
       each4<L>([&](int j, int q) {
         float w4[4], b4[4], c4[4], x4[4];
         pw.q[j].get4(q, w4);
@@ -420,7 +445,7 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
     put_row<SX>(r, t, sl, v);
     if (n) {
       const float rstd2 = center_and_rstd(v, sl, pre.kind, pre.eps, inv_h, waves, buf);
-      scale_and_shift<SP>(v, sl, rstd2, qw, pre.bias);
+      scale_and_shift<kHeld>(v, sl, rstd2, qw, pre.bias, qb);
       put_row<SY>(n, t, sl, v);
     }
   }
@@ -735,6 +760,15 @@ unsigned forward_groups(int64_t T, int threads, int per_cu) {
   return (unsigned)(T < most ? T : most);
 }
 
+// Whether a residual launch has parameters or gates besides the norms' weights: its
+// kernel holds them, or loads them ahead, where the lanes hold 8 elements (8192 x 3584
+// all gates and layer norm 46 us, loaded in each row's turn 57; two layer norms with
+// biases 47, so 59; a token gate 43, so 46).  It has more registers to keep, and those
+// without any take none of it (fp32 stream of 8192 x 4096 94.5 us, so 96).
+bool extras(const NormSpec& post, const GateSpec& gate, const NormSpec& pre) {
+  return post.bias || pre.bias || gate.channel || gate.token;
+}
+
 // A backward launch: `groups` workgroups of `rows` rows at a time, `waves` wavefronts
 // each.
 struct BackwardShape {
@@ -795,9 +829,18 @@ hipError_t launch_norm(const void* x, int xdt, int64_t T, int H, const NormSpec&
                        void* out, int odt, hipStream_t s) {
   const int e = lane_elements(H), threads = threads_for(H, e);
   return with_types(xdt, odt, pdt, e, [&](auto sx, auto so, auto sp, auto layout) {
-    hipLaunchKernelGGL(
-        (norm_kernel<decltype(sx), decltype(so), decltype(sp), decltype(layout)>),
-        dim3(forward_groups(T, threads, 32)), dim3(threads), 0, s, x, T, H, n, out);
+    auto go = [&](auto kernel) {
+      hipLaunchKernelGGL(kernel, dim3(forward_groups(T, threads, 32)), dim3(threads), 0, s, x, T, H,
+                         n, out);
+    };
+    typedef decltype(sx) SX;
+    typedef decltype(so) SO;
+    typedef decltype(sp) SP;
+    typedef decltype(layout) L;
+    // (a bias loaded with each row waits for the next row's: 16384 x 4096 48.2 us, so 50.6)
+    if constexpr (L::N * L::V <= 8)
+      if (n.bias) return go(norm_kernel<SX, SO, SP, L, true>);
+    go(norm_kernel<SX, SO, SP, L, false>);
   });
 }
 
@@ -808,14 +851,31 @@ hipError_t launch_norm_residual(const void* y, int ydt, const void* x, int xdt, 
   // 14 wavefronts of 65 registers do not share one, 7 of 110 do; 8192 rows 97 -> 85
   // us, one row 3.4 -> 3.2).  Up to 4096 that costs as much as it gives (16384 rows of
   // 4096 95 -> 100 us, 1024 rows 7.0 -> 6.4).
-  const int e = ydt == kDtBF16 && xdt == kDtBF16 && H > 4096 ? 16 : lane_elements(H);
+  // Nor with a bias from 8 rows a CU on: the parameters that 8 elements leave room to
+  // hold are worth more there (7168, layer norm, all gates, 8192 rows 97 -> 87 us, 2048
+  // 22.9 -> 21.4, but 1024 12.6 -> 13.2).
+  const bool held = (post.bias || pre.bias) && T >= 8 * 256;
+  const bool half = ydt == kDtBF16 && xdt == kDtBF16 && H > 4096 && !held;
+  const int e = half ? 16 : lane_elements(H);
   const int threads = threads_for(H, e);
+  // With an fp32 stream, rows of 6 to 8 wavefronts and no post layer norm (whose two more
+  // reductions want a second workgroup to run beside), one workgroup a CU: 16384 x 4096,
+  // channel gate, next layer norm 136 us, with two 149; 4 wavefronts a row 37.3, so 36.0.
+  // Without gates or biases two (8192 x 4096 72 us, with one 78).
+  const bool few = xdt == kDtF32 && post.kind != kNormLayer && threads > 5 * kWave;
   return with_types(ydt, xdt, pdt, e, [&](auto sy, auto sx, auto sp, auto layout) {
+    auto go = [&](auto kernel, int per_cu) {
+      hipLaunchKernelGGL(kernel, dim3(forward_groups(T, threads, per_cu)), dim3(threads), 0, s, y,
+                         nullptr, 0, nullptr, x, T, H, post, gate, r, pre, n);
+    };
     typedef decltype(sy) SY;
-    hipLaunchKernelGGL(
-        (norm_residual_kernel<SY, SY, decltype(sx), decltype(sp), decltype(layout), false>),
-        dim3(forward_groups(T, threads, 16)), dim3(threads), 0, s, y, nullptr, 0, nullptr, x, T, H,
-        post, gate, r, pre, n);
+    typedef decltype(sx) SX;
+    typedef decltype(sp) SP;
+    typedef decltype(layout) L;
+    if constexpr (L::N * L::V <= 8)
+      if (extras(post, gate, pre))
+        return go(norm_residual_kernel<SY, SY, SX, SP, L, false, true>, few ? 8 : 16);
+    go(norm_residual_kernel<SY, SY, SX, SP, L, false, false>, 16);
   });
 }
 
@@ -827,10 +887,19 @@ hipError_t launch_combine_norm_residual(const void* y, int ydt, const float* w, 
   const int e = lane_elements(H), threads = threads_for(H, e);
   return with_types(ydt, xdt, pdt, e, [&](auto sy, auto sx, auto sp, auto layout) {
     auto go = [&](auto ss) {
-      hipLaunchKernelGGL((norm_residual_kernel<decltype(sy), decltype(ss), decltype(sx),
-                                               decltype(sp), decltype(layout), true>),
-                         dim3(forward_groups(T, threads, 16)), dim3(threads), 0, s, y, w, K, shared,
-                         x, T, H, post, gate, r, pre, n);
+      auto launch = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(forward_groups(T, threads, 16)), dim3(threads), 0, s, y, w,
+                           K, shared, x, T, H, post, gate, r, pre, n);
+      };
+      typedef decltype(sy) SY;
+      typedef decltype(ss) SS;
+      typedef decltype(sx) SX;
+      typedef decltype(sp) SP;
+      typedef decltype(layout) L;
+      if constexpr (L::N * L::V <= 8)
+        if (extras(post, gate, pre))
+          return launch(norm_residual_kernel<SY, SS, SX, SP, L, true, true>);
+      launch(norm_residual_kernel<SY, SS, SX, SP, L, true, false>);
     };
     if (sdt == kDtF32) go(F32());
     else go(BF16());

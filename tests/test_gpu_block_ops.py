@@ -981,3 +981,31 @@ def test_gradients_of_rows_taken_together(T, H, kind):
     want, err = ref.backward(gw, 4 * E24 * gw.abs())
     close(dx, want + dres.double(), err + E24 * (want.abs() + dres.double().abs()))
     close(dw2, *columns(d * ref.xh, d.abs() * (ref.e_xh + 4 * E24 * ref.xh.abs())))
+
+
+@pytest.mark.parametrize("kind,pre_kind", [(B.NORM_RMS, B.NORM_RMS), (B.NORM_RMS, B.NORM_LAYER),
+                                           (B.NORM_LAYER, B.NORM_RMS)])
+@pytest.mark.parametrize("T,H,ydt,xdt,pdt", [
+    (4500, 264, "bf16", "bf16", "f32"), (1100, 2048, "bf16", "bf16", "bf16"),
+    (700, 3584, "bf16", "f32", "f32"), (530, 4096, "f32", "f32", "bf16"),
+    (600, 5000, "bf16", "bf16", "f32"), (2050, 5000, "bf16", "bf16", "bf16")])
+def test_gates_and_biases_of_rows_in_turn(T, H, ydt, xdt, pdt, kind, pre_kind):
+    """More rows than workgroups, each with its own gate, from pair rows too."""
+    g = gen(T + H + 41)
+    y, x = stream_rows(g, T, H, ydt, kind), stream_rows(g, T, H, xdt, pre_kind)
+    post, pre = params(g, H, pdt, kind), params(g, H, pdt, pre_kind)
+    gate = gates(g, T, H, pdt, True, True, 0.6)
+    r = torch.full((T, H), float("nan"), dtype=DT[xdt], device=DEV)
+    n = torch.full((T, H), float("nan"), dtype=DT[ydt], device=DEV)
+    B.moe_norm_residual(y, x, post, gate, r, pre=pre, n=n)
+    check_residual(r, n, reference(y, post), x, gate, pre, T)
+    w = torch.rand(T, 2, generator=g, device=DEV)
+    pairs = randn(g, 2 * T, H, dt=ydt)
+    c = torch.empty(T, H, device=DEV)
+    B.moe_combine(pairs, w, c)
+    B.moe_combine_norm_residual(pairs, w, x, post, gate, r, pre=pre, n=n)
+    check_residual(r, n, reference(c, post), x, gate, pre, T)
+    o = torch.full((T, H), float("nan"), dtype=DT[ydt], device=DEV)
+    B.moe_norm(x, pre, o)
+    ref = reference(x, pre)
+    close(o, ref.out, ref.e_out)

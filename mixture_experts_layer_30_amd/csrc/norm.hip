@@ -172,62 +172,59 @@ __device__ __forceinline__ void each4(F f) {
     for (int q = 0; q < L::N / 4; ++q) f(j, q);
 }
 
-// Sum over the wavefront, in its last lane.
-__device__ __forceinline__ float wave_sum_last(float v) {
+// Sum over each row of 16 lanes, in every lane of it.
+__device__ __forceinline__ float lane_row_sum(float v) {
   v = dpp_add<kQuadXor1>(v);
   v = dpp_add<kQuadXor2>(v);
   v = dpp_add<kRowHalfMirror>(v);
-  v = dpp_add<kRowMirror>(v);
-  // row_bcast:15 into rows 1 and 3, row_bcast:31 into rows 2 and 3
-  v += __int_as_float(
-      __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));
-  v += __int_as_float(
-      __builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));
-  return v;
+  return dpp_add<kRowMirror>(v);
 }
 
-// Sums of kN <= 4 values over the row's `waves` wavefronts, the workgroup's from
-// `first` on, in every lane.  Each wavefront leaves its sums in buf, one row of 16
-// per value; every wavefront then adds up its part of the rows, value i's on its
-// lanes 16 i .. 16 i + 15.  Consecutive calls alternate between two buffers (a
-// wavefront may still read the last call's while another is in the next).
-template <int kN>
-__device__ __forceinline__ void block_sum(float (&v)[kN], int waves, float* buf, int first = 0) {
-  const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = wave_sum_last(v[i]);
-  if (waves == 1) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      v[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v[i]), kWave - 1));
-    return;
-  }
-  if (lane == kWave - 1) {
-#pragma unroll
-    for (int i = 0; i < kN; ++i) buf[i * kMaxWaves + threadIdx.x / kWave] = v[i];
-  }
-  __syncthreads();
-  const uint32_t col = (uint32_t)(lane % kMaxWaves - first);
-  float s = lane < kN * kMaxWaves && col < (uint32_t)waves ? buf[lane] : 0.0f;
-  s = dpp_add<kQuadXor1>(s);
-  s = dpp_add<kQuadXor2>(s);
-  s = dpp_add<kRowHalfMirror>(s);
-  s = dpp_add<kRowMirror>(s);
-#pragma unroll
-  for (int i = 0; i < kN; ++i)
-    v[i] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(s), i * kMaxWaves));
+__device__ __forceinline__ float at_lane(float v, int lane) {
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane));
 }
 
-// Two buffers of block_sum, taken in turn.
+// Buffers of block_sum, two taken in turn (a wavefront may still read the last call's
+// while another is in the next).
 template <int kN>
 struct SumBuffers {
-  float (*buf)[kN * kMaxWaves];
+  f32x4 (*buf)[kN * kMaxWaves];
   int next;
-  __device__ __forceinline__ float* take() {
+  __device__ __forceinline__ f32x4* take() {
     next ^= 1;
     return buf[next];
   }
 };
+
+// Sums of kN <= 4 values over the row's `waves` wavefronts, the workgroup's from
+// `first` on, in every lane.  Each row of 16 lanes leaves its sums in buf, four of a
+// wavefront together; every wavefront then adds up its part of them, value i's on its
+// lanes 16 i .. 16 i + 15.  (Sums of whole wavefronts first take six instructions more
+// a value.)
+template <int kN>
+__device__ __forceinline__ void block_sum(float (&v)[kN], int waves, f32x4* buf, int first = 0) {
+  const int lane = threadIdx.x & (kWave - 1);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = lane_row_sum(v[i]);
+  if (waves == 1) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i)
+      v[i] = (at_lane(v[i], 0) + at_lane(v[i], 16)) + (at_lane(v[i], 32) + at_lane(v[i], 48));
+    return;
+  }
+  if (lane % 16 == 0) {
+    float* p = reinterpret_cast<float*>(buf) + threadIdx.x / 16;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) p[i * kMaxWaves * 4] = v[i];
+  }
+  __syncthreads();
+  const uint32_t col = (uint32_t)(lane % kMaxWaves - first);
+  f32x4 q = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (lane < kN * kMaxWaves && col < (uint32_t)waves) q = buf[lane];
+  const float s = lane_row_sum((q[0] + q[1]) + (q[2] + q[3]));
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = at_lane(s, i * kMaxWaves);
+}
 
 // 1 / deviation of the row in v, whose elements past the end are 0; for a layer
 // norm the row's mean is taken from it first.
@@ -296,7 +293,7 @@ __device__ __forceinline__ void put_row(void* p, int64_t t, const L& sl,
 template <class SX, class SO, class SP, class L, bool kHeld>
 __global__ __launch_bounds__(1024) void norm_kernel(const void* x, int64_t T, int H, NormSpec n,
                                                     void* out) {
-  __shared__ float sums[2][kMaxWaves];
+  __shared__ f32x4 sums[2][kMaxWaves];
   SumBuffers<1> buf{sums, 0};
   const int waves = blockDim.x / kWave;
   const L sl{(uint32_t)H, threadIdx.x, blockDim.x};
@@ -327,7 +324,7 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
     const void* y, const float* __restrict__ w, int K, const void* shared, const void* x,
     int64_t T, int H, NormSpec post, GateSpec gate, void* r, NormSpec pre, void* n) {
   constexpr int N = L::N, V = L::V;
-  __shared__ float sums[2][kMaxWaves];
+  __shared__ f32x4 sums[2][kMaxWaves];
   SumBuffers<1> buf{sums, 0};
   const int waves = blockDim.x / kWave;
   const L sl{(uint32_t)H, threadIdx.x, blockDim.x};
@@ -469,8 +466,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
     const void* e, const void* v, const void* dres, int64_t T, int H, int waves, int rows,
     NormSpec n, GateSpec gate, void* dv, float* part1, float* part0, float* __restrict__ dtoken) {
   constexpr int N = L::N, V = L::V;
-  __shared__ float sums4[2][kMaxWaves * 4];
-  __shared__ float sums1[2][kMaxWaves];
+  __shared__ f32x4 sums4[2][kMaxWaves * 4];
+  __shared__ f32x4 sums1[2][kMaxWaves];
   SumBuffers<4> buf{sums4, 0};
   SumBuffers<1> buf1{sums1, 0};
   extern __shared__ f32x4 staged[];
@@ -483,7 +480,9 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
   const float inv_h = 1.0f / (float)H;
   const bool layer = n.kind == kNormLayer;
   const bool bias_sum = dtoken && n.bias;
-  // (16 elements a lane leave no registers for the next row's)
+  // 16 elements a lane leave no registers for the next row's, and none for a row as fp32
+  // values, which are converted anew at each use there (8 elements: 4099 x 3584, layer
+  // norm, all gates, 26.1 us then, 24.1 held; the arithmetic is as much as the loads).
   constexpr bool kAhead = N * V <= 8;
   // channel bias, which every row of a token gradient takes: loaded with each row 31.4
   // us instead of 28.7 (4099 x 3584, layer norm, all gates)
@@ -549,7 +548,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
         cv.q[j].get4(q, x);
         m[0] += (x[0] + x[1]) + (x[2] + x[3]);
       });
-      cv.keep();
+      if (!kAhead) cv.keep();
       block_sum<1>(m, waves, buf1.take(), first);
       mean = m[0] * inv_h;
     }
@@ -593,8 +592,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
         for (int i = 0; i < 4; ++i) s[3] = fmaf(d[i], c[i] * b[i], s[3]);
       });
     }
-    cv.keep();
-    ce.keep();
+    if (!kAhead) cv.keep();
+    if (!kAhead) ce.keep();
     block_sum<4>(s, waves, buf.take(), first);
     const float rstd =
         n.kind == kNormNone ? 1.0f : live ? rsqrtf(fmaf(s[0], inv_h, n.eps)) : 0.0f;

@@ -4,7 +4,7 @@
 #include <math.h>
 #include <stdint.h>
 
-#include "kernels.h"
+#include "block_kernels.h"
 #include "moe_layer.h"
 
 namespace {

@@ -12,6 +12,7 @@
 // HBM-bound: reads T*K*H + T*H elements, writes T*H.
 #include "common.h"
 #include "kernels.h"
+#include "rows.h"
 
 namespace moe {
 

@@ -25,8 +25,9 @@
 // 8192 x 7168 with a gradient that passes by 90 us (5.2 TB/s), the end of a layer
 // pass, combine to next norm, of 128 x 7168 with 8 pair rows a token 6.5 us (8192
 // tokens 212 us, 6.1 TB/s).
+#include "block_kernels.h"
 #include "common.h"
-#include "kernels.h"
+#include "rows.h"
 
 namespace moe {
 

@@ -21,8 +21,9 @@
 // of 65536 rows of 7168 with 16 thousand padding rows 409 us (2.3 GB, 5.7 TB/s).  Units
 // by alignment row, so that the rows are read and written in order and the tokens
 // gathered, run the last one in 470 us.
+#include "block_kernels.h"
 #include "common.h"
-#include "kernels.h"
+#include "rows.h"
 
 namespace moe {
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include "common.h"
+#include "rows.h"
 
 namespace moe {
 

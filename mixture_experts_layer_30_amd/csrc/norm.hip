@@ -822,7 +822,11 @@ hipError_t with_types(int a, int b, int c, int elements, F f) {
 }  // namespace
 
 int64_t norm_workspace_floats(int64_t T, int H) {
-  return 2 * (int64_t)backward_shape(T, H).groups * H;
+  // (a launch of a few more than 256 rows takes half as many workgroups as one of 256:
+  // what is asked for never falls as T grows, so that the largest batch's serves all)
+  const int groups = backward_shape(T, H).groups;
+  const int64_t least = T < 256 ? T : 256;
+  return 2 * (groups > least ? groups : least) * H;
 }
 
 hipError_t launch_norm(const void* x, int xdt, int64_t T, int H, const NormSpec& n, int pdt,

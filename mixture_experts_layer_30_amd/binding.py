@@ -384,6 +384,9 @@ class Norm:
         self._c = moe_norm_params()
         self._ref = ctypes.byref(self._c)
 
+    def __reduce__(self):   # a copy has a struct of its own
+        return type(self), (self.kind, self.eps, self.weight, self.bias)
+
     def ref(self):
         c, w, b = self._c, self.weight, self.bias
         c.kind = self.kind
@@ -401,6 +404,9 @@ class Gate:
         self.alpha, self.channel, self.token = alpha, channel, token
         self._c = moe_gate_params()
         self._ref = ctypes.byref(self._c)
+
+    def __reduce__(self):   # (see Norm)
+        return type(self), (self.alpha, self.channel, self.token)
 
     def ref(self):
         c, ch, tok = self._c, self.channel, self.token

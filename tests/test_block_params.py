@@ -1,0 +1,47 @@
+"""Norm and Gate objects without a GPU: what a call hands to the library."""
+import copy
+import pickle
+
+import torch
+
+from mixture_experts_layer_30_amd import binding as B
+
+
+def held(o):
+    """The C struct that a call with o reads, as plain values."""
+    c = o.ref()._obj
+    return tuple(getattr(c, f) for f, _ in c._fields_)
+
+
+def test_copies_are_norms_and_gates_of_their_own():
+    """A copy changed afterwards, in one call with the first: neither takes the other's values."""
+    a = B.Norm(B.NORM_RMS, 0.25, torch.ones(8))
+    b = copy.copy(a)
+    assert b.weight is a.weight
+    b.kind, b.eps, b.weight, b.bias = B.NORM_LAYER, 0.5, torch.zeros(8), torch.zeros(8)
+    first, second = a.ref()._obj, b.ref()._obj   # (a call makes both before it reads either)
+    assert (first.kind, first.eps, first.weight, first.bias) == (B.NORM_RMS, 0.25, a.weight.data_ptr(), None)
+    assert (second.kind, second.eps, second.weight, second.bias) == \
+        (B.NORM_LAYER, 0.5, b.weight.data_ptr(), b.bias.data_ptr())
+    g = B.Gate(0.75, torch.ones(8), torch.ones(3))
+    h = copy.copy(g)
+    h.alpha, h.channel = 2.0, None
+    first, second = g.ref()._obj, h.ref()._obj
+    assert (first.alpha, first.channel) == (0.75, g.channel.data_ptr())
+    assert (second.alpha, second.channel, second.token) == (2.0, None, g.token.data_ptr())
+
+
+def test_deep_copies_and_pickles():
+    for o in (B.Norm(B.NORM_LAYER, 0.125, torch.arange(8.0), torch.ones(8)),
+              B.Gate(1.5, torch.arange(8.0), torch.ones(3)), B.Norm(), B.Gate()):
+        for c in (copy.deepcopy(o), pickle.loads(pickle.dumps(o))):
+            assert type(c) is type(o)
+            for name, v in vars(o).items():
+                if isinstance(v, torch.Tensor):
+                    w = getattr(c, name)
+                    assert torch.equal(v, w) and v.data_ptr() != w.data_ptr()
+            for field, x, y in zip(o.ref()._obj._fields_, held(o), held(c)):
+                if field[0] in ("kind", "eps", "alpha"):
+                    assert x == y
+                else:
+                    assert (x is None) == (y is None) and (x is None or x != y)

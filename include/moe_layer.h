@@ -394,8 +394,9 @@ moe_status moe_route_backward(const int32_t *topk_ids, const float *topk_w, cons
  *   MOE_NORM_LAYER  norm(v) = (v - mean(v)) * rstd * weight + bias,
  *                   rstd = 1 / sqrt(mean((v - mean(v))^2) + eps)
  *   MOE_NORM_NONE   norm(v) = v (weight and bias must be NULL)
- * weight, bias [H]; NULL: ones, zeros.  Statistics are fp32 (the variance from
- * the centred values); results are rounded once.
+ * weight, bias [H]; NULL: ones, zeros.  Statistics are fp32, a layer norm's from
+ * the centred values, whose own mean, what the first one's rounding left, is
+ * taken off too; results are rounded once.
  */
 typedef enum { MOE_NORM_NONE = 0, MOE_NORM_RMS = 1, MOE_NORM_LAYER = 2 } moe_norm_kind;
 
@@ -446,8 +447,9 @@ typedef struct {
  * (else it may be NULL), with no contents to keep before or after the call;
  * calls that may overlap need one each.  T = 0 writes zeros to those gradients
  * and does nothing else.
- * Squares are summed in fp32: with eps = 0 a row of zeros, or one whose squares
- * underflow, has no norm (NaN), and elements past 1e19 overflow it.
+ * Squares are summed in fp32: with eps = 0 a row of zeros (for a layer norm: of
+ * one value), or one whose squares underflow, has no norm (NaN), and elements past
+ * 1e19 overflow it.
  * Limits: H a multiple of 8, at most 16384; T*H < 2^39.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY (workspace).
  */

@@ -6,9 +6,11 @@
 // registers, so that the statistics, the normed row, the residual sum and the
 // next norm come from one read, and asks for its next row before it works on
 // this one.  Row sums go over the wavefront by lane permutations, then over the
-// wavefronts in order through LDS; a layer norm sums the centred squares in a
-// second pass over the registers, since the difference of the two raw moments
-// loses the variance of a row far from zero.
+// wavefronts in order through LDS.  A layer norm takes a second pass over the
+// registers: an fp32 mean m of a row far from zero is off by a few units in its last
+// place, so the mean d of x - m is summed next to the squares of x - m (one more
+// addition an element), and x - m - d, mean((x - m)^2) - d^2 are used.  What is left
+// of the error goes by the row's deviation and no longer by its mean.
 //
 // Rows are read and written through buffer descriptors of the row's length: a
 // lane past its end reads zeros and writes nothing, and a row that is not there
@@ -173,12 +175,23 @@ __device__ __forceinline__ void each4(F f) {
     for (int q = 0; q < L::N / 4; ++q) f(j, q);
 }
 
-// Sum over each row of 16 lanes, in every lane of it.
-__device__ __forceinline__ float lane_row_sum(float v) {
-  v = dpp_add<kQuadXor1>(v);
-  v = dpp_add<kQuadXor2>(v);
-  v = dpp_add<kRowHalfMirror>(v);
-  return dpp_add<kRowMirror>(v);
+// Sums over each row of 16 lanes, in every lane of it: a step of all kN at a time, since
+// one that takes the step before's result has to wait two cycles for it.
+template <int kN>
+__device__ __forceinline__ void lane_row_sums(float (&v)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = dpp_add<kQuadXor1>(v[i]);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = dpp_add<kQuadXor2>(v[i]);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = dpp_add<kRowHalfMirror>(v[i]);
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = dpp_add<kRowMirror>(v[i]);
+}
+
+// v, the same in every lane, in a scalar register.
+__device__ __forceinline__ float scalar(float v) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(v)));
 }
 
 __device__ __forceinline__ float at_lane(float v, int lane) {
@@ -205,12 +218,12 @@ struct SumBuffers {
 template <int kN>
 __device__ __forceinline__ void block_sum(float (&v)[kN], int waves, f32x4* buf, int first = 0) {
   const int lane = threadIdx.x & (kWave - 1);
-#pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = lane_row_sum(v[i]);
+  lane_row_sums(v);
   if (waves == 1) {
 #pragma unroll
     for (int i = 0; i < kN; ++i)
-      v[i] = (at_lane(v[i], 0) + at_lane(v[i], 16)) + (at_lane(v[i], 32) + at_lane(v[i], 48));
+      v[i] = scalar((at_lane(v[i], 0) + at_lane(v[i], 16)) +
+                    (at_lane(v[i], 32) + at_lane(v[i], 48)));
     return;
   }
   if (lane % 16 == 0) {
@@ -222,9 +235,17 @@ __device__ __forceinline__ void block_sum(float (&v)[kN], int waves, f32x4* buf,
   const uint32_t col = (uint32_t)(lane % kMaxWaves - first);
   f32x4 q = {0.0f, 0.0f, 0.0f, 0.0f};
   if (lane < kN * kMaxWaves && col < (uint32_t)waves) q = buf[lane];
-  const float s = lane_row_sum((q[0] + q[1]) + (q[2] + q[3]));
+  float s[1] = {(q[0] + q[1]) + (q[2] + q[3])};
+  lane_row_sums(s);
 #pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = at_lane(s, i * kMaxWaves);
+  for (int i = 0; i < kN; ++i) v[i] = at_lane(s[0], i * kMaxWaves);
+}
+
+// 1 / deviation, from the mean of the squares of a row less an approximate mean, and the
+// mean that those still have.
+__device__ __forceinline__ float rstd_of(float squares, float inv_h, float eps, float rest) {
+  const float v = fmaf(-rest, rest, fmaf(squares, inv_h, eps));
+  return rsqrtf(v < eps ? eps : v);   // (a NaN stays)
 }
 
 // 1 / deviation of the row in v, whose elements past the end are 0; for a layer
@@ -232,29 +253,44 @@ __device__ __forceinline__ void block_sum(float (&v)[kN], int waves, f32x4* buf,
 template <class L>
 __device__ __forceinline__ float center_and_rstd(float (&v)[L::V][L::N], const L& sl, int kind,
                                                  float eps, float inv_h, int waves,
-                                                 SumBuffers<1>& buf) {
-  if (kind == kNormLayer) {
-    float m[1] = {0.0f};
+                                                 SumBuffers<2>& buf) {
+  auto sum = [&] {
+    float m = 0.0f;
 #pragma unroll
     for (int j = 0; j < L::V; ++j)
 #pragma unroll
-      for (int i = 0; i < L::N; ++i) m[0] += v[j][i];
-    block_sum<1>(m, waves, buf.take());
-    const float mean = m[0] * inv_h;
+      for (int i = 0; i < L::N; ++i) m += v[j][i];
+    return m;
+  };
+  auto squares = [&] {
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < L::V; ++j)
+#pragma unroll
+      for (int i = 0; i < L::N; ++i) s = fmaf(v[j][i], v[j][i], s);
+    return s;
+  };
+  auto take = [&](float mean) {
 #pragma unroll
     for (int j = 0; j < L::V; ++j) {
       const float c = sl.in(j) ? mean : 0.0f;
 #pragma unroll
       for (int i = 0; i < L::N; ++i) v[j][i] -= c;
     }
+  };
+  if (kind == kNormLayer) {
+    float m[1] = {sum()};
+    block_sum<1>(m, waves, buf.take());
+    take(m[0] * inv_h);
+    float s[2] = {squares(), sum()};
+    block_sum<2>(s, waves, buf.take());
+    const float rest = s[1] * inv_h;
+    take(rest);
+    return rstd_of(s[0], inv_h, eps, rest);
   }
-  float s[1] = {0.0f};
-#pragma unroll
-  for (int j = 0; j < L::V; ++j)
-#pragma unroll
-    for (int i = 0; i < L::N; ++i) s[0] = fmaf(v[j][i], v[j][i], s[0]);
+  float s[1] = {squares()};
   block_sum<1>(s, waves, buf.take());
-  return rsqrtf(fmaf(s[0], inv_h, eps));
+  return rstd_of(s[0], inv_h, eps, 0.0f);
 }
 
 // v = v * rstd * weight + bias, element by element; `bias` as the norm has it, kHeld:
@@ -294,8 +330,8 @@ __device__ __forceinline__ void put_row(void* p, int64_t t, const L& sl,
 template <class SX, class SO, class SP, class L, bool kHeld>
 __global__ __launch_bounds__(1024) void norm_kernel(const void* x, int64_t T, int H, NormSpec n,
                                                     void* out) {
-  __shared__ f32x4 sums[2][kMaxWaves];
-  SumBuffers<1> buf{sums, 0};
+  __shared__ f32x4 sums[2][2 * kMaxWaves];
+  SumBuffers<2> buf{sums, 0};
   const int waves = blockDim.x / kWave;
   const L sl{(uint32_t)H, threadIdx.x, blockDim.x};
   const uint32_t xb = H * SX::kBytes;
@@ -325,8 +361,8 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
     const void* y, const float* __restrict__ w, int K, const void* shared, const void* x,
     int64_t T, int H, NormSpec post, GateSpec gate, void* r, NormSpec pre, void* n) {
   constexpr int N = L::N, V = L::V;
-  __shared__ f32x4 sums[2][kMaxWaves];
-  SumBuffers<1> buf{sums, 0};
+  __shared__ f32x4 sums[2][2 * kMaxWaves];
+  SumBuffers<2> buf{sums, 0};
   const int waves = blockDim.x / kWave;
   const L sl{(uint32_t)H, threadIdx.x, blockDim.x};
   const uint32_t xb = H * SX::kBytes, yb = H * SY::kBytes, sb = H * SS::kBytes;
@@ -460,17 +496,16 @@ __global__ __launch_bounds__(1024) void norm_residual_kernel(
 //   dweight = channel S1,  dbias = channel S0,  dchannel = weight S1 + bias S0.
 // A workgroup takes `rows` rows at a time, each on `waves` wavefronts, and adds their
 // sums up at the end; the partial sums go to part1, part0 [gridDim.x][H] where given.
-// One reduction a row (the sums are of the centred row), two for a layer norm.  The
-// norm before a block is the case without gates, with dres.
+// One reduction a row; a layer norm has one before it, of the row and the sums that do
+// not need its mean, and the second's are of the centred row and then of what is left of
+// its mean.  The norm before a block is the case without gates, with dres.
 template <class SE, class SV, class SP, class L, bool kDres, bool kSum0>
 __global__ __launch_bounds__(1024) void norm_backward_kernel(
     const void* e, const void* v, const void* dres, int64_t T, int H, int waves, int rows,
     NormSpec n, GateSpec gate, void* dv, float* part1, float* part0, float* __restrict__ dtoken) {
   constexpr int N = L::N, V = L::V;
-  __shared__ f32x4 sums4[2][kMaxWaves * 4];
-  __shared__ f32x4 sums1[2][kMaxWaves];
-  SumBuffers<4> buf{sums4, 0};
-  SumBuffers<1> buf1{sums1, 0};
+  __shared__ f32x4 sums[2][kMaxWaves * 3];
+  SumBuffers<3> buf{sums, 0};
   extern __shared__ f32x4 staged[];
   // the row of the workgroup's `rows` at a time that this wavefront works on
   const int row = rows > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / kWave / waves) : 0;
@@ -541,44 +576,13 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
     Part<SE, L> ce = re;
     const float a = !live ? 0.0f : gate.token ? gate.alpha * token : gate.alpha;
     if (kAhead && t0 + step < T) fetch(t + step);
-    float mean = 0.0f;
-    if (layer) {
-      float m[1] = {0.0f};
-      each4<L>([&](int j, int q) {
-        float x[4];
-        cv.q[j].get4(q, x);
-        m[0] += (x[0] + x[1]) + (x[2] + x[3]);
-      });
-      if (!kAhead) cv.keep();
-      block_sum<1>(m, waves, buf1.take(), first);
-      mean = m[0] * inv_h;
-    }
-    // of the centred squares, g times the centred row, g, and e channel bias
-    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    each4<L>([&](int j, int q) {
-      float x[4], d[4];
-      cv.q[j].get4(q, x);
-      ce.q[j].get4(q, d);
-      if (layer) {
-        const float c = sl.in(j) ? mean : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          x[i] -= c;
-          s[2] = fmaf(d[i], f[j][4 * q + i], s[2]);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        s[0] = fmaf(x[i], x[i], s[0]);
-        s[1] = fmaf(d[i] * f[j][4 * q + i], x[i], s[1]);
-      }
-    });
+    float eb = 0.0f;   // sum of e channel bias
     if (bias_sum && kHeld) {
       each4<L>([&](int j, int q) {
         float d[4];
         ce.q[j].get4(q, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[3] = fmaf(d[i], cb[j][4 * q + i], s[3]);
+        for (int i = 0; i < 4; ++i) eb = fmaf(d[i], cb[j][4 * q + i], eb);
       });
     } else if (bias_sum) {
       Part<SP, L> pb, pc;
@@ -590,20 +594,75 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
         pc.q[j].get4(q, c);
         ce.q[j].get4(q, d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[3] = fmaf(d[i], c[i] * b[i], s[3]);
+        for (int i = 0; i < 4; ++i) eb = fmaf(d[i], c[i] * b[i], eb);
       });
     }
+    float mean = 0.0f, g_sum = 0.0f;
+    if (layer) {
+      // of the row, g, and e channel bias
+      float m[3] = {0.0f, 0.0f, eb};
+      each4<L>([&](int j, int q) {
+        float x[4], d[4];
+        cv.q[j].get4(q, x);
+        ce.q[j].get4(q, d);
+        m[0] += (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) m[1] = fmaf(d[i], f[j][4 * q + i], m[1]);
+      });
+      if (!kAhead) cv.keep();
+      if (!kAhead) ce.keep();
+      block_sum<3>(m, waves, buf.take(), first);
+      mean = m[0] * inv_h;
+      g_sum = m[1];
+      eb = m[2];
+    }
+    // of the centred squares, g times the centred row, and what the centred row still sums
+    // to, or e channel bias where the row is not centred
+    float s[3] = {0.0f, 0.0f, layer ? 0.0f : eb};
+    float held[kAhead ? V : 1][N];   // the centred row
+    each4<L>([&](int j, int q) {
+      float x[4], d[4];
+      cv.q[j].get4(q, x);
+      ce.q[j].get4(q, d);
+      if (layer) {
+        const float c = sl.in(j) ? mean : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] -= c;
+        s[2] += (x[0] + x[1]) + (x[2] + x[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        s[0] = fmaf(x[i], x[i], s[0]);
+        s[1] = fmaf(d[i] * f[j][4 * q + i], x[i], s[1]);
+        if (kAhead) held[j][4 * q + i] = x[i];
+      }
+    });
     if (!kAhead) cv.keep();
     if (!kAhead) ce.keep();
-    block_sum<4>(s, waves, buf.take(), first);
-    const float rstd =
-        n.kind == kNormNone ? 1.0f : live ? rsqrtf(fmaf(s[0], inv_h, n.eps)) : 0.0f;
-    if (dtoken && live && sl.lane == 0) dtoken[t] = gate.alpha * fmaf(s[1], rstd, s[3]);
-    // dv = (ar e) f - ag - ((x - mean) rstd) agx  (rstd by itself: its cube overflows
+    block_sum<3>(s, waves, buf.take(), first);
+    float rest = 0.0f;
+    if (layer) {
+      rest = s[2] * inv_h;
+      s[1] = fmaf(-rest, g_sum, s[1]);
+    } else {
+      eb = s[2];
+    }
+    const float rstd = n.kind == kNormNone ? 1.0f : live ? rstd_of(s[0], inv_h, n.eps, rest) : 0.0f;
+    if (dtoken && live && sl.lane == 0) dtoken[t] = gate.alpha * fmaf(s[1], rstd, eb);
+    // dv = (ar e) f - ag - ((x - mean - rest) rstd) agx  (rstd by itself: its cube overflows
     // for rows as small as 1e-13)
     const float ar = a * rstd;
     const float agx = n.kind != kNormNone ? ar * (rstd * (s[1] * inv_h)) : 0.0f;
-    const float ag = layer ? ar * (s[2] * inv_h) : 0.0f;
+    const float ag = layer ? ar * (g_sum * inv_h) : 0.0f;
+    // (below four roundings of a normed value of 1 it is not worth the subtractions: layer
+    // norm of 8192 x 7168 78 us, with them in every row 81)
+    if constexpr (kAhead)
+      if (layer && !(fabsf(rest * rstd) <= 0x1p-22f)) {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+          for (int i = 0; i < N; ++i) held[j][i] -= rest;
+      }
     const Row out = at(dv, t, vb);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
@@ -611,7 +670,16 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
 #pragma unroll
       for (int q = 0; q < N / 4; ++q) {
         float x[4], d[4];
-        cv.q[j].get4(q, x);
+        if constexpr (kAhead) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[i] = held[j][4 * q + i];
+        } else {
+          cv.q[j].get4(q, x);
+          if (layer) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[i] = (x[i] - mean) - rest;
+          }
+        }
         ce.q[j].get4(q, d);
         float* oq = o + 4 * q;
         if (kDres) {
@@ -622,10 +690,7 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(
         }
         if (layer) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[i] -= mean;
-            oq[i] -= ag;
-          }
+          for (int i = 0; i < 4; ++i) oq[i] -= ag;
         }
         if (kSum0) {
 #pragma unroll

@@ -1,0 +1,153 @@
+"""The operators around the experts where their arithmetic or their choice of kernel is
+at its edge: rows far from zero, slots of weight zero, no tokens, norms without biases,
+rows that the workgroups take in turn at every width, every subset of the gradients.
+
+Tolerances are bounds on rounding as in test_gpu_block_ops.py, whose helpers are used;
+e = 2^-24 is one fp32 rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+from mixture_experts_layer_30_amd import binding as B
+from test_gpu_block_ops import (DEV, E24, EPS, Ref, close, columns, gate_factors, gates, gen,
+                                params, randn, tchain)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.lib()
+
+
+def workspace(T, H):
+    return torch.full((max(B.moe_norm_workspace_bytes(T, H), 16),), 255, dtype=torch.uint8, device=DEV)
+
+
+def nans(*shape):
+    return torch.full(shape, float("nan"), device=DEV)
+
+
+# ------------------------------------------------------------ rows far from zero
+
+# additions one after the other in a sum over a row: 16 products a lane, 4 across 16
+# lanes, 2 + 4 across the wavefronts; and the product with 1 / H
+C = 28
+
+
+class Far(Ref):
+    """A layer norm of rows whose mean is far larger than their deviation, with a bound on
+    what two passes can do.  A mean m of fp32 sums is off by at most d0 = C e mean|x|.  The
+    centred values x - m and their own mean, at most d0, leave an error of
+    dm = (C + 1) e (mean|x - mean| + d0): what is left goes by the deviation and no longer
+    by the mean, but for the second order C e d0."""
+
+    def __init__(self, x, n):
+        eps = float(np.float32(n.eps))
+        super().__init__(x, n.kind, n.weight, n.bias, eps)
+        x = x.double()
+        c = x - x.mean(1, keepdim=True)
+        d0 = C * E24 * x.abs().mean(1, keepdim=True)
+        dm = (C + 1) * E24 * (c.abs().mean(1, keepdim=True) + d0)
+        # x - m, then less the mean of that: a rounding each
+        e_c = dm + 2 * E24 * (c.abs() + d0)
+        var = (c * c).mean(1, keepdim=True)
+        # the mean of (x - m)^2 is var + d0^2 at most, from which the square of its mean is taken
+        e_var = (C + 6) * E24 * (var + d0 * d0) + 2 * (d0 + dm) * dm
+        assert (e_var <= 0.01 * (var + eps)).all()   # (so the root's error is half of it, and 1%)
+        e_r = 0.51 * e_var / (var + eps) + 4 * E24
+        self.e_xh = self.rstd * e_c + self.xh.abs() * e_r * 1.02
+        self.e_out = self.e_xh * self.w.abs() + 3 * E24 * ((self.xh * self.w).abs() + self.b.abs())
+        # the dot products go over x - m, whose magnitude is that of c and d0
+        self.xm, self.e_r = self.xh.abs() + d0 * self.rstd, e_r
+
+    def backward(self, g, eg):
+        xh = self.xh
+        m = (g * xh).mean(1, keepdim=True)
+        em = (eg * self.xm + g.abs() * self.e_xh).mean(1, keepdim=True) + \
+            (C + 4) * E24 * (g.abs() * self.xm).mean(1, keepdim=True)
+        mg = g.mean(1, keepdim=True)
+        o = g - xh * m - mg
+        e = eg + self.e_xh * m.abs() + self.xm * em + 6 * E24 * (g.abs() + self.xm * m.abs() + mg.abs())
+        e = e + eg.mean(1, keepdim=True) + (C + 4) * E24 * g.abs().mean(1, keepdim=True)
+        return o * self.rstd, self.rstd * (e + (self.e_r + 4 * E24) * o.abs())
+
+
+def far_rows(g, H):
+    """Constant rows, and rows whose mean is 300 to 100 thousand times their deviation."""
+    x = torch.randn(14, H, generator=g, device=DEV)
+    for i, v in enumerate((1000.0, 100.0, -333.3, 1e4, 0.1, 1.0)):
+        x[i] = v
+    for i, v in enumerate((300.0, 1e3, -1e3, 1e4, -3e4, 1e5)):
+        x[6 + i] += v
+    x[12] = x[12] * 1e-3 + 5.0
+    return x
+
+
+@pytest.mark.parametrize("H", [1000, 3584, 7168, 8200, 16384])
+def test_layer_norm_of_rows_far_from_zero(H):
+    g = gen(H + 51)
+    x = far_rows(g, H)
+    T = x.shape[0]
+    for n in (params(g, H, "f32", B.NORM_LAYER), B.Norm(B.NORM_LAYER, EPS)):
+        o = torch.empty_like(x)
+        B.moe_norm(x, n, o)
+        ref = Far(x, n)
+        close(o, ref.out, ref.e_out)
+        # after a block too: gate 1 on a stream of zeros, and before the next, block's output 0
+        zero, r, o2 = torch.zeros_like(x), torch.empty_like(x), torch.empty_like(x)
+        B.moe_norm_residual(x, zero, n, B.Gate(), r)
+        close(r, ref.out, ref.e_out + E24 * ref.out.abs())
+        B.moe_norm_residual(zero, x, B.Norm(B.NORM_NONE), B.Gate(), r, pre=n, n=o2)
+        assert torch.equal(r, x)
+        close(o2, ref.out, ref.e_out)
+        one = torch.ones(T, 1, device=DEV)
+        B.moe_combine_norm_residual(x, one, zero, n, B.Gate(), r)
+        close(r, ref.out, ref.e_out + E24 * ref.out.abs())
+
+
+@pytest.mark.parametrize("H", [1000, 3584, 7168, 8200, 16384])
+def test_layer_norm_gradients_of_rows_far_from_zero(H):
+    g = gen(H + 52)
+    x = far_rows(g, H)
+    T = x.shape[0]
+    n, d = params(g, H, "f32", B.NORM_LAYER), randn(g, T, H)
+    gate = gates(g, T, H, "f32", True, True, 0.5)
+    ref = Far(x, n)
+    dx, dw, db = torch.empty_like(x), nans(H), nans(H)
+    B.moe_norm_backward(d, x, n, dx, workspace(T, H), dweight=dw, dbias=db)
+    gw = d.double() * ref.w
+    close(dx, *ref.backward(gw, E24 * gw.abs()))
+    e1 = ref.e_xh + 4 * E24 * ref.xm
+    close(dw, *columns(d.double() * ref.xh, d.double().abs() * e1))
+    close(db, *columns(d.double(), 0 * gw))
+    dc, dq = nans(H), nans(T)
+    B.moe_norm_residual_backward(d, x, n, gate, dx, workspace(T, H), dw, db, dc, dq)
+    a, c = gate_factors(gate, T)
+    du = a * c * d.double()
+    gw = du * ref.w
+    close(dx, *ref.backward(gw, 4 * E24 * gw.abs()))
+    close(dw, *columns(du * ref.xh, du.abs() * e1))
+    close(db, *columns(du, 4 * E24 * du.abs()))
+    # from two sums each, put together at the end
+    mag = (ref.xm * ref.w).abs() + ref.b.abs()
+    ad = (a * d.double())
+    err = (ad.abs() * (ref.e_out + 4 * E24 * mag)).sum(0) + (tchain(T) + 2) * E24 * (ad.abs() * mag).sum(0)
+    close(dc, (ad * ref.out).sum(0), err)
+    v = 0.5 * c * d.double()
+    close(dq, (v * ref.out).sum(1), (v.abs() * (ref.e_out + (C + 8) * E24 * mag)).sum(1))
+
+
+@pytest.mark.parametrize("H", [264, 3584, 7168])
+def test_layer_norm_of_constant_bf16_rows(H):
+    """Constant rows have the bias for a norm, to half a step of the result."""
+    g = gen(H + 53)
+    x = torch.tensor([3.0, 300.0, -1000.0, 0.1, 0.0], device=DEV)[:, None].expand(5, H).bfloat16().contiguous()
+    n = params(g, H, "bf16", B.NORM_LAYER)
+    o = torch.empty(5, H, device=DEV)
+    B.moe_norm(x, n, o)
+    # Far's bound at no deviation: (C + 3) e d0 / sqrt(eps), d0 = C e 1000, below 4e-6 a weight
+    close(o, n.bias.double()[None].expand(5, H), 4e-6 * n.weight.double().abs()[None])

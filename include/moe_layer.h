@@ -356,7 +356,8 @@ moe_status dense_ffn_fa(const void *x, moe_dtype dt, int64_t T, int H, int I_fa,
  * read their rows, as moe_combine does, so that the two agree bit for bit on
  * the same rows.  topk_w NULL: every weight 1 (dw must then be NULL).  The
  * gradient of `shared` is dout itself.  Either of drows and dw may be NULL;
- * drows may be rows.  dw is fp32, summed over H in a fixed order.  No atomics:
+ * drows may be rows.  The dw of a slot of weight 0 is taken from its row like any
+ * other's (NaN or infinite where that row is).  dw is fp32, summed over H in a fixed order.  No atomics:
  * every result is the same on every run.
  * x, dx [T][H] dt; rows, drows [plan->cap][H] dt / rdt; dout, out [T][H] odt;
  * shared [T][H] sdt; topk_w, dw [T][K] fp32.  dout and rows have the same type.
@@ -381,7 +382,8 @@ moe_status moe_unpermute_backward(const void *dout, const void *rows, moe_dtype 
  * a token's selected logits,
  *   dlogits[t][id_j] = w_j * (dw_j - sum_i w_i dw_i), 0 for experts not selected.
  * topk_ids, topk_w: as routed; a slot with a negative id (unused), or one that
- * is >= E, takes no part.  An expert listed twice gets the sum.
+ * is >= E, takes no part, and neither does one of weight 0, whatever its dw: it
+ * adds 0 to its expert.  An expert listed twice gets the sum.
  * topk_ids [T][K] int32; topk_w, dw [T][K] fp32; dlogits [T][E] fp32 (every
  * element written).  Errors: as moe_route.
  */

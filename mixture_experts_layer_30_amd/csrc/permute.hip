@@ -290,7 +290,9 @@ __global__ __launch_bounds__(kThreads) void unpermute_backward_kernel(
   }
 }
 
-// dlogits[t][e] = sum over the slots j with id e of w_j (dw_j - sum_i w_i dw_i).
+// dlogits[t][e] = sum over the slots j with id e of w_j (dw_j - sum_i w_i dw_i), slots of
+// weight 0 left out of both sums: the way back does not read their rows, so that their
+// dw may be anything.
 // One wavefront a token, its slots held 64 to a register (kSlotRegs of them); each
 // lane owns every 64th expert (kOutRegs) and looks the slots through in order.
 template <int kSlotRegs, int kOutRegs>
@@ -311,8 +313,9 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
       d[j] = there ? dw[t * K + k] : 0.0f;
       if (id[j] < 0 || id[j] >= E) {   // unused: whatever its weight and gradient hold
         id[j] = -1;
-        g[j] = d[j] = 0.0f;
+        g[j] = 0.0f;
       }
+      if (g[j] == 0.0f) d[j] = 0.0f;
     }
     // in 64 bits: with one weight near 1, its dw less the sum is what the others leave
     double s = 0.0;

@@ -11,7 +11,7 @@ import torch
 
 from mixture_experts_layer_30_amd import binding as B
 from test_gpu_block_ops import (DEV, E24, EPS, Ref, close, columns, gate_factors, gates, gen,
-                                params, randn, tchain)
+                                pairs_of, params, randn, routed, softmax_grad, tchain)
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +151,45 @@ def test_layer_norm_of_constant_bf16_rows(H):
     B.moe_norm(x, n, o)
     # Far's bound at no deviation: (C + 3) e d0 / sqrt(eps), d0 = C e 1000, below 4e-6 a weight
     close(o, n.bias.double()[None].expand(5, H), 4e-6 * n.weight.double().abs()[None])
+
+
+# ----------------------------------------------------------- slots of weight zero
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("T,E,K", [(5, 4, 2), (33, 64, 8), (9, 256, 8), (3, 200, 100)])
+def test_gradients_next_to_a_slot_of_weight_zero(T, E, K, bad):
+    """A slot of weight 0 adds nothing to the tokens, whatever its row holds: the logits'
+    gradient goes on without it, and its own is 0."""
+    H = 64
+    ids, w, plan = routed(T, E, K, 16, B.PAD_BLOCK, T + E)
+    w[:, -1] = 0.0
+    inv = pairs_of(plan, T, K)
+    g = gen(T + E + 54)
+    rows, dout = randn(g, plan.cap, H), randn(g, T, H)
+    rows[inv[:, -1]] = bad
+    out, drows = torch.empty(T, H, device=DEV), torch.empty_like(rows)
+    B.moe_unpermute(rows, w, plan, out)
+    assert torch.isfinite(out).all()
+    dw, o = nans(T, K), nans(T, E)
+    B.moe_unpermute_backward(dout, rows, w, plan, drows, dw)
+    assert torch.isfinite(dw[:, :-1]).all() and (drows[inv[:, -1]] == 0).all()
+    B.moe_route_backward(ids, w, dw, o)
+    clean = dw.clone()
+    clean[:, -1] = 0.0
+    ref, mag = softmax_grad(ids, w, clean, E)
+    # the mean is taken in 64 bits: a rounding for the product and one for the result
+    close(o, ref, 2 * E24 * ref.abs() + K * 2.0 ** -52 * mag)
+    assert (o.gather(1, ids[:, -1:].long()) == 0).all()
+
+
+@pytest.mark.parametrize("T,E,K,budget", [(1, 256, 8, False), (37, 37, 5, True), (3, 256, 256, True),
+                                          (2049, 8, 2, False), (5, 200, 100, True)])
+def test_route_backward_to_its_last_rounding(T, E, K, budget):
+    """The mean over the slots is summed in 64 bits: the result is off by its own rounding
+    and what 64 bits leave."""
+    ids, w, _ = routed(T, E, K, 16, B.PAD_BLOCK, T + E + 1, budget)
+    dw, o = randn(gen(T + 55), T, K), nans(T, E)
+    B.moe_route_backward(ids, w, dw, o)
+    ref, mag = softmax_grad(ids, w, dw, E)
+    close(o, ref, 2 * K * 2.0 ** -52 * mag)

@@ -984,6 +984,8 @@ hipError_t launch_norm_backward(const void* e, int edt, const void* v, int vdt, 
   const int elements = lane_elements(H);
   const int staged = (threads - shape.waves * kWave) * elements * 4;
   ParamGrads p{nullptr, nullptr, n.weight, n.bias, gate.channel, dweight, dbias, dchannel};
+  // (no tokens: zeros, whatever the parameters that the sums would be multiplied with)
+  if (T == 0) p.weight = p.bias = p.channel = nullptr;
   float* part1 = dweight || dchannel ? workspace : nullptr;
   float* part0 = dbias || (dchannel && n.bias) ? workspace + (int64_t)G * H : nullptr;
   p.part1 = part1;

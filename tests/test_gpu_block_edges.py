@@ -193,3 +193,19 @@ def test_route_backward_to_its_last_rounding(T, E, K, budget):
     B.moe_route_backward(ids, w, dw, o)
     ref, mag = softmax_grad(ids, w, dw, E)
     close(o, ref, 2 * K * 2.0 ** -52 * mag)
+
+
+# ------------------------------------------------------------------ empty batches
+
+
+def test_gradients_of_no_tokens_are_zero_whatever_the_parameters():
+    x, v = torch.empty(0, 64, device=DEV), torch.ones(64, device=DEV)
+    bad = v.clone()
+    bad[3], bad[7], bad[11] = float("inf"), float("nan"), float("-inf")
+    n, gate = B.Norm(B.NORM_RMS, EPS, bad, bad), B.Gate(1.0, bad)
+    d = [nans(64) for _ in range(5)]
+    ws = torch.empty(0, dtype=torch.uint8, device=DEV)
+    B.moe_norm_backward(x, x, n, x, dweight=d[0], dbias=d[1], workspace=ws)
+    B.moe_norm_residual_backward(x, x, n, gate, x, ws, d[2], d[3], d[4])
+    for t in d:
+        assert (t == 0).all()

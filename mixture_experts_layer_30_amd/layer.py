@@ -201,7 +201,8 @@ class MoEBlock:
     The layer's inputs["x"] is written by the pre norm.  router(tokens, logits), when
     given, fills inputs["logits"] from it on the current stream (the router's product
     is the caller's); without one they are there before each pass.  Buffers are
-    allocated once; a pass only enqueues work on the current stream."""
+    allocated once; a pass only enqueues work on the current stream, of the GPU that
+    holds the layer, which has to be the current one."""
 
     def __init__(self, layer, pre, post, gate=None, next_norm=None, router=None,
                  stream_dtype=torch.bfloat16):
@@ -214,12 +215,14 @@ class MoEBlock:
 
     def forward(self, x):
         """One pass over the residual stream x [T,H] (of stream_dtype); returns (r, n)."""
+        self._here(x)
         B.moe_norm(x, self.pre, self.layer.inputs["x"])
         return self.normed(x)
 
     def normed(self, x):
         """forward(x) where the layer's inputs["x"] holds pre(x) already, as written by the
         block before (its n is that tensor)."""
+        self._here(x)
         layer = self.layer
         if self.router is not None:
             self.router(layer.inputs["x"], layer.inputs["logits"])
@@ -228,3 +231,8 @@ class MoEBlock:
                                     self.post, self.gate, self.r, pre=self.next_norm, n=self.n,
                                     shared=layer.shared_out if layer.has_shared else None)
         return self.r, self.n
+
+    @staticmethod
+    def _here(x):
+        if x.get_device() < 0 or x.get_device() != torch.cuda.current_device():
+            raise B.MoEError(B.MOE_EINVAL, f"tokens on {x.device}, which is not the current GPU")

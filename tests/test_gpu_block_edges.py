@@ -5,13 +5,16 @@ rows that the workgroups take in turn at every width, every subset of the gradie
 Tolerances are bounds on rounding as in test_gpu_block_ops.py, whose helpers are used;
 e = 2^-24 is one fp32 rounding.
 """
+import itertools
+
 import numpy as np
 import pytest
 import torch
 
 from mixture_experts_layer_30_amd import binding as B
-from test_gpu_block_ops import (DEV, E24, EPS, Ref, close, columns, gate_factors, gates, gen,
-                                pairs_of, params, randn, routed, softmax_grad, tchain)
+from test_gpu_block_ops import (DEV, DT, E24, EPS, Ref, close, columns, gate_factors, gates, gen,
+                                hchain, pairs_of, params, randn, reference, check_residual,
+                                routed, softmax_grad, stream_rows, tchain)
 
 pytestmark = pytest.mark.gpu
 
@@ -209,3 +212,151 @@ def test_gradients_of_no_tokens_are_zero_whatever_the_parameters():
     B.moe_norm_residual_backward(x, x, n, gate, x, ws, d[2], d[3], d[4])
     for t in d:
         assert (t == 0).all()
+
+
+# ------------------------------------------------- norms without biases, rows in turn
+
+# (T, H, y, x, parameters): one row a workgroup, then more rows than workgroups at each
+# width of a lane -- 8 elements, 16 by width, and 16 of bf16 rows past 4096
+TURNS = [(5, 72, "bf16", "bf16", "bf16"), (128, 7168, "bf16", "bf16", "bf16"),
+         (4500, 264, "bf16", "f32", "f32"), (1300, 3584, "f32", "f32", "bf16"),
+         (700, 4096, "bf16", "f32", "bf16"), (1200, 4104, "bf16", "bf16", "f32"),
+         (1100, 7168, "bf16", "bf16", "bf16"), (530, 8200, "bf16", "bf16", "bf16"),
+         (300, 8200, "f32", "f32", "f32"), (300, 16384, "bf16", "f32", "f32"),
+         (270, 12288, "f32", "bf16", "f32")]
+
+
+@pytest.mark.parametrize("kind,pre_kind", [(B.NORM_RMS, B.NORM_RMS), (B.NORM_LAYER, None),
+                                           (B.NORM_RMS, B.NORM_LAYER)])
+@pytest.mark.parametrize("T,H,ydt,xdt,pdt", TURNS)
+def test_residual_without_biases(T, H, ydt, xdt, pdt, kind, pre_kind):
+    """From y and from pair rows, without a gate, with a token's, and with a channel's."""
+    g = gen(T + H + 61)
+    y, x = stream_rows(g, T, H, ydt, kind), stream_rows(g, T, H, xdt, pre_kind)
+    post = params(g, H, pdt, kind, bias=False)
+    pre = params(g, H, pdt, pre_kind, bias=False) if pre_kind is not None else None
+    w = torch.rand(T, 2, generator=g, device=DEV)
+    pairs = randn(g, 2 * T, H, dt=ydt)
+    c = torch.empty(T, H, device=DEV)
+    B.moe_combine(pairs, w, c)
+    from_y, from_c = reference(y, post), reference(c, post)
+    for channel, token in ((False, False), (False, True), (True, False)):
+        gate = gates(g, T, H, pdt, channel, token, 0.7)
+        for ref in (from_y, from_c):
+            r = torch.full((T, H), float("nan"), dtype=DT[xdt], device=DEV)
+            n = torch.full((T, H), float("nan"), dtype=DT[ydt], device=DEV) if pre else None
+            if ref is from_y:
+                B.moe_norm_residual(y, x, post, gate, r, pre=pre, n=n)
+            else:
+                B.moe_combine_norm_residual(pairs, w, x, post, gate, r, pre=pre, n=n)
+            check_residual(r, n, ref, x, gate, pre, T)
+
+
+@pytest.mark.parametrize("kind", [B.NORM_RMS, B.NORM_LAYER])
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("T,H,ydt,xdt,pdt", [(800, 8200, "bf16", "bf16", "bf16"), (530, 16384, "f32", "bf16", "f32"),
+                                             (560, 12288, "bf16", "f32", "bf16")])
+def test_wide_rows_in_turn(T, H, ydt, xdt, pdt, kind, bias):
+    """Norms wider than 8192: more rows than workgroups, forward and all the gradients."""
+    g = gen(T + H + 62)
+    y = stream_rows(g, T, H, ydt, kind)
+    n = params(g, H, pdt, kind, bias=bias)
+    ref = reference(y, n)
+    o = torch.full((T, H), float("nan"), dtype=DT[xdt], device=DEV)
+    B.moe_norm(y, n, o)
+    close(o, ref.out, ref.e_out)
+    dr, dres = randn(g, T, H, dt=xdt), randn(g, T, H, dt=ydt)
+    d = dr.double()
+    dx, dw, db = torch.full_like(y, float("nan")), nans(H), nans(H) if bias else None
+    B.moe_norm_backward(dr, y, n, dx, workspace(T, H), dres=dres, dweight=dw, dbias=db)
+    gw = d * ref.w
+    want, err = ref.backward(gw, E24 * gw.abs())
+    close(dx, want + dres.double(), err + E24 * (want.abs() + dres.double().abs()))
+    close(dw, *columns(d * ref.xh, d.abs() * (ref.e_xh + E24 * ref.xh.abs())))
+    if bias:
+        close(db, *columns(d, 0 * d))
+    check_gradients(dr, y, n, gates(g, T, H, pdt, True, True, 0.6), ref, subsets=[(1, bias, 1, 1)])
+
+
+# ----------------------------------------------------- every subset of the gradients
+
+
+def check_gradients(dr, y, post, gate, ref, subsets):
+    T, H = y.shape
+    a, c = gate_factors(gate, T)
+    d = dr.double()
+    du, ad = a * c * d, a * d
+    gw = du * ref.w
+    dy_ref = ref.backward(gw, 4 * E24 * gw.abs())
+    mag = (ref.xh * ref.w).abs() + ref.b.abs()
+    v = torch.tensor(gate.alpha, dtype=torch.float32).double().item() * c * d
+    refs = [columns(du * ref.xh, du.abs() * (ref.e_xh + 4 * E24 * ref.xh.abs())),
+            columns(du, 4 * E24 * du.abs()),
+            ((ad * ref.out).sum(0), (ad.abs() * (ref.e_out + 3 * E24 * mag)).sum(0) +
+             (tchain(T) + 2) * E24 * (ad.abs() * mag).sum(0)),
+            ((v * ref.out).sum(1), (v.abs() * (ref.e_out + (hchain(H) + 4) * E24 * mag)).sum(1))]
+    ws = workspace(T, H)
+    for asked in subsets:
+        outs = [nans(n) if on else None for on, n in zip(asked, (H, H, H, T))]
+        dy = torch.full_like(y, float("nan"))
+        B.moe_norm_residual_backward(dr, y, post, gate, dy, ws if any(asked[:3]) else None, *outs)
+        close(dy, *dy_ref)
+        for o, r in zip(outs, refs):
+            if o is not None:
+                close(o, *r)
+
+
+@pytest.mark.parametrize("kind,bias", [(B.NORM_RMS, True), (B.NORM_RMS, False), (B.NORM_LAYER, True),
+                                       (B.NORM_LAYER, False), (B.NORM_NONE, False)])
+@pytest.mark.parametrize("T,H,ydt,xdt", [(515, 520, "bf16", "bf16"), (300, 3584, "bf16", "f32"),
+                                         (4099, 128, "f32", "f32"), (300, 8200, "bf16", "bf16"),
+                                         (2, 16384, "f32", "bf16")])
+def test_every_subset_of_the_gradients(T, H, ydt, xdt, kind, bias):
+    g = gen(T + H + 71)
+    y, dr = stream_rows(g, T, H, ydt, kind), randn(g, T, H, dt=xdt)
+    post, gate = params(g, H, "f32", kind, bias=bias), gates(g, T, H, "f32", True, True, 0.6)
+    norm = (False, True) if kind != B.NORM_NONE else (False,)
+    subsets = list(itertools.product(norm, norm, (False, True), (False, True)))
+    check_gradients(dr, y, post, gate, reference(y, post), subsets)
+
+
+# --------------------------------------------------------------- past 32-bit offsets
+
+
+def test_gates_gradients_past_32_bit_offsets():
+    """A token buffer of more than 2^32 bytes and 2^31 elements, whose last 40 rows carry
+    nearly all of the sums over the tokens: one of them lost would show."""
+    T, H = 300007, 7168
+    g = gen(81)
+    y = torch.empty(T, H, dtype=torch.bfloat16, device=DEV).normal_(generator=g)
+    n, gate = params(g, H, "f32", B.NORM_RMS), gates(g, T, H, "f32", True, True, 0.5)
+    gate.token[-40:] += 1e5
+    ws = workspace(T, H)
+    dw, db, dc, dq = nans(H), nans(H), nans(H), nans(T)
+    dy = torch.empty_like(y)
+    B.moe_norm_residual_backward(y, y, n, gate, dy, ws, dw, db, dc, dq)   # y for the gradient too
+    some = torch.cat([torch.arange(40), torch.arange(T - 40, T)]).to(DEV)
+    ref, part = reference(y[some], n), B.Gate(gate.alpha, gate.channel, gate.token[some])
+    a, c = gate_factors(part, 80)
+    d = y[some].double()
+    gw = a * c * d * ref.w
+    close(dy[some], *ref.backward(gw, 4 * E24 * gw.abs()))
+    v, mag = 0.5 * c * d, (ref.xh * ref.w).abs() + ref.b.abs()
+    close(dq[some], (v * ref.out).sum(1), (v.abs() * (ref.e_out + (hchain(H) + 4) * E24 * mag)).sum(1))
+    sums, mags, last = (torch.zeros(2, H, dtype=torch.float64, device=DEV) for _ in range(3))
+    for lo in range(0, T, 8192):
+        ref = reference(y[lo:lo + 8192], n)
+        ad = 0.5 * gate.token[lo:lo + 8192].double()[:, None] * y[lo:lo + 8192].double()
+        for i, v in enumerate((ad * ref.xh, ad)):
+            sums[i] += v.sum(0)
+            mags[i] += v.abs().sum(0)
+    for i, v in enumerate(((a * d * reference(y[some], n).xh)[40:], (a * d)[40:])):
+        last[i] = v.abs().sum(0) / 40
+    # rows one after the other in a sum: T / 512 in a workgroup, then 512 / 64 + 8 + 8 of their
+    # sums; a row's own value is right to hchain(H) roundings
+    err = (hchain(H) + T / 512 + 30) * E24 * mags
+    assert (err * 100 < last).all()   # the bound is far below what a row of the last adds
+    ch, w, b = gate.channel.double(), n.weight.double(), n.bias.double()
+    close(dw, ch * sums[0], ch.abs() * err[0])
+    close(db, ch * sums[1], ch.abs() * err[1])
+    close(dc, w * sums[0] + b * sums[1], w.abs() * err[0] + b.abs() * err[1])

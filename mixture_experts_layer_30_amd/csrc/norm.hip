@@ -928,10 +928,14 @@ hipError_t launch_norm_residual(const void* y, int ydt, const void* x, int xdt, 
   const int e = half ? 16 : lane_elements(H);
   const int threads = threads_for(H, e);
   // With an fp32 stream, rows of 6 to 8 wavefronts and no post layer norm (whose two more
-  // reductions want a second workgroup to run beside), one workgroup a CU: 16384 x 4096,
-  // channel gate, next layer norm 136 us, with two 149; 4 wavefronts a row 37.3, so 36.0.
-  // Without gates or biases two (8192 x 4096 72 us, with one 78).
-  const bool few = xdt == kDtF32 && post.kind != kNormLayer && threads > 5 * kWave;
+  // reductions want a second workgroup to run beside), one workgroup a CU from 32 rows for
+  // each on: channel gate and next layer norm, 16384 rows of 3328, 3584, 4096 111, 128, 133
+  // us, with two 124, 128, 141; a token gate 111, 120, 135, so 121, 129, 139.  Of fewer rows
+  // a CU has too little in flight: 2048 rows of 2816 with it 15.6 us, with two 13.3, 4096
+  // 27.0 and 23.7, 1024 of 4096 10.8 and 10.1.  4 wavefronts a row 37.3, so 36.0.  Without
+  // gates or biases two (8192 x 4096 72 us, with one 78).
+  const bool few =
+      xdt == kDtF32 && post.kind != kNormLayer && threads > 5 * kWave && T >= 32 * 256;
   return with_types(ydt, xdt, pdt, e, [&](auto sy, auto sx, auto sp, auto layout) {
     auto go = [&](auto kernel, int per_cu) {
       hipLaunchKernelGGL(kernel, dim3(forward_groups(T, threads, per_cu)), dim3(threads), 0, s, y,

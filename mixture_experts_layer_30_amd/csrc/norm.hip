@@ -285,8 +285,9 @@ __device__ __forceinline__ float center_and_rstd(float (&v)[L::V][L::N], const L
     float s[2] = {squares(), sum()};
     block_sum<2>(s, waves, buf.take());
     const float rest = s[1] * inv_h;
+    const float rstd = rstd_of(s[0], inv_h, eps, rest);
     take(rest);
-    return rstd_of(s[0], inv_h, eps, rest);
+    return rstd;
   }
   float s[1] = {squares()};
   block_sum<1>(s, waves, buf.take());

@@ -24,6 +24,10 @@
  *                                 and residual sum after it; their gradients
  *   moe_combine_norm_residual     moe_combine with the latter in one launch
  *
+ * The gradients are calls of their own, chained by the caller; the grouped FFN has
+ * none: a caller who trains the experts brings their products and gradients over
+ * the rows of moe_permute.
+ *
  * Sources for what each call computes are cited at the call.  "Serving-tax
  * notes" below means the talk notes on "Demystifying the Mixture of Experts
  * Serving Tax" (MLSys 2026); "TEMPO page" means the article on TEMPO
@@ -357,8 +361,8 @@ moe_status dense_ffn_fa(const void *x, moe_dtype dt, int64_t T, int H, int I_fa,
  * the same rows.  topk_w NULL: every weight 1 (dw must then be NULL).  The
  * gradient of `shared` is dout itself.  Either of drows and dw may be NULL;
  * drows may be rows.  The dw of a slot of weight 0 is taken from its row like any
- * other's (NaN or infinite where that row is).  dw is fp32, summed over H in a fixed order.  No atomics:
- * every result is the same on every run.
+ * other's (NaN or infinite where that row is).  dw is fp32, summed over H in a
+ * fixed order.  No atomics: every result is the same on every run.
  * x, dx [T][H] dt; rows, drows [plan->cap][H] dt / rdt; dout, out [T][H] odt;
  * shared [T][H] sdt; topk_w, dw [T][K] fp32.  dout and rows have the same type.
  * Limits: H a multiple of 8, T*H < 2^39.  Row indices of the plan outside
@@ -450,8 +454,8 @@ typedef struct {
  * calls that may overlap need one each.  T = 0 writes zeros to those gradients
  * and does nothing else.
  * Squares are summed in fp32: with eps = 0 a row of zeros (for a layer norm: of
- * one value), or one whose squares underflow, has no norm (NaN), and elements past
- * 1e19 overflow it.
+ * one value), or one whose squares underflow, has no norm (what is written for it
+ * means nothing, and may be NaN), and elements past 1e19 overflow it.
  * Limits: H a multiple of 8, at most 16384; T*H < 2^39.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY (workspace).
  */

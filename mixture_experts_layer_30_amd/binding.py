@@ -320,6 +320,10 @@ def dense_ffn_fp8(x, q13, s13, q2, s2, workspace, out, stream=None):
 
 
 # ---------------------------------------------- around the experts: rows, norms, gates
+#
+# These calls are outside torch's autograd: a tensor that requires grad gets none from
+# them, and buffers are written without autograd's knowledge.  The gradients are the
+# *_backward calls, in the caller's order; the grouped FFN has none.
 
 
 def _refuse(what):

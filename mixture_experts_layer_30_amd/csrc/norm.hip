@@ -22,11 +22,15 @@
 // kernel adds the rows in order, so no atomics and the same result every run.
 //
 // Measured on MI355X, inputs that no cache holds (a copy of 1 GB runs at 5.1 TB/s):
-// RMS norm of 16384 x 4096 bf16 46 us (5.8 TB/s), gated residual on an fp32 stream
-// with the next layer norm at the same size 142 us (5.7 TB/s), RMS norm gradients of
-// 8192 x 7168 with a gradient that passes by 90 us (5.2 TB/s), the end of a layer
-// pass, combine to next norm, of 128 x 7168 with 8 pair rows a token 6.5 us (8192
-// tokens 212 us, 6.1 TB/s).
+// RMS norm of 16384 x 4096 bf16 46 us (5.8 TB/s), layer norm 48, gated residual on an
+// fp32 stream with the next layer norm at the same size 134-140 us (5.8-6.0 TB/s), RMS
+// norm gradients of 8192 x 7168 with a gradient that passes by 92 us (5.1 TB/s; both
+// launches), layer norm's of 4099 x 3584 with all gates 25 us (3.5 TB/s, vector
+// instructions as much as memory), the end of a layer pass, combine to next norm, of
+// 128 x 7168 with 8 pair rows a token 7 us (8192 tokens 214 us, 6.0 TB/s).  Rows past
+// 8192 elements: forward 5.2-5.9 TB/s, gradients 3.2-5.2.  The pairs of times at the
+// choices below are of builds that differ in that choice alone, the layer norms' from
+// before the second pass over the mean, which costs them 0-5%.
 #include "block_kernels.h"
 #include "common.h"
 #include "rows.h"

@@ -379,17 +379,30 @@ def _ref(o):
     return None if o is None else o.ref()
 
 
-class Norm:
+class _Params:
+    """Holds the C struct that a call reads; a copy has one of its own."""
+    _type = None
+
+    def __init__(self):
+        self._c = self._type()
+        self._ref = ctypes.byref(self._c)
+
+    def __getstate__(self):
+        return {k: v for k, v in self.__dict__.items() if k not in ("_c", "_ref")}
+
+    def __setstate__(self, state):
+        self.__dict__.update(state)
+        _Params.__init__(self)
+
+
+class Norm(_Params):
     """A norm's kind, eps and parameters (see moe_norm_params in include/moe_layer.h).
     weight, bias [H] fp32 or bf16, or None: ones, zeros.  Holds the tensors it points to."""
+    _type = moe_norm_params
 
     def __init__(self, kind=NORM_RMS, eps=1e-6, weight=None, bias=None):
         self.kind, self.eps, self.weight, self.bias = kind, eps, weight, bias
-        self._c = moe_norm_params()
-        self._ref = ctypes.byref(self._c)
-
-    def __reduce__(self):   # a copy has a struct of its own
-        return type(self), (self.kind, self.eps, self.weight, self.bias)
+        super().__init__()
 
     def ref(self):
         c, w, b = self._c, self.weight, self.bias
@@ -400,17 +413,14 @@ class Norm:
         return self._ref
 
 
-class Gate:
+class Gate(_Params):
     """alpha * channel[h] * token[t] (see moe_gate_params): channel [H] of the parameters'
     type, token [T] fp32, either None.  Holds the tensors it points to."""
+    _type = moe_gate_params
 
     def __init__(self, alpha=1.0, channel=None, token=None):
         self.alpha, self.channel, self.token = alpha, channel, token
-        self._c = moe_gate_params()
-        self._ref = ctypes.byref(self._c)
-
-    def __reduce__(self):   # (see Norm)
-        return type(self), (self.alpha, self.channel, self.token)
+        super().__init__()
 
     def ref(self):
         c, ch, tok = self._c, self.channel, self.token

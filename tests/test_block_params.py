@@ -71,3 +71,19 @@ def test_block_refuses_tokens_of_another_device_before_it_runs(call, device, mon
     with pytest.raises(B.MoEError) as e:
         getattr(block, call)(x)
     assert e.value.status == B.MOE_EINVAL and layer.passes == 0
+
+
+class Named(B.Norm):
+    """A subclass with an argument and an attribute of its own."""
+
+    def __init__(self, name, **k):
+        super().__init__(**k)
+        self.name = name
+
+
+def test_copies_keep_what_a_user_adds():
+    n = Named("first", kind=B.NORM_LAYER, eps=0.5)
+    n.step = 3
+    for c in (copy.copy(n), copy.deepcopy(n)):
+        assert type(c) is Named and (c.name, c.step) == ("first", 3)
+        assert held(c) == held(n) and c.ref()._obj is not n.ref()._obj

@@ -223,7 +223,8 @@ TURNS = [(5, 72, "bf16", "bf16", "bf16"), (128, 7168, "bf16", "bf16", "bf16"),
          (700, 4096, "bf16", "f32", "bf16"), (1200, 4104, "bf16", "bf16", "f32"),
          (1100, 7168, "bf16", "bf16", "bf16"), (530, 8200, "bf16", "bf16", "bf16"),
          (300, 8200, "f32", "f32", "f32"), (300, 16384, "bf16", "f32", "f32"),
-         (270, 12288, "f32", "bf16", "f32")]
+         (270, 12288, "f32", "bf16", "f32"),
+         (8200, 2568, "bf16", "f32", "bf16")]   # one workgroup a CU where there is a gate
 
 
 @pytest.mark.parametrize("kind,pre_kind", [(B.NORM_RMS, B.NORM_RMS), (B.NORM_LAYER, None),

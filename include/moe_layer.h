@@ -24,9 +24,14 @@
  *                                 and residual sum after it; their gradients
  *   moe_combine_norm_residual     moe_combine with the latter in one launch
  *
- * The gradients are calls of their own, chained by the caller; the grouped FFN has
- * none: a caller who trains the experts brings their products and gradients over
- * the rows of moe_permute.
+ * And for training:
+ *
+ *   moe_grouped_ffn_train, dense_ffn_train         the FFN, keeping what its gradients
+ *                                                  need, in bf16 or in 8 bits
+ *   moe_grouped_ffn_backward, dense_ffn_backward   the gradients of rows and weights
+ *   moe_pack_fp8, moe_unpack_fp8                   activations kept in 8 bits, and read back
+ *
+ * The gradients are calls of their own, chained by the caller.
  *
  * Sources for what each call computes are cited at the call.  "Serving-tax
  * notes" below means the talk notes on "Demystifying the Mixture of Experts
@@ -481,6 +486,83 @@ moe_status moe_norm_residual_backward(const void *dr, moe_dtype xdt, const void 
                                       const moe_gate_params *gate, moe_dtype pdt, void *dy,
                                       float *dweight, float *dbias, float *dchannel, float *dtoken,
                                       void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Training the experts: the FFN over the rows of an alignment, and its gradients.
+ * With x the token of row r, of expert e, and (g, u) = W13_e x, W13 = (W1, W3):
+ *
+ *   moe_grouped_ffn_train     a = silu(g) * u;  rows[r] = W2_e a;  g and u kept in
+ *                             `saved`
+ *   moe_grouped_ffn_backward  from drows and saved: da = W2_e^T drows[r],
+ *                               dg = da * u * s (1 + g (1 - s)),  du = da * g s,
+ *                               s = 1 / (1 + exp(-g)),
+ *                             dxrows[r] = W13_e^T (dg, du), and over the rows of e
+ *                               dw13_e = sum (dg, du) x^T,  dw2_e = sum drows[r] a^T
+ *   dense_ffn_train, _backward   the same over all T tokens with one set of weights
+ *                             (row t is token t): a layer's shared experts
+ *
+ * Around them in a step: rows go to moe_unpermute; drows come from
+ * moe_unpermute_backward; dxrows go to moe_permute_backward.  The row buffers
+ * [plan->cap][H] are in the alignment's order (any padding); only the rows that
+ * hold a pair are read, and only they are written: the others are left as they were.
+ *
+ * saved: the gate and up values of every row, [rows][2I] (gate columns, then up
+ * columns; rows = plan->cap, or T), where `format` says so as e4m3 codes with the
+ * scales of moe_pack_fp8: [rows][2I/32] bytes.  The gradients are those at the kept
+ * values: a, too, is computed from them again.  The forward computes a and rows from
+ * the values before they are rounded.
+ * x, w13, w2, rows, drows, dxrows are bf16, and so are a, dg and du between the
+ * products; sums are fp32.  dw13 [E][2I][H] and dw2 [E][H][I] (dense: without E) are
+ * of type dwdt, overwritten; an expert without rows (or T = 0) gets zeros.  Each of
+ * dxrows, dw13 and dw2 may be NULL, not all of them; x may be NULL where dw13 is, and
+ * w13 where dxrows is.  dxrows may not be drows.  No atomics: the same on every run.
+ * workspace: 16-byte aligned, with no contents to keep before or after the call; the
+ * forward needs moe_ffn_train_workspace_bytes(rows, H, I) bytes, the gradients
+ * moe_ffn_backward_workspace_bytes(rows, H, I); calls that may overlap need one each.
+ * Limits: H, I at most 2^20, an expert's w13 below 4 GB, and the grouped x below 4 GB.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY (plan, workspace).
+ */
+typedef enum { MOE_SAVE_BF16 = 0, MOE_SAVE_FP8 = 1 } moe_save_format;
+
+typedef struct {
+    int32_t format;      /* moe_save_format */
+    void *h;             /* [rows][2I] bf16, or e4m3 codes */
+    uint8_t *scales;     /* [rows][2I/32] (MOE_SAVE_FP8) */
+} moe_saved;
+
+int64_t moe_ffn_train_workspace_bytes(int64_t rows, int H, int I);      /* -1 on bad arguments */
+int64_t moe_ffn_backward_workspace_bytes(int64_t rows, int H, int I);   /* -1 on bad arguments */
+moe_status moe_grouped_ffn_train(const void *x, int64_t T, int H, int I, int E, int K,
+                                 const void *w13, const void *w2, const moe_plan *plan,
+                                 const moe_saved *saved, void *workspace, int64_t workspace_bytes,
+                                 void *rows, void *stream);
+moe_status moe_grouped_ffn_backward(const void *drows, const void *x, int64_t T, int H, int I,
+                                    int E, int K, const void *w13, const void *w2,
+                                    const moe_plan *plan, const moe_saved *saved, void *workspace,
+                                    int64_t workspace_bytes, void *dxrows, void *dw13, void *dw2,
+                                    moe_dtype dwdt, void *stream);
+moe_status dense_ffn_train(const void *x, int64_t T, int H, int I, const void *w13, const void *w2,
+                           const moe_saved *saved, void *workspace, int64_t workspace_bytes,
+                           void *out, void *stream);
+moe_status dense_ffn_backward(const void *dout, const void *x, int64_t T, int H, int I,
+                              const void *w13, const void *w2, const moe_saved *saved,
+                              void *workspace, int64_t workspace_bytes, void *dx, void *dw13,
+                              void *dw2, moe_dtype dwdt, void *stream);
+
+/*
+ * Activations kept in 8 bits until the backward pass.  Each 32 neighbours of a row
+ * share the least power of two s = 2^e with max |v| <= 448 s, e >= -127, held as the
+ * byte e + 127; v is kept as the OCP FP8 E4M3 value nearest to v / s (ties to even):
+ * off by at most 2^-4 of |v| and 2^-10 s.  A value that is not finite is kept as NaN and
+ * has no part in the maximum.  moe_unpack_fp8 gives code * s, rounded to the type asked
+ * for (both hold it exactly but bf16 below 2^-133).
+ * x [T][H] dt; codes [T][H]; scales [T][H/32].  Limits: H a multiple of 32, T*H < 2^39.
+ * Errors: MOE_EINVAL, MOE_EUNSUPPORTED.
+ */
+moe_status moe_pack_fp8(const void *x, moe_dtype dt, int64_t T, int H, uint8_t *codes,
+                        uint8_t *scales, void *stream);
+moe_status moe_unpack_fp8(const uint8_t *codes, const uint8_t *scales, int64_t T, int H, void *x,
+                          moe_dtype dt, void *stream);
 
 /*
  * FP8 weights: weight quantization, the notes' decode-phase remedy (Serving-tax

@@ -17,6 +17,7 @@ MOE_F32, MOE_BF16 = 0, 1
 SCHED_AUTO, SCHED_STREAM, SCHED_TILE, SCHED_RING, SCHED_SPAN = 0, 1, 2, 3, 4
 PAD_BLOCK, PAD_MAX = 0, 1
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
+SAVE_BF16, SAVE_FP8 = 0, 1
 
 # every function the C header declares
 EXPORTS = ["moe_last_error", "moe_status_string", "moe_align_capacity", "moe_align_capacity_ex",
@@ -26,7 +27,10 @@ EXPORTS = ["moe_last_error", "moe_status_string", "moe_align_capacity", "moe_ali
            "dense_ffn_fp8", "moe_grouped_ffn_noalloc", "moe_permute", "moe_permute_backward",
            "moe_unpermute", "moe_unpermute_backward", "moe_route_backward",
            "moe_norm_workspace_bytes", "moe_norm", "moe_norm_backward", "moe_norm_residual",
-           "moe_norm_residual_backward", "moe_combine_norm_residual"]
+           "moe_norm_residual_backward", "moe_combine_norm_residual",
+           "moe_ffn_train_workspace_bytes", "moe_ffn_backward_workspace_bytes",
+           "moe_grouped_ffn_train", "moe_grouped_ffn_backward", "dense_ffn_train",
+           "dense_ffn_backward", "moe_pack_fp8", "moe_unpack_fp8"]
 
 # workspace bytes held per GPU by moe_grouped_ffn_noalloc (MOE_NOALLOC_SCRATCH_BYTES)
 NOALLOC_SCRATCH_BYTES = 128 << 20
@@ -51,6 +55,10 @@ class moe_norm_params(ctypes.Structure):
 
 class moe_gate_params(ctypes.Structure):
     _fields_ = [("alpha", ctypes.c_float), ("channel", ctypes.c_void_p), ("token", ctypes.c_void_p)]
+
+
+class moe_saved(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int32), ("h", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -123,6 +131,22 @@ def lib():
                                                 vp, vp, vp, i64, vp])):
             getattr(L, name).restype = i32
             getattr(L, name).argtypes = args
+        V = ctypes.POINTER(moe_saved)
+        for name, args in (
+                ("moe_grouped_ffn_train", [vp, i64, i32, i32, i32, i32, vp, vp, P, V, vp, i64, vp,
+                                           vp]),
+                ("moe_grouped_ffn_backward", [vp, vp, i64, i32, i32, i32, i32, vp, vp, P, V, vp, i64,
+                                              vp, vp, vp, i32, vp]),
+                ("dense_ffn_train", [vp, i64, i32, i32, vp, vp, V, vp, i64, vp, vp]),
+                ("dense_ffn_backward", [vp, vp, i64, i32, i32, vp, vp, V, vp, i64, vp, vp, vp, i32,
+                                        vp]),
+                ("moe_pack_fp8", [vp, i32, i64, i32, vp, vp, vp]),
+                ("moe_unpack_fp8", [vp, vp, i64, i32, vp, i32, vp])):
+            getattr(L, name).restype = i32
+            getattr(L, name).argtypes = args
+        for name in ("moe_ffn_train_workspace_bytes", "moe_ffn_backward_workspace_bytes"):
+            getattr(L, name).restype = i64
+            getattr(L, name).argtypes = [i64, i32, i32]
         L.moe_norm_workspace_bytes.restype = i64
         L.moe_norm_workspace_bytes.argtypes = [i64, i32]
         _lib = L
@@ -323,7 +347,7 @@ def dense_ffn_fp8(x, q13, s13, q2, s2, workspace, out, stream=None):
 #
 # These calls are outside torch's autograd: a tensor that requires grad gets none from
 # them, and buffers are written without autograd's knowledge.  The gradients are the
-# *_backward calls, in the caller's order; the grouped FFN has none.
+# *_backward calls, in the caller's order.
 
 
 def _refuse(what):
@@ -653,3 +677,156 @@ def moe_norm_residual_backward(dr, y, post, gate, dy, workspace=None, dweight=No
     _call(lib().moe_norm_residual_backward, dev, stream, _addr(dr), _dt(dr), _addr(y), _dt(y), T, H,
           _ref(post), _ref(gate), pdt, _addr(dy), _addr(dweight), _addr(dbias),
           _addr(dchannel), _addr(dtoken), ws, n)
+
+
+# ---------------------------------------------- training the experts
+
+
+def moe_ffn_train_workspace_bytes(rows, H, I):
+    return lib().moe_ffn_train_workspace_bytes(rows, H, I)
+
+
+def moe_ffn_backward_workspace_bytes(rows, H, I):
+    return lib().moe_ffn_backward_workspace_bytes(rows, H, I)
+
+
+class Saved:
+    """The gate and up values that a forward keeps for the gradients (see moe_saved in
+    include/moe_layer.h): h [rows,2I] bf16, or e4m3 codes as uint8 and scales [rows,2I/32]
+    (SAVE_FP8).  rows: a plan's cap, or the tokens of a dense FFN."""
+
+    def __init__(self, rows, I, format=SAVE_BF16, device="cuda"):
+        if format not in (SAVE_BF16, SAVE_FP8):
+            _refuse(f"format {format}")
+        self.rows, self.I, self.format = rows, I, format
+        fp8 = format == SAVE_FP8
+        self.h = torch.empty(rows, 2 * I, dtype=torch.uint8 if fp8 else torch.bfloat16,
+                             device=device)
+        self.scales = torch.empty(rows, 2 * I // 32, dtype=torch.uint8, device=device) if fp8 else None
+
+
+def _saved(s, rows, I, *tensors):
+    """The C struct of what a call keeps or reads back, checked; on one GPU with the tensors."""
+    if s.rows < rows or s.I != I:
+        _refuse(f"saved holds {s.rows} rows of I = {s.I}, the call has {rows} of {I}")
+    fp8 = s.format == SAVE_FP8
+    _shaped(s.h, (s.rows, 2 * I), "saved.h", torch.uint8 if fp8 else torch.bfloat16)
+    if fp8:
+        if s.scales is None:
+            _refuse("saved has no scales")
+        _shaped(s.scales, (s.rows, 2 * I // 32), "saved.scales", torch.uint8)
+    dev = _one_device(s.h, s.scales, *tensors)
+    return dev, ctypes.byref(moe_saved(s.format, s.h.data_ptr(), _addr(s.scales)))
+
+
+_BF16 = torch.bfloat16
+
+
+def _weights(w13, w2, H, E=None):
+    """(E, I) of the weights; E given: the grouped ones, [E,2I,H] and [E,H,I]."""
+    if w2.dim() != (2 if E is None else 3):
+        _refuse(f"w2 must be {'[H, I]' if E is None else '[E, H, I]'}, got {list(w2.shape)}")
+    I = w2.shape[-1]
+    lead = () if E is None else (E,)
+    _shaped(w2, lead + (H, I), "w2", _BF16)
+    if w13 is not None:
+        _shaped(w13, lead + (2 * I, H), "w13", _BF16)
+    return I
+
+
+def _weight_grads(dw13, dw2, H, I, E=None):
+    lead = () if E is None else (E,)
+    dt = None
+    for t, shape, what in ((dw13, lead + (2 * I, H), "dw13"), (dw2, lead + (H, I), "dw2")):
+        if t is not None:
+            if dt is not None and t.dtype is not dt:
+                raise MoEError(MOE_EUNSUPPORTED, f"gradients of {dt} and {t.dtype} in one call")
+            _shaped(t, shape, what)
+            dt = t.dtype
+    return MOE_BF16 if dt is None else _dt(dw13 if dw13 is not None else dw2)
+
+
+def moe_grouped_ffn_train(x, w13, w2, plan, saved, workspace, rows, stream=None):
+    """rows[r] = W2 (silu(g) * u), (g, u) = W13 x of the token of row r, of its expert; g and u
+    kept in saved.  x [T,H], w13 [E,2I,H], w2 [E,H,I], rows [plan.cap,H], all bf16; rows that
+    hold no pair are left as they were."""
+    T, H = _planned(x, plan, "x")
+    _need(x, _BF16, "x")
+    I = _weights(w13, w2, H, plan.E)
+    _rows(rows, plan, H, "rows", _BF16)
+    dev, kept = _saved(saved, plan.cap, I, x, w13, w2, rows, workspace, plan.inv_pos)
+    ws, n = _workspace(workspace)
+    _call(lib().moe_grouped_ffn_train, dev, stream, _addr(x), T, H, I, plan.E, plan.K, _addr(w13),
+          _addr(w2), ctypes.byref(plan.c), kept, ws, n, _addr(rows))
+
+
+def moe_grouped_ffn_backward(drows, x, w13, w2, plan, saved, workspace, dxrows=None, dw13=None,
+                             dw2=None, stream=None):
+    """Gradients of moe_grouped_ffn_train from drows [plan.cap,H], at the values kept in saved:
+    dxrows [plan.cap,H] bf16, dw13 and dw2 of the weights' shapes, both bf16 or both fp32, where
+    given.  x may be None where dw13 is, w13 where dxrows is."""
+    H = w2.shape[1] if w2.dim() == 3 else 0
+    I = _weights(w13, w2, H, plan.E)
+    _rows(drows, plan, H, "drows", _BF16)
+    if x is not None:
+        _shaped(x, (plan.T, H), "x", _BF16)
+    if dxrows is not None:
+        _rows(dxrows, plan, H, "dxrows", _BF16)
+    dt = _weight_grads(dw13, dw2, H, I, plan.E)
+    dev, kept = _saved(saved, plan.cap, I, drows, x, w13, w2, dxrows, dw13, dw2, workspace,
+                       plan.inv_pos)
+    ws, n = _workspace(workspace)
+    _call(lib().moe_grouped_ffn_backward, dev, stream, _addr(drows), _addr(x), plan.T, H, I, plan.E,
+          plan.K, _addr(w13), _addr(w2), ctypes.byref(plan.c), kept, ws, n, _addr(dxrows),
+          _addr(dw13), _addr(dw2), dt)
+
+
+def dense_ffn_train(x, w13, w2, saved, workspace, out, stream=None):
+    """moe_grouped_ffn_train over all T tokens with one set of weights: w13 [2I,H], w2 [H,I],
+    out [T,H]."""
+    T, H = _tokens(x, "x")
+    _need(x, _BF16, "x")
+    I = _weights(w13, w2, H)
+    _shaped(out, (T, H), "out", _BF16)
+    dev, kept = _saved(saved, T, I, x, w13, w2, out, workspace)
+    ws, n = _workspace(workspace)
+    _call(lib().dense_ffn_train, dev, stream, _addr(x), T, H, I, _addr(w13), _addr(w2), kept, ws, n,
+          _addr(out))
+
+
+def dense_ffn_backward(dout, x, w13, w2, saved, workspace, dx=None, dw13=None, dw2=None,
+                       stream=None):
+    """Gradients of dense_ffn_train from dout [T,H] (see moe_grouped_ffn_backward)."""
+    T, H = _tokens(dout, "dout")
+    _need(dout, _BF16, "dout")
+    I = _weights(w13, w2, H)
+    for t, what in ((x, "x"), (dx, "dx")):
+        if t is not None:
+            _shaped(t, (T, H), what, _BF16)
+    dt = _weight_grads(dw13, dw2, H, I)
+    dev, kept = _saved(saved, T, I, dout, x, w13, w2, dx, dw13, dw2, workspace)
+    ws, n = _workspace(workspace)
+    _call(lib().dense_ffn_backward, dev, stream, _addr(dout), _addr(x), T, H, I, _addr(w13),
+          _addr(w2), kept, ws, n, _addr(dx), _addr(dw13), _addr(dw2), dt)
+
+
+def _codes(x, what, codes, scales):
+    T, H = _tokens(x, what)
+    if H % 32:
+        raise MoEError(MOE_EUNSUPPORTED, f"H = {H} must be a multiple of 32")
+    _shaped(codes, (T, H), "codes", torch.uint8)
+    _shaped(scales, (T, H // 32), "scales", torch.uint8)
+    return T, H, _one_device(x, codes, scales)
+
+
+def moe_pack_fp8(x, codes, scales, stream=None):
+    """x [T,H] (fp32 or bf16) as e4m3 codes [T,H] and, for each 32 of a row, the exponent of
+    their scale + 127 [T,H/32], both uint8."""
+    T, H, dev = _codes(x, "x", codes, scales)
+    _call(lib().moe_pack_fp8, dev, stream, _addr(x), _dt(x), T, H, _addr(codes), _addr(scales))
+
+
+def moe_unpack_fp8(codes, scales, x, stream=None):
+    """x [T,H] (fp32 or bf16) = the values that the codes stand for."""
+    T, H, dev = _codes(x, "x", codes, scales)
+    _call(lib().moe_unpack_fp8, dev, stream, _addr(codes), _addr(scales), T, H, _addr(x), _dt(x))

@@ -1,0 +1,55 @@
+// Host-side launchers of the experts' training kernels (internal to the library).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace moe {
+
+// What the calls of one training step share.  Rows: expert e owns the rows offsets[e] ..
+// offsets[e] + counts[e] - 1 of the `rows` of every row buffer, and row r holds pair
+// sorted_ids[r]; counts == nullptr: one expert, whose row r is token r.
+struct TrainRows {
+  const int32_t* counts;
+  const int32_t* offsets;
+  const int32_t* sorted_ids;
+  int64_t tokens;   // T
+  int64_t rows;     // of the row buffers: the plan's cap, or T
+  int K;
+  int E, H, I;
+};
+
+// The gate and up values a forward keeps: [rows][2I] bf16, or [rows][2I] e4m3 codes and
+// [rows][2I / 32] biased exponents of their blocks' scales (fp8).
+struct SavedRows {
+  void* h;
+  uint8_t* scales;
+  bool fp8;
+};
+
+// act [rows][I] = silu(g) * u with g, u = w13 x; g and u kept
+hipError_t launch_train_gate_up(const TrainRows& r, const void* x, const void* w13,
+                                const SavedRows& saved, uint16_t* act, hipStream_t s);
+// y [rows][H] = w2 act
+hipError_t launch_train_down(const TrainRows& r, const void* w2, const uint16_t* act, void* y,
+                             hipStream_t s);
+// from da = w2^T dy: act = silu(g) * u, and dh [rows][2I], the gradients of g and of u
+hipError_t launch_train_dact(const TrainRows& r, const void* w2, const void* dy,
+                             const SavedRows& saved, uint16_t* act, uint16_t* dh, hipStream_t s);
+// dx [rows][H] = w13^T dh
+hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
+                           hipStream_t s);
+// dw13 [E][2I][H] = sum over an expert's rows of dh x^T; f32: its type is fp32, else bf16
+hipError_t launch_train_dw13(const TrainRows& r, const void* x, const uint16_t* dh, void* dw13,
+                             bool f32, hipStream_t s);
+// dw2 [E][H][I] = sum over an expert's rows of dy act^T
+hipError_t launch_train_dw2(const TrainRows& r, const uint16_t* act, const void* dy, void* dw2,
+                            bool f32, hipStream_t s);
+
+// [T][H] values in blocks of 32 to e4m3 codes and the biased exponents of the blocks' scales
+hipError_t launch_pack_fp8(const void* x, int dt, int64_t T, int H, uint8_t* codes,
+                           uint8_t* scales, hipStream_t s);
+hipError_t launch_unpack_fp8(const uint8_t* codes, const uint8_t* scales, int64_t T, int H,
+                             void* x, int dt, hipStream_t s);
+
+}  // namespace moe

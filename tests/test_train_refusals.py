@@ -1,0 +1,204 @@
+"""Training the experts without a GPU: the C entry points refuse bad arguments before launching
+anything, and the binding refuses tensors of the wrong shape, type, layout or device before
+calling the library."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from mixture_experts_layer_30_amd import binding as B
+
+FAKE = 0x10000  # an aligned, never dereferenced address
+INV, UNS, CAP = B.MOE_EINVAL, B.MOE_EUNSUPPORTED, B.MOE_ECAPACITY
+BF, F32 = B.MOE_BF16, B.MOE_F32
+T, H, I, E, K = 128, 256, 192, 8, 2
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(B.LIB_PATH):
+        from mixture_experts_layer_30_amd import build
+        build.build()
+    return B.lib()
+
+
+def plan(cap=384, block_m=16, ptr=FAKE):
+    return ctypes.byref(B.moe_plan(ptr, ptr, ptr, ptr, ptr, block_m, cap - cap % block_m))
+
+
+def saved(format=B.SAVE_FP8, h=FAKE, scales=FAKE):
+    return ctypes.byref(B.moe_saved(format, h, scales))
+
+
+def call(fn, good, **bad):
+    assert set(bad) <= set(good), bad
+    return int(fn(*{**good, **bad}.values(), None))
+
+
+def expect(fn, good, table):
+    for status, bad in table:
+        assert call(fn, good, **bad) == status, bad
+        assert fn.__name__.encode() in B.lib().moe_last_error(), bad
+
+
+SIZES = [(INV, dict(T=-1)), (UNS, dict(T=1 << 31)), (UNS, dict(H=0)), (UNS, dict(H=200)),
+         (UNS, dict(I=0)), (UNS, dict(I=100)), (UNS, dict(H=(1 << 20) + 64)), (UNS, dict(I=1 << 21)),
+         (UNS, dict(H=1 << 15, I=1 << 15)), (INV, dict(saved=None)), (INV, dict(saved=saved(2))),
+         (INV, dict(saved=saved(h=None))), (INV, dict(saved=saved(h=FAKE + 8))),
+         (INV, dict(saved=saved(scales=None))), (CAP, dict(bytes=100)), (INV, dict(workspace=None)),
+         (INV, dict(workspace=FAKE + 8))]
+ROUTED = [(INV, dict(K=0)), (INV, dict(K=9)), (UNS, dict(E=257)), (INV, dict(plan=None)),
+          (INV, dict(plan=plan(ptr=0))), (INV, dict(plan=plan(ptr=FAKE + 2))),
+          (CAP, dict(plan=plan(cap=256))), (UNS, dict(plan=plan(block_m=2000, cap=4000))),
+          (UNS, dict(T=1 << 23))]
+
+
+def test_workspace_bytes(L):
+    assert L.moe_ffn_train_workspace_bytes(0, H, I) == 0
+    assert L.moe_ffn_train_workspace_bytes(384, H, I) == 384 * I * 2
+    assert L.moe_ffn_backward_workspace_bytes(384, H, I) == 384 * I * 6
+    for fn in (L.moe_ffn_train_workspace_bytes, L.moe_ffn_backward_workspace_bytes):
+        for bad in ((-1, H, I), (1 << 31, H, I), (1, 100, I), (1, H, 0), (1, H, 1 << 21)):
+            assert fn(*bad) == -1, bad
+
+
+def test_grouped_train(L):
+    n = L.moe_ffn_train_workspace_bytes(384, H, I)
+    good = dict(x=FAKE, T=T, H=H, I=I, E=E, K=K, w13=FAKE, w2=FAKE, plan=plan(), saved=saved(),
+                workspace=FAKE, bytes=n, rows=FAKE)
+    expect(L.moe_grouped_ffn_train, good, SIZES + ROUTED + [
+        (INV, dict(x=None)), (INV, dict(w13=None)), (INV, dict(w2=FAKE + 4)), (INV, dict(rows=None)),
+        (CAP, dict(bytes=n - 1))])
+    assert call(L.moe_grouped_ffn_train, good, T=0, x=None, rows=None, w13=None, plan=plan(cap=0),
+                saved=saved(h=None, scales=None), workspace=None, bytes=0) == B.MOE_OK
+
+
+def test_grouped_backward(L):
+    n = L.moe_ffn_backward_workspace_bytes(384, H, I)
+    good = dict(drows=FAKE, x=FAKE, T=T, H=H, I=I, E=E, K=K, w13=FAKE, w2=FAKE, plan=plan(),
+                saved=saved(), workspace=FAKE, bytes=n, dxrows=2 * FAKE, dw13=FAKE, dw2=FAKE, dwdt=BF)
+    expect(L.moe_grouped_ffn_backward, good, SIZES + ROUTED + [
+        (INV, dict(drows=None)), (INV, dict(x=None)), (INV, dict(w13=None)), (INV, dict(w2=None)),
+        (INV, dict(x=FAKE + 2, dw13=None)), (INV, dict(w13=FAKE + 2, dxrows=None)),
+        (INV, dict(dxrows=None, dw13=None, dw2=None)), (INV, dict(dxrows=FAKE)),
+        (INV, dict(dxrows=FAKE + 8)), (INV, dict(dw13=FAKE + 8)), (INV, dict(dw2=FAKE + 8)),
+        (UNS, dict(dwdt=2)), (CAP, dict(bytes=n - 1))])
+    assert call(L.moe_grouped_ffn_backward, good, T=0, drows=None, x=None, w13=None, w2=None,
+                plan=plan(cap=0), saved=saved(h=None, scales=None), workspace=None, bytes=0,
+                dw13=None, dw2=None) == B.MOE_OK
+
+
+def test_dense(L):
+    n = L.moe_ffn_train_workspace_bytes(T, H, I)
+    good = dict(x=FAKE, T=T, H=H, I=I, w13=FAKE, w2=FAKE, saved=saved(), workspace=FAKE, bytes=n,
+                out=FAKE)
+    expect(L.dense_ffn_train, good, SIZES + [
+        (INV, dict(x=None)), (INV, dict(w13=FAKE + 8)), (INV, dict(w2=None)), (INV, dict(out=None))])
+    n = L.moe_ffn_backward_workspace_bytes(T, H, I)
+    good = dict(dout=FAKE, x=FAKE, T=T, H=H, I=I, w13=FAKE, w2=FAKE, saved=saved(), workspace=FAKE,
+                bytes=n, dx=2 * FAKE, dw13=FAKE, dw2=FAKE, dwdt=F32)
+    expect(L.dense_ffn_backward, good, SIZES + [
+        (INV, dict(dout=None)), (INV, dict(dx=FAKE)), (INV, dict(dx=None, dw13=None, dw2=None)),
+        (INV, dict(w2=None)), (INV, dict(x=None)), (UNS, dict(dwdt=-1))])
+
+
+def test_pack(L):
+    good = dict(x=FAKE, dt=BF, T=T, H=H, codes=FAKE, scales=FAKE)
+    table = [(INV, dict(T=-1)), (UNS, dict(T=1 << 31)), (UNS, dict(H=40)), (UNS, dict(H=0)),
+             (UNS, dict(dt=2)), (INV, dict(x=None)), (INV, dict(x=FAKE + 8)),
+             (INV, dict(codes=None)), (INV, dict(codes=FAKE + 8)), (INV, dict(scales=None))]
+    expect(L.moe_pack_fp8, good, table)
+    assert call(L.moe_pack_fp8, good, T=0, x=None, codes=None, scales=None) == B.MOE_OK
+    good = dict(codes=FAKE, scales=FAKE, T=T, H=H, x=FAKE, dt=F32)
+    expect(L.moe_unpack_fp8, good, table)
+
+
+# ------------------------------------------------------------------ the binding
+
+
+def bf(*shape):
+    return torch.zeros(*shape, dtype=torch.bfloat16)
+
+
+def u8(*shape):
+    return torch.zeros(*shape, dtype=torch.uint8)
+
+
+def refused(status, fn, *args, **kw):
+    with pytest.raises(B.MoEError) as e:
+        fn(*args, **kw)
+    assert e.value.status == status, e.value
+    return str(e.value)
+
+
+def setup():
+    p = B.Plan(T, K, E, 16, "cpu")
+    s = B.Saved(p.cap, I, B.SAVE_FP8, "cpu")
+    return dict(x=bf(T, H), w13=bf(E, 2 * I, H), w2=bf(E, H, I), plan=p, saved=s,
+                workspace=u8(64), rows=bf(p.cap, H))
+
+
+def test_binding_grouped(L):
+    fn = B.moe_grouped_ffn_train
+    good = setup()
+    assert "GPU" in refused(INV, fn, **good)
+    cap = good["plan"].cap
+    for status, bad in [
+            (INV, dict(x=bf(T + 1, H))), (UNS, dict(x=torch.zeros(T, H))),
+            (INV, dict(x=bf(H, T).t())), (INV, dict(w13=bf(E, I, H))),
+            (UNS, dict(w13=torch.zeros(E, 2 * I, H))), (INV, dict(w2=bf(E, I, H))),
+            (INV, dict(w2=bf(H, I))), (INV, dict(rows=bf(cap - 1, H))), (UNS, dict(rows=torch.zeros(cap, H))),
+            (INV, dict(rows=bf(cap, 2 * H)[:, :H])), (INV, dict(saved=B.Saved(cap, 2 * I, B.SAVE_FP8, "cpu"))),
+            (INV, dict(saved=B.Saved(cap - 1, I, B.SAVE_FP8, "cpu"))),
+            (INV, dict(workspace=u8(64, 2)[:, 0]))]:
+        refused(status, fn, **{**good, **bad})
+    s = B.Saved(cap, I, B.SAVE_FP8, "cpu")
+    s.scales = None
+    refused(INV, fn, **{**good, "saved": s})
+    refused(INV, B.Saved, 4, I, 7, "cpu")
+
+
+def test_binding_backward(L):
+    fn = B.moe_grouped_ffn_backward
+    good = setup()
+    good["drows"] = good.pop("rows")
+    cap = good["plan"].cap
+    good.update(dxrows=bf(cap, H), dw13=bf(E, 2 * I, H), dw2=bf(E, H, I))
+    assert "GPU" in refused(INV, fn, **good)
+    for status, bad in [
+            (INV, dict(drows=bf(cap - 1, H))), (UNS, dict(drows=torch.zeros(cap, H))),
+            (INV, dict(x=bf(T + 1, H))), (INV, dict(dxrows=bf(cap, H + 64))),
+            (UNS, dict(dxrows=torch.zeros(cap, H))), (INV, dict(dw13=bf(E, H, 2 * I))),
+            (UNS, dict(dw13=torch.zeros(E, 2 * I, H))), (UNS, dict(dw13=None, dw2=torch.zeros(E, H, I).half())),
+            (INV, dict(dw2=bf(E, H, 2 * I)[:, :, :I])), (INV, dict(w2=bf(E, H)))]:
+        refused(status, fn, **{**good, **bad})
+
+
+def test_binding_dense(L):
+    s = B.Saved(T, I, B.SAVE_BF16, "cpu")
+    good = dict(x=bf(T, H), w13=bf(2 * I, H), w2=bf(H, I), saved=s, workspace=u8(64), out=bf(T, H))
+    assert "GPU" in refused(INV, B.dense_ffn_train, **good)
+    for status, bad in [(INV, dict(x=bf(T, H + 64))), (UNS, dict(x=torch.zeros(T, H))),
+                        (INV, dict(w13=bf(1, 2 * I, H))), (INV, dict(w2=bf(1, H, I))),
+                        (UNS, dict(out=torch.zeros(T, H))), (INV, dict(out=bf(T + 1, H))),
+                        (INV, dict(saved=B.Saved(T - 1, I, B.SAVE_BF16, "cpu")))]:
+        refused(status, B.dense_ffn_train, **{**good, **bad})
+    good = dict(dout=good.pop("out"), **good, dx=bf(T, H), dw13=bf(2 * I, H), dw2=bf(H, I))
+    assert "GPU" in refused(INV, B.dense_ffn_backward, **good)
+    for status, bad in [(INV, dict(dout=bf(T, H + 64))), (UNS, dict(dout=torch.zeros(T, H))),
+                        (INV, dict(x=bf(T + 1, H))), (INV, dict(dx=bf(T, 2 * H)[:, :H])),
+                        (INV, dict(dw2=bf(I, H)))]:
+        refused(status, B.dense_ffn_backward, **{**good, **bad})
+
+
+def test_binding_pack(L):
+    for fn, x in ((B.moe_pack_fp8, "x"), (B.moe_unpack_fp8, "x")):
+        good = dict(x=bf(T, H), codes=u8(T, H), scales=u8(T, H // 32))
+        assert "GPU" in refused(INV, fn, **good)
+        for status, bad in [(INV, dict(x=bf(T))), (INV, dict(codes=u8(T, H // 2))),
+                            (UNS, dict(codes=bf(T, H))), (INV, dict(scales=u8(T, H))),
+                            (UNS, dict(x=bf(T, 40), codes=u8(T, 40), scales=u8(T, 1))),
+                            (INV, dict(x=bf(H, T).t()))]:
+            refused(status, fn, **{**good, **bad})
+    refused(UNS, B.moe_pack_fp8, torch.zeros(T, H).half(), u8(T, H), u8(T, H // 32))

@@ -20,20 +20,6 @@ moe_status check_sorted(const char* what, int64_t T, int H, int E, int K, const 
   return check_plan(what, plan, T, K, E);
 }
 
-moe::RowMap plan_rows(const moe_plan* plan, int K) {
-  moe::RowMap rm{};
-  rm.counts = plan->expert_counts;
-  rm.offsets = plan->expert_offsets;
-  rm.sorted_ids = plan->sorted_ids;
-  rm.block_expert = plan->block_expert;
-  rm.inv_pos = plan->inv_pos;
-  rm.K = K;
-  rm.block_m = plan->block_m;
-  rm.min_rows = 1;
-  rm.max_rows = INT32_MAX;
-  return rm;
-}
-
 moe_status check_norm(const char* what, const char* name, const moe_norm_params* n, bool none_ok,
                       moe::NormSpec* out) {
   if (!n) return fail(MOE_EINVAL, "%s: %s is NULL", what, name);

@@ -1,4 +1,4 @@
-// Checks of arguments and their messages, shared by the C ABI of the operators around the
+// Checks of arguments, their messages and the plan as the kernels take it, shared by the C ABI of the operators around the
 // layer pass and of the training step.
 #pragma once
 
@@ -80,6 +80,20 @@ inline moe_status check_plan(const char* what, const moe_plan* plan, int64_t T, 
 
 inline moe_status null_pointer(const char* what) {
   return fail(MOE_EINVAL, "%s: NULL or misaligned pointer", what);
+}
+
+inline moe::RowMap plan_rows(const moe_plan* plan, int K) {
+  moe::RowMap rm{};
+  rm.counts = plan->expert_counts;
+  rm.offsets = plan->expert_offsets;
+  rm.sorted_ids = plan->sorted_ids;
+  rm.block_expert = plan->block_expert;
+  rm.inv_pos = plan->inv_pos;
+  rm.K = K;
+  rm.block_m = plan->block_m;
+  rm.min_rows = 1;
+  rm.max_rows = INT32_MAX;
+  return rm;
 }
 
 }  // namespace moe_checks

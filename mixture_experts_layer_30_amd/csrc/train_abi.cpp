@@ -84,8 +84,8 @@ moe_status forward(const char* what, const moe::TrainRows& r, const void* x, con
   return hip_status(e, what);
 }
 
-moe_status backward(const char* what, const moe::TrainRows& r, const void* dy, const void* x,
-                    const void* w13, const void* w2, const moe_saved* kept, void* workspace,
+moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* plan, const void* dy,
+                    const void* x, const void* w13, const void* w2, const moe_saved* kept, void* workspace,
                     int64_t workspace_bytes, void* dx, void* dw13, void* dw2, int dwdt,
                     void* stream) {
   if (dwdt != MOE_F32 && dwdt != MOE_BF16) return fail(MOE_EUNSUPPORTED, "%s: dwdt", what);
@@ -105,11 +105,20 @@ moe_status backward(const char* what, const moe::TrainRows& r, const void* dy, c
   }
   uint16_t* act = static_cast<uint16_t*>(workspace);
   uint16_t* dh = act + rounded(r.rows * r.I * 2) / 2;
+  uint16_t* x_rows = dh + rounded(r.rows * r.I * 4) / 2;
   const hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;
   if (r.tokens > 0) e = moe::launch_train_dact(r, w2, dy, saved, act, dh, s);
   if (e == hipSuccess && dx && r.tokens > 0) e = moe::launch_train_dx(r, w13, dh, dx, s);
-  if (e == hipSuccess && dw13) e = moe::launch_train_dw13(r, x, dh, dw13, dwdt == MOE_F32, s);
+  const uint16_t* xr = static_cast<const uint16_t*>(x);
+  if (e == hipSuccess && dw13 && plan && r.tokens > 0) {
+    // x by row: the contraction over rows then reads whole lines in order (gathering in it
+    // took the registers that hide its loads; the copy is 1% of a Mixtral-shaped backward)
+    e = moe::launch_permute(x, moe::kDtBF16, r.tokens, r.K, r.H, plan_rows(plan, r.K), r.E, r.rows,
+                            x_rows, s);
+    xr = x_rows;
+  }
+  if (e == hipSuccess && dw13) e = moe::launch_train_dw13(r, xr, dh, dw13, dwdt == MOE_F32, s);
   if (e == hipSuccess && dw2) e = moe::launch_train_dw2(r, act, dy, dw2, dwdt == MOE_F32, s);
   return hip_status(e, what);
 }
@@ -135,7 +144,8 @@ int64_t moe_ffn_train_workspace_bytes(int64_t rows, int H, int I) {
 
 int64_t moe_ffn_backward_workspace_bytes(int64_t rows, int H, int I) {
   const int64_t act = moe_ffn_train_workspace_bytes(rows, H, I);
-  return act < 0 ? -1 : act + rounded(rows * I * 4);
+  // a and dh of every row, and x by row
+  return act < 0 ? -1 : act + rounded(rows * I * 4) + rounded(rows * H * 2);
 }
 
 moe_status moe_grouped_ffn_train(const void* x, int64_t T, int H, int I, int E, int K,
@@ -157,7 +167,7 @@ moe_status moe_grouped_ffn_backward(const void* drows, const void* x, int64_t T,
   const char* what = "moe_grouped_ffn_backward";
   moe_status st = check_grouped(what, T, H, I, E, K, plan);
   if (st) return st;
-  return backward(what, planned(plan, T, E, K, H, I), drows, x, w13, w2, saved, workspace,
+  return backward(what, planned(plan, T, E, K, H, I), plan, drows, x, w13, w2, saved, workspace,
                   workspace_bytes, dxrows, dw13, dw2, dwdt, stream);
 }
 
@@ -177,7 +187,7 @@ moe_status dense_ffn_backward(const void* dout, const void* x, int64_t T, int H,
   const char* what = "dense_ffn_backward";
   moe_status st = check_ffn(what, T, H, I);
   if (st) return st;
-  return backward(what, dense(T, H, I), dout, x, w13, w2, saved, workspace, workspace_bytes, dx,
+  return backward(what, dense(T, H, I), nullptr, dout, x, w13, w2, saved, workspace, workspace_bytes, dx,
                   dw13, dw2, dwdt, stream);
 }
 

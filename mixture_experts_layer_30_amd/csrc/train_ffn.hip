@@ -16,9 +16,11 @@
 //
 //   along   a stage's 256 rows of 64 bytes; 16-byte segment s of row r at s ^ ((r >> 1) & 3);
 //           a fragment is one 16-byte read
-//   across  a stage's 32 rows of 512 bytes; segment s of row k at
-//           s ^ (3 ((k >> 3) & 1) | (k & 3) << 2); a fragment is two transposing 8-byte reads
-//           (a lane's 4 values of one column from 4 rows), spread over all banks by the swizzle
+//   across  a stage's 32 rows of 512 bytes in 16 chunks of two, k and k + 8, 64 bytes between
+//           the chunks; the segments of the second row at s ^ 3.  A fragment is two transposing
+//           8-byte reads (a lane's 4 values of one column from 4 rows): the gaps put the 4 rows
+//           that a read takes together in different quarters of the banks, and the swizzle k
+//           and k + 8 in different halves of those, so that 32 lanes meet every bank once
 //
 // Direct loads go through buffer descriptors, whose range check writes zeros for what lies
 // outside: rows past an expert's last one, features past an edge that is no multiple of 256.
@@ -38,16 +40,21 @@ namespace {
 constexpr int kTile = 256;                    // features, and rows, of a tile
 constexpr int kStep = 32;                     // contraction of a stage
 constexpr int kStages = 4;
-constexpr int kOperand = kTile * kStep * 2;   // bytes of an operand's stage
+constexpr int kAlong = kTile * kStep * 2;     // bytes of an operand's stage
+constexpr int kChunk = 2 * kTile * 2 + 64;    // two rows and a gap
+constexpr int kAcross = 16 * kChunk;
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kMaxE = 256;
 constexpr int TM = 8;                         // a wavefront's MFMA tiles of features
 constexpr uint32_t kOutside = 0xfffffff0u;    // an offset that every descriptor refuses
 
+template <bool kAAcross, bool kBAcross>
 struct Smem {
-  uint8_t a[kStages][kOperand];
-  uint8_t b[kStages][kOperand];
+  static constexpr int kA = kAAcross ? kAcross : kAlong;
+  static constexpr int kB = kBAcross ? kAcross : kAlong;
+  uint8_t a[kStages][kA];   // the features' operand
+  uint8_t b[kStages][kB];   // the rows'
   int tok[kTile];
   int pre[kMaxE + 1];
   int wsum[kWaves];
@@ -135,17 +142,18 @@ struct Along {
   }
 };
 
-// the row of a stage and the 16-byte segment that a lane fetches with load j
+// Chunk q = 2 wave + j of a stage: its first row, and the row and the 16-byte segment that a
+// lane fetches.
+__device__ __forceinline__ int chunk_row(int q) { return (q & 7) | (q >> 3) << 4; }
 __device__ __forceinline__ int across_row(const Lane& l, int j) {
-  return 2 * (2 * l.wave + j) + (l.lane >> 5);
+  return chunk_row(2 * l.wave + j) + ((l.lane >> 5) << 3);
 }
-__device__ __forceinline__ int across_key(int k) { return 3 * ((k >> 3) & 1) | (k & 3) << 2; }
-__device__ __forceinline__ int across_seg(const Lane& l, int j) {
-  return (l.lane & 31) ^ across_key(across_row(l, j));
+__device__ __forceinline__ int across_seg(const Lane& l) {
+  return (l.lane & 31) ^ (3 * (l.lane >> 5));
 }
 
 // Contraction across memory: rows of `row_bytes`, `rows` of them, the tile's features from
-// byte `col`; load j holds rows 4 wave + 2 j, + 1 of the stage.
+// byte 2 f0.
 struct Across {
   const uint8_t* base;
   uint32_t off[2];
@@ -157,7 +165,7 @@ struct Across {
     rows = n;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const uint32_t col = (uint32_t)f0 * 2 + (uint32_t)across_seg(l, j) * 16;
+      const uint32_t col = (uint32_t)f0 * 2 + (uint32_t)across_seg(l) * 16;
       off[j] = col < bytes ? (uint32_t)across_row(l, j) * bytes + col : kOutside;
     }
   }
@@ -166,7 +174,7 @@ struct Across {
     const int left = min(kStep, rows - step * kStep);
     const Rsrc r = make_rsrc(base + (size_t)step * kStep * row_bytes, (uint32_t)left * row_bytes);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) load_lds16(r, off[j], 0, stage + (2 * l.wave + j) * 1024);
+    for (int j = 0; j < 2; ++j) load_lds16(r, off[j], 0, stage + (2 * l.wave + j) * kChunk);
   }
 };
 
@@ -180,66 +188,30 @@ __device__ __forceinline__ uint32_t divided(const Divider& d, uint32_t p) {
   return __umulhi(p * 2, d.mul) >> d.shift;
 }
 
-// The same with the rows gathered: row k of the contraction is token ids[k] / K of x (one row
-// at least).  The ids are the same in half a wavefront, so they come by scalar loads, a step
-// ahead of their use.
-struct AcrossTokens {
-  Rsrc r;
-  const int32_t* ids;
-  Divider div;
-  uint32_t col[2], row_bytes, tokens;
-  int rows, next[4];
-  __device__ __forceinline__ void set(const Lane& l, const void* x, uint32_t T, uint32_t bytes,
-                                      const int32_t* p, int n, Divider d, int f0) {
-    r = make_rsrc(x, T * bytes);
-    ids = p;
-    div = d;
-    row_bytes = bytes;
-    tokens = T;
-    rows = n;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      col[j] = (uint32_t)f0 * 2 + (uint32_t)across_seg(l, j) * 16;
-      if (col[j] >= bytes) col[j] = kOutside;
-    }
-    fetch(l, 0);
-  }
-  __device__ __forceinline__ void fetch(const Lane& l, int step) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) next[q] = ids[min(step * kStep + 4 * l.wave + q, rows - 1)];
-  }
-  __device__ __forceinline__ void issue(const Lane& l, int step, uint8_t* stage) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int p = l.lane < 32 ? next[2 * j] : next[2 * j + 1];
-      const uint32_t t = divided(div, (uint32_t)p & 0x7fffffffu);
-      const bool in = step * kStep + across_row(l, j) < rows && p >= 0 && t < tokens &&
-                      col[j] != kOutside;
-      load_lds16(r, in ? t * row_bytes + col[j] : kOutside, 0, stage + (2 * l.wave + j) * 1024);
-    }
-    fetch(l, step + 1);
-  }
-};
-
 // ------------------------------------------------------------------ reading fragments
 
-// 8 values of the contraction for this lane's column, from byte `at` and 4 rows further
+// 8 values of the contraction for this lane's column, from byte `at` and 4 chunks further
 __device__ __forceinline__ u32x4 read_across(const uint8_t* at) {
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsVec4)at);
-  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsVec4)(at + 4 * kTile * 2));
+  const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsVec4)(at + 4 * kChunk));
   const uint2 a = __builtin_bit_cast(uint2, lo), b = __builtin_bit_cast(uint2, hi);
   return u32x4{a.x, a.y, b.x, b.y};
 }
 
-template <bool kAcross>
+// the byte of a stage of which this lane's transposing reads of row group g, row r, start
+__device__ __forceinline__ int across_at(const Lane& l) {
+  return ((l.m >> 2) + 8 * (l.g >> 1)) * kChunk + (l.g & 1) * (kTile * 2);
+}
+
+template <bool kIsAcross>
 __device__ __forceinline__ void read_features(const Lane& l, const uint8_t* stage, u32x4 (&f)[TM]) {
-  if constexpr (kAcross) {
-    const int r = l.m >> 2, c = l.m & 3;   // the row and the 4 features this lane points at
-    const int at = (8 * l.g + r) * (kTile * 2) + l.wm * 256 + (r << 6) +
-                   ((c ^ (3 * (l.g & 1))) << 4) + ((c & 1) << 3);
+  if constexpr (kIsAcross) {
+    const int c = l.m & 3;   // the 4 features this lane points at
+    const int at = across_at(l) + l.wm * 256 + ((c ^ (3 * (l.g & 1))) << 4) + ((c & 1) << 3);
+    const uint8_t* even = stage + at;
+    const uint8_t* odd = stage + (at ^ 8);
 #pragma unroll
-    for (int tm = 0; tm < TM; ++tm)
-      f[tm] = read_across(stage + (at ^ ((tm >> 1) << 6) ^ ((tm & 1) << 3)));
+    for (int tm = 0; tm < TM; ++tm) f[tm] = read_across((tm & 1 ? odd : even) + (tm >> 1) * 64);
   } else {
     const int at = (l.wm * 128 + l.m) * 64 + ((l.g ^ ((l.m >> 1) & 3)) << 4);
 #pragma unroll
@@ -248,14 +220,13 @@ __device__ __forceinline__ void read_features(const Lane& l, const uint8_t* stag
 }
 
 // the rows of wavefront column wn: tiles of 16 wn, wn + 4, ...
-template <bool kAcross, int TN>
+template <bool kIsAcross, int TN>
 __device__ __forceinline__ void read_rows(const Lane& l, const uint8_t* stage, u32x4 (&f)[TN]) {
-  if constexpr (kAcross) {
-    const int r = l.m >> 2, c = l.m & 3;
-    const int at = (8 * l.g + r) * (kTile * 2) +
-                   (((2 * l.wn + (c >> 1)) ^ (3 * (l.g & 1)) ^ (r << 2)) << 4) + ((c & 1) << 3);
+  if constexpr (kIsAcross) {
+    const int c = l.m & 3;
+    const int at = across_at(l) + (((2 * l.wn + (c >> 1)) ^ (3 * (l.g & 1))) << 4) + ((c & 1) << 3);
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn) f[tn] = read_across(stage + (at ^ (tn << 7)));
+    for (int tn = 0; tn < TN; ++tn) f[tn] = read_across(stage + at + tn * 128);
   } else {
     const int at = (l.wn * 16 + l.m) * 64 + ((l.g ^ ((l.m >> 1) & 3)) << 4);
 #pragma unroll
@@ -270,8 +241,15 @@ __device__ __forceinline__ void read_rows(const Lane& l, const uint8_t* stage, u
 // wavefront's reads of stage t are done; after it stage t's slot is free for stage t + 4.
 // The next item may fill the ring at once: every read was waited for at the last barrier.
 
+// The ring's slots come as pointers that do not alias, so that a read waits for the direct loads
+// into its own slot alone: the compiler otherwise has every transposing read wait for all of them
+// (measured: 620 TFLOP/s where both operands are read so, against the figures below).
 template <bool kAAcross, bool kBAcross, int TN, class LA, class LB>
-__device__ __forceinline__ void product(const Lane& l, Smem& sm, LA& la, LB& lb, int nk,
+__device__ __forceinline__ void product(const Lane& l, uint8_t* __restrict__ a0,
+                                        uint8_t* __restrict__ a1, uint8_t* __restrict__ a2,
+                                        uint8_t* __restrict__ a3, uint8_t* __restrict__ b0,
+                                        uint8_t* __restrict__ b1, uint8_t* __restrict__ b2,
+                                        uint8_t* __restrict__ b3, LA& la, LB& lb, int nk,
                                         f32x4 (&acc)[TM][TN]) {
 #pragma unroll
   for (int tm = 0; tm < TM; ++tm)
@@ -279,27 +257,47 @@ __device__ __forceinline__ void product(const Lane& l, Smem& sm, LA& la, LB& lb,
     for (int tn = 0; tn < TN; ++tn) acc[tm][tn] = f32x4{0.f, 0.f, 0.f, 0.f};
   if (nk == 0) return;
 
-  auto issue = [&](int t, int slot) {
-    la.issue(l, t, sm.a[slot]);
-    lb.issue(l, t, sm.b[slot]);
+  u32x4 fa[2][TM], fb[2][TN];
+  auto slot_a = [&](auto s) -> uint8_t* {
+    constexpr int k = decltype(s)::value % kStages;
+    if constexpr (k == 0) return a0;
+    else if constexpr (k == 1) return a1;
+    else if constexpr (k == 2) return a2;
+    else return a3;
   };
-  auto ops = [&](const u32x4 (&fa)[TM], const u32x4 (&fb)[TN]) {
+  auto slot_b = [&](auto s) -> uint8_t* {
+    constexpr int k = decltype(s)::value % kStages;
+    if constexpr (k == 0) return b0;
+    else if constexpr (k == 1) return b1;
+    else if constexpr (k == 2) return b2;
+    else return b3;
+  };
+  auto issue = [&](int t, auto s) {
+    la.issue(l, t, slot_a(s));
+    lb.issue(l, t, slot_b(s));
+  };
+  auto read = [&](auto s) {
+    constexpr int k = decltype(s)::value;
+    read_features<kAAcross>(l, slot_a(s), fa[k & 1]);
+    read_rows<kBAcross, TN>(l, slot_b(s), fb[k & 1]);
+  };
+  auto ops = [&](auto s) {
+    constexpr int k = decltype(s)::value & 1;
 #pragma unroll
     for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm) acc[tm][tn] = mfma16x16x32(fa[tm], fb[tn], acc[tm][tn]);
+      for (int tm = 0; tm < TM; ++tm)
+        acc[tm][tn] = mfma16x16x32(fa[k][tm], fb[k][tn], acc[tm][tn]);
   };
-  u32x4 fa[2][TM], fb[2][TN];
-  // the steady form (t + 4 < nk) has no conditions
-  auto steady = [&](int t, auto slot) {
-    constexpr int s = decltype(slot)::value, cur = s & 1, nxt = cur ^ 1;
+  // step t, of slot s: the steady form (t + 4 < nk) has no conditions
+  auto steady = [&](int t, auto s) {
+    constexpr int k = decltype(s)::value;
     wait_vm<8>();
     wait_lgkm0();
     barrier();
     issue(t + 4, s);
-    read_features<kAAcross>(l, sm.a[(s + 1) % kStages], fa[nxt]);
-    read_rows<kBAcross, TN>(l, sm.b[(s + 1) % kStages], fb[nxt]);
-    ops(fa[cur], fb[cur]);
+    read(std::integral_constant<int, k + 1>{});
+    ops(s);
     // the direct loads, then the reads one by one between the first ops, and no op moved
     // past the next barrier, whose wait would then find the matrix pipe empty
     constexpr int kReads = TM * (kAAcross ? 2 : 1) + TN * (kBAcross ? 2 : 1);
@@ -312,19 +310,16 @@ __device__ __forceinline__ void product(const Lane& l, Smem& sm, LA& la, LB& lb,
     }
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto last = [&](int t, auto cur_c) {
-    constexpr int cur = decltype(cur_c)::value, nxt = cur ^ 1;
+  auto last = [&](int t, auto s) {
+    constexpr int k = decltype(s)::value;
     if (t + 3 < nk) wait_vm<8>();
     else if (t + 2 < nk) wait_vm<4>();
     else wait_vm<0>();
     wait_lgkm0();
     barrier();
-    if (t + 4 < nk) issue(t + 4, t % kStages);
-    if (t + 1 < nk) {
-      read_features<kAAcross>(l, sm.a[(t + 1) % kStages], fa[nxt]);
-      read_rows<kBAcross, TN>(l, sm.b[(t + 1) % kStages], fb[nxt]);
-    }
-    ops(fa[cur], fb[cur]);
+    if (t + 4 < nk) issue(t + 4, s);
+    if (t + 1 < nk) read(std::integral_constant<int, k + 1>{});
+    ops(s);
     __builtin_amdgcn_sched_barrier(0);
   };
   using C0 = std::integral_constant<int, 0>;
@@ -332,16 +327,16 @@ __device__ __forceinline__ void product(const Lane& l, Smem& sm, LA& la, LB& lb,
   using C2 = std::integral_constant<int, 2>;
   using C3 = std::integral_constant<int, 3>;
 
-#pragma unroll
-  for (int s = 0; s < kStages; ++s)
-    if (s < nk) issue(s, s);
-  if (nk >= 4) wait_vm<12>();
+  issue(0, C0{});
+  if (nk > 1) issue(1, C1{});
+  if (nk > 2) issue(2, C2{});
+  if (nk > 3) issue(3, C3{});
+  if (nk > 3) wait_vm<12>();
   else if (nk == 3) wait_vm<8>();
   else if (nk == 2) wait_vm<4>();
   else wait_vm<0>();
   barrier();
-  read_features<kAAcross>(l, sm.a[0], fa[0]);
-  read_rows<kBAcross, TN>(l, sm.b[0], fb[0]);
+  read(C0{});
   int t = 0;
   for (; t + 7 < nk; t += 4) {
     steady(t, C0{});
@@ -349,10 +344,14 @@ __device__ __forceinline__ void product(const Lane& l, Smem& sm, LA& la, LB& lb,
     steady(t + 2, C2{});
     steady(t + 3, C3{});
   }
-  for (; t < nk; t += 2) {
-    last(t, C0{});
-    if (t + 1 < nk) last(t + 1, C1{});
-  }
+  // 1 to 7 steps left
+  last(t, C0{});
+  if (t + 1 < nk) last(t + 1, C1{});
+  if (t + 2 < nk) last(t + 2, C2{});
+  if (t + 3 < nk) last(t + 3, C3{});
+  if (t + 4 < nk) last(t + 4, C0{});
+  if (t + 5 < nk) last(t + 5, C1{});
+  if (t + 6 < nk) last(t + 6, C2{});
 }
 
 // ------------------------------------------------------------------ storing
@@ -436,8 +435,8 @@ __device__ __forceinline__ void kept8(const Args& a, size_t row, int col, float*
 
 // One item of the products over rows: features f0 .. of the tile, rows row0 .. row0 + n - 1 of
 // expert e, n <= 64 TN.
-template <Op kOp, bool kFp8, int TN>
-__device__ __forceinline__ void rows_item(const Args& a, const Lane& l, Smem& sm, int e, int f0,
+template <Op kOp, bool kFp8, int TN, class Sm>
+__device__ __forceinline__ void rows_item(const Args& a, const Lane& l, Sm& sm, int e, int f0,
                                           int64_t row0, int n) {
   const int H = a.r.H, I = a.r.I;
   f32x4 acc[TM][TN];
@@ -473,12 +472,14 @@ __device__ __forceinline__ void rows_item(const Args& a, const Lane& l, Smem& sm
       }
       return (uint32_t)f * row_bytes;
     });
-    product<false, false, TN>(l, sm, feats, rows, nk, acc);
+    product<false, false, TN>(l, sm.a[0], sm.a[1], sm.a[2], sm.a[3], sm.b[0], sm.b[1],
+                             sm.b[2], sm.b[3], feats, rows, nk, acc);
   } else {
     Across feats;
     const int F = kOp == kDAct ? I : H;
     feats.set(l, a.w + (size_t)e * Kdim * F, (uint32_t)F * 2, Kdim, f0);
-    product<true, false, TN>(l, sm, feats, rows, nk, acc);
+    product<true, false, TN>(l, sm.a[0], sm.a[1], sm.a[2], sm.a[3], sm.b[0], sm.b[1],
+                             sm.b[2], sm.b[3], feats, rows, nk, acc);
   }
 
 #pragma unroll
@@ -546,7 +547,7 @@ __device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int64_t* r
 // tile run side by side on one L2.
 template <Op kOp, bool kFp8>
 __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
-  __shared__ __attribute__((aligned(1024))) Smem sm;
+  __shared__ __attribute__((aligned(1024))) Smem<kOp == kDAct || kOp == kDX, false> sm;
   const Lane l;
   const int nexp = a.r.counts ? a.r.E : 1;
   const int per_tile = kOp == kGateUp ? kTile / 2 : kTile;
@@ -614,16 +615,15 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
 // contraction the expert's rows; an expert without rows gets zeros.
 struct WeightArgs {
   TrainRows r;
-  Divider div;
-  const uint16_t* m_rows;   // x (kTokens: gathered by token) or rows
+  const uint16_t* m_rows;
   const uint16_t* n_rows;
   void* out;
   int M, N;
 };
 
-template <bool kTokens, class TOut>
+template <class TOut>
 __global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
-  __shared__ __attribute__((aligned(1024))) Smem sm;
+  __shared__ __attribute__((aligned(1024))) Smem<true, true> sm;
   const Lane l;
   const int E = a.r.counts ? a.r.E : 1;
   const int tm_n = (a.M + kTile - 1) / kTile, tn_n = (a.N + kTile - 1) / kTile;
@@ -647,17 +647,10 @@ __global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
     f32x4 acc[TM][4];
     Across nr;
     nr.set(l, a.n_rows + (size_t)row0 * a.N, (uint32_t)a.N * 2, n, n0);
-    if constexpr (kTokens) {
-      AcrossTokens mr;
-      if (n > 0)
-        mr.set(l, a.m_rows, (uint32_t)a.r.tokens, (uint32_t)a.M * 2, a.r.sorted_ids + row0, n, a.div,
-               m0);
-      product<true, true, 4>(l, sm, mr, nr, nk, acc);
-    } else {
-      Across mr;
-      mr.set(l, a.m_rows + (size_t)row0 * a.M, (uint32_t)a.M * 2, n, m0);
-      product<true, true, 4>(l, sm, mr, nr, nk, acc);
-    }
+    Across mr;
+    mr.set(l, a.m_rows + (size_t)row0 * a.M, (uint32_t)a.M * 2, n, m0);
+    product<true, true, 4>(l, sm.a[0], sm.a[1], sm.a[2], sm.a[3], sm.b[0], sm.b[1], sm.b[2],
+                           sm.b[3], mr, nr, nk, acc);
     TOut* out = static_cast<TOut*>(a.out) + (size_t)e * a.M * a.N;
 #pragma unroll
     for (int tn4 = 0; tn4 < 4; ++tn4) {
@@ -712,16 +705,12 @@ hipError_t launch_rows(const Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <bool kTokens>
 hipError_t launch_weights(const WeightArgs& a, bool f32, hipStream_t s) {
   const int64_t items = (int64_t)(a.r.counts ? a.r.E : 1) * ((a.M + kTile - 1) / kTile) *
                         ((a.N + kTile - 1) / kTile);
-  if (f32)
-    hipLaunchKernelGGL((weights_kernel<kTokens, float>), dim3(grid_of(items)), dim3(kThreads), 0, s,
-                       a);
-  else
-    hipLaunchKernelGGL((weights_kernel<kTokens, uint16_t>), dim3(grid_of(items)), dim3(kThreads), 0,
-                       s, a);
+  const dim3 grid(grid_of(items)), block(kThreads);
+  if (f32) hipLaunchKernelGGL(weights_kernel<float>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(weights_kernel<uint16_t>, grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -775,16 +764,14 @@ hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* 
   return launch_rows<kDX, false>(a, s);
 }
 
-hipError_t launch_train_dw13(const TrainRows& r, const void* x, const uint16_t* dh, void* dw13,
-                             bool f32, hipStream_t s) {
-  const WeightArgs a{r, divider(r.K), static_cast<const uint16_t*>(x), dh, dw13, r.H, 2 * r.I};
-  return r.counts ? launch_weights<true>(a, f32, s) : launch_weights<false>(a, f32, s);
+hipError_t launch_train_dw13(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
+                             void* dw13, bool f32, hipStream_t s) {
+  return launch_weights(WeightArgs{r, x_rows, dh, dw13, r.H, 2 * r.I}, f32, s);
 }
 
 hipError_t launch_train_dw2(const TrainRows& r, const uint16_t* act, const void* dy, void* dw2,
                             bool f32, hipStream_t s) {
-  const WeightArgs a{r, divider(r.K), act, static_cast<const uint16_t*>(dy), dw2, r.I, r.H};
-  return launch_weights<false>(a, f32, s);
+  return launch_weights(WeightArgs{r, act, static_cast<const uint16_t*>(dy), dw2, r.I, r.H}, f32, s);
 }
 
 }  // namespace moe

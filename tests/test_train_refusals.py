@@ -57,7 +57,7 @@ ROUTED = [(INV, dict(K=0)), (INV, dict(K=9)), (UNS, dict(E=257)), (INV, dict(pla
 def test_workspace_bytes(L):
     assert L.moe_ffn_train_workspace_bytes(0, H, I) == 0
     assert L.moe_ffn_train_workspace_bytes(384, H, I) == 384 * I * 2
-    assert L.moe_ffn_backward_workspace_bytes(384, H, I) == 384 * I * 6
+    assert L.moe_ffn_backward_workspace_bytes(384, H, I) == 384 * (I * 6 + H * 2)
     for fn in (L.moe_ffn_train_workspace_bytes, L.moe_ffn_backward_workspace_bytes):
         for bad in ((-1, H, I), (1 << 31, H, I), (1, 100, I), (1, H, 0), (1, H, 1 << 21)):
             assert fn(*bad) == -1, bad

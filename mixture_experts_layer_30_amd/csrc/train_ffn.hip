@@ -10,21 +10,32 @@
 // Six products in three forms, by which index runs along memory.  In the forward both operands
 // have the contraction there ("along"); in da and dx the weights have it across their rows; in
 // the weights' gradients both operands do, since the contraction is over rows ("across").
-// All run on one tile: 256 features x 256 rows (or features), 8 wavefronts as 2 x 4 of
-// 128 x 64 with 16x16x32 bf16 MFMAs, the contraction in steps of 32 through a ring of 4 stages
-// of 32 KB in LDS, filled by direct loads three steps ahead.
 //
-//   along   a stage's 256 rows of 64 bytes; 16-byte segment s of row r at s ^ ((r >> 1) & 3);
+// All run on one tile, 256 features x 256 rows (or features), by 8 wavefronts as 2 x 4 of
+// 128 x 64 with 16x16x32 bf16 MFMAs, in blocks of 64 of the contraction.  A block is four units
+// of 16 KB, the halves of either operand, each with two slots in LDS that direct loads fill.  A
+// wavefront takes a block in four phases, a quarter of its tile each (16 MFMAs), in the order
+// (A0,Bf) (A0,Bg) (A1,Bg) (A1,Bf), f and g changing places with the block: each phase needs one
+// set of fragments that is not in registers yet, and refills the slot that the phase before has
+// read.  So a load has seven phases to land, and 96 KB a CU are in flight.
+// (Blocks of 32 in a ring of four stages read 64 bytes of a row at a time, half a line, and the
+// 32 KB of L1 hold the other half no longer than a step: Mixtral-shaped gate/up of 4096 tokens
+// at 985 TFLOP/s.)
+//
+//   along   a unit's 128 rows of 128 bytes; 16-byte segment s of row r at s ^ ((r >> 1) & 7);
 //           a fragment is one 16-byte read
-//   across  a stage's 32 rows of 512 bytes in 16 chunks of two, k and k + 8, 64 bytes between
-//           the chunks; the segments of the second row at s ^ 3.  A fragment is two transposing
-//           8-byte reads (a lane's 4 values of one column from 4 rows): the gaps put the 4 rows
-//           that a read takes together in different quarters of the banks, and the swizzle k
-//           and k + 8 in different halves of those, so that 32 lanes meet every bank once
+//   across  a unit's 64 rows of 256 bytes in 16 chunks of four, k, k + 8, k + 16, k + 24, with
+//           64 bytes between the chunks; the segments of the second and fourth at s ^ 3.  A
+//           fragment is two transposing 8-byte reads (a lane's 4 values of one column from 4
+//           rows): the gaps put the 4 rows that a read takes together in different quarters of
+//           the banks, the swizzle k and k + 8 in different halves of those, so that 32 lanes
+//           meet every bank once
 //
-// Direct loads go through buffer descriptors, whose range check writes zeros for what lies
-// outside: rows past an expert's last one, features past an edge that is no multiple of 256.
-// So every step runs the same instructions, and nothing outside a matrix is read.
+// Direct loads go through buffer descriptors, whose range check (of the lane's and the scalar
+// offset together) writes zeros for what lies outside: rows past an expert's last one, features past an edge that is no multiple of 256,
+// blocks past the end.  So every block runs the same instructions, and nothing outside a matrix
+// is read.  The blocks of a workgroup's items are one stream: the loads of an item begin while
+// the one before is worked on.
 //
 // The features of a tile are dealt to MFMA rows so that a lane's sums of two neighbouring MFMA
 // tiles are 8 neighbours in memory (feature(): 16-byte stores, 64 bytes of a row side by side).
@@ -37,42 +48,60 @@ namespace moe {
 
 namespace {
 
-constexpr int kTile = 256;                    // features, and rows, of a tile
-constexpr int kStep = 32;                     // contraction of a stage
-constexpr int kStages = 4;
-constexpr int kAlong = kTile * kStep * 2;     // bytes of an operand's stage
-constexpr int kChunk = 2 * kTile * 2 + 64;    // two rows and a gap
-constexpr int kAcross = 16 * kChunk;
+constexpr int kTile = 256;                // features, and rows, of a tile
+constexpr int kHalf = 128;
+constexpr int kBlock = 64;                // contraction of a block
+constexpr int kChunk = 4 * kHalf * 2 + 64;   // four rows and a gap, across
+constexpr int kUnit = 16 * kChunk;        // bytes of a unit (along: 16 KB of them)
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * kWave;
 constexpr int kMaxE = 256;
-constexpr int TM = 8;                         // a wavefront's MFMA tiles of features
+constexpr int TM = 8, TN = 4;             // a wavefront's MFMA tiles of features, and of rows
 constexpr uint32_t kOutside = 0xfffffff0u;    // an offset that every descriptor refuses
 
-template <bool kAAcross, bool kBAcross>
-struct Smem {
-  static constexpr int kA = kAAcross ? kAcross : kAlong;
-  static constexpr int kB = kBAcross ? kAcross : kAlong;
-  uint8_t a[kStages][kA];   // the features' operand
-  uint8_t b[kStages][kB];   // the rows'
-  int tok[kTile];
-  int pre[kMaxE + 1];
-  int wsum[kWaves];
+// The units: each a variable of its own, see stream()
+#define TRAIN_UNITS                                                                          \
+  __shared__ __attribute__((aligned(128))) uint8_t a00[kUnit], a01[kUnit], a10[kUnit], a11[kUnit]; \
+  __shared__ __attribute__((aligned(128))) uint8_t b00[kUnit], b01[kUnit], b10[kUnit], b11[kUnit]; \
+  const Units units{a00, a01, a10, a11, b00, b01, b10, b11}
+
+// [half][slot] of the features' operand, and of the rows'
+struct Units {
+  uint8_t *a00, *a01, *a10, *a11, *b00, *b01, *b10, *b11;
 };
 
-enum Op { kGateUp, kDown, kDAct, kDX, kDW13, kDW2 };
+// what a job keeps in LDS
+struct Smem {
+  int pre[kMaxE + 1];
+  int wsum[kWaves];
+  int rows[kMaxE];
+};
+
+enum Op { kGateUp, kDown, kDAct, kDX };
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void* LdsPtr;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* LdsVec4;
 
+// A value that is the same in every lane, in a scalar register: descriptors are built of them
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
+__device__ __forceinline__ const uint8_t* uniform(const void* p) {
+  const uint64_t v = (uint64_t)p;
+  return (const uint8_t*)((uint64_t)uniform((uint32_t)(v >> 32)) << 32 | uniform((uint32_t)v));
+}
+
 __device__ __forceinline__ Rsrc make_rsrc(const void* p, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, bytes, 0x00020000);
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(uniform(p)), 0, uniform(bytes),
+                                           0x00020000);
 }
 
 __device__ __forceinline__ void load_lds16(Rsrc r, uint32_t lane_off, uint32_t off, void* lds) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 16, (int)lane_off, (int)off, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (LdsPtr)lds, 16, (int)lane_off, (int)uniform(off), 0,
+                                           0);
 }
 
 __device__ __forceinline__ void barrier() { asm volatile("s_barrier" ::: "memory"); }
@@ -87,11 +116,11 @@ __device__ __forceinline__ void wait_lgkm0() {
   __builtin_amdgcn_s_waitcnt(15 | (3 << 14) | (0x7 << 4) | (0 << 8));
 }
 
-// what a lane is, in the block and in an MFMA
+// what a lane is, in the workgroup and in an MFMA
 struct Lane {
   int tid, lane, wave, wm, wn, m, g;
-  __device__ __forceinline__ Lane() {
-    tid = threadIdx.x;
+  __device__ __forceinline__ explicit Lane(int thread) {
+    tid = thread;
     lane = tid & (kWave - 1);
     wave = __builtin_amdgcn_readfirstlane(tid / kWave);   // so that its indices stay scalar
     wm = wave >> 2;
@@ -99,14 +128,21 @@ struct Lane {
     m = lane & 15;
     g = lane >> 4;
   }
+  // The same, worked out again: what is used between items alone keeps no register over the
+  // product, whose sums and fragments take 224 of 256.
+  __device__ __forceinline__ Lane again() const {
+    int t = tid;
+    asm volatile("" : "+v"(t));
+    return Lane(t);
+  }
 };
 
-// Feature (of a tile's 256) of MFMA tile tm (of 8 of wavefront row wm), row 4c + j: the pair of
-// tiles tm, tm ^ 1 holds 32 neighbours, and lane group c of the two 8 neighbours, 4 in each.
-// Which tile has the first 4 alternates with c, so that the transposing reads of one tile use
-// both halves of the 16-byte segments and with them every bank.
-__device__ __forceinline__ int feature(int wm, int tm, int c, int j) {
-  return wm * 128 + 32 * (tm >> 1) + 8 * c + 4 * ((c ^ tm) & 1) + j;
+// Feature (of a half's 64 of wavefront row wm) of MFMA tile t (of 4), row 4c + j: a pair of tiles
+// t, t ^ 1 holds 32 neighbours, and lane group c of the two 8 neighbours, 4 in each.  Which tile
+// has the first 4 alternates with c, so that the transposing reads of one tile use both halves
+// of the 16-byte segments and with them every bank.
+__device__ __forceinline__ int feature(int t, int c, int j) {
+  return 32 * (t >> 1) + 8 * c + 4 * ((c ^ t) & 1) + j;
 }
 
 // The 8 sums of a lane in a pair of tiles, in the order of their features
@@ -116,65 +152,109 @@ __device__ __forceinline__ void in_order(int g, f32x4 even, f32x4 odd, float* v)
   v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
 }
 
-// ------------------------------------------------------------------ filling a stage
-//
-// A wavefront's two direct loads j = 0, 1 fill KB 2 wave + j of an operand's 16 KB.
+// the first feature of the 8 of pair p (of 4) of a lane's tiles
+__device__ __forceinline__ int pair_feature(const Lane& l, int p) {
+  return kHalf * (p >> 1) + 64 * l.wm + 32 * (p & 1) + 8 * l.g;
+}
 
-// Contraction along memory: load j holds rows 16 (2 wave + j) .. + 15, 4 lanes a row.
-// row_off(r): the byte offset of the operand's row r, or kOutside.
+// the row of a lane's sums in MFMA tile tn
+__device__ __forceinline__ int tile_row(const Lane& l, int tn) { return (l.wn + 4 * tn) * 16 + l.m; }
+
+// ------------------------------------------------------------------ filling a unit
+//
+// A wavefront's two direct loads j = 0, 1 fill KB (or chunk) 2 wave + j of a unit's 16.  at()
+// sets the block that issue() loads; `live` false: zeros.  Rows and features that the result has
+// no place for may hold anything (their sums are not stored), rows of the contraction that are
+// not there hold zeros.
+
+// Contraction along memory: load j has rows 16 wave + 8 j .. + 7 of the half, 8 lanes a row.
+__device__ __forceinline__ int along_row(const Lane& l, int j) {
+  return 16 * l.wave + 8 * j + (l.lane >> 3);
+}
+__device__ __forceinline__ uint32_t along_seg(const Lane& l, int j) {
+  return (uint32_t)(((l.lane & 7) ^ ((4 * j + (l.lane >> 4)) & 7)) << 4);   // (row >> 1) & 7
+}
+
 struct Along {
-  Rsrc r;
-  uint32_t off[2];
+  const uint8_t* base;
+  uint32_t bytes, half, off[2], k, n;
+  // row_off(r): the byte offset of row r of the first half; the second half's are `half_bytes`
+  // further
   template <class F>
-  __device__ __forceinline__ void set(const Lane& l, Rsrc rs, F row_off) {
-    r = rs;
+  __device__ __forceinline__ void set(const Lane& l, const void* p, uint32_t all, uint32_t half_bytes,
+                                      F row_off) {
+    base = uniform(p);
+    bytes = uniform(all);
+    half = uniform(half_bytes);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const int row = 16 * (2 * l.wave + j) + (l.lane >> 2);
-      const uint32_t o = row_off(row);
-      off[j] = o == kOutside ? o : o + (uint32_t)(((l.lane & 3) ^ ((row >> 1) & 3)) << 4);
-    }
+    for (int j = 0; j < 2; ++j) off[j] = row_off(along_row(l, j)) + along_seg(l, j);
   }
-  __device__ __forceinline__ void issue(const Lane& l, int step, uint8_t* stage) {
+  __device__ __forceinline__ void at(int block, bool live) {
+    k = (uint32_t)block * (kBlock * 2);
+    n = uniform(live ? bytes : 0);
+  }
+  __device__ __forceinline__ void issue(const Lane& l, int h, uint8_t* unit) const {
+    const Rsrc r = make_rsrc(base, n);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      load_lds16(r, off[j], (uint32_t)step * (kStep * 2), stage + (2 * l.wave + j) * 1024);
+      load_lds16(r, off[j], k + (h ? half : 0), unit + (2 * l.wave + j) * 1024);
   }
 };
 
-// Chunk q = 2 wave + j of a stage: its first row, and the row and the 16-byte segment that a
-// lane fetches.
-__device__ __forceinline__ int chunk_row(int q) { return (q & 7) | (q >> 3) << 4; }
-__device__ __forceinline__ int across_row(const Lane& l, int j) {
-  return chunk_row(2 * l.wave + j) + ((l.lane >> 5) << 3);
-}
-__device__ __forceinline__ int across_seg(const Lane& l) {
-  return (l.lane & 31) ^ (3 * (l.lane >> 5));
-}
+// The same with rows of their own places.
+struct Gathered {
+  const uint8_t* base;
+  uint32_t bytes, off[2][2], k, n;
+  // row_off(r): the byte offset of the operand's row r, or kOutside
+  template <class F>
+  __device__ __forceinline__ void set(const Lane& l, const void* p, uint32_t all, F row_off) {
+    base = uniform(p);
+    bytes = uniform(all);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t o = row_off(kHalf * h + along_row(l, j));
+        off[h][j] = o == kOutside ? o : o + along_seg(l, j);
+      }
+  }
+  __device__ __forceinline__ void at(int block, bool live) {
+    k = (uint32_t)block * (kBlock * 2);
+    n = uniform(live ? bytes : 0);
+  }
+  __device__ __forceinline__ void issue(const Lane& l, int h, uint8_t* unit) const {
+    const Rsrc r = make_rsrc(base, n);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) load_lds16(r, off[h][j], k, unit + (2 * l.wave + j) * 1024);
+  }
+};
 
-// Contraction across memory: rows of `row_bytes`, `rows` of them, the tile's features from
-// byte 2 f0.
+// Contraction across memory: `rows` rows of `row_bytes`, the tile's features from f0 on.  Chunk q
+// has rows (q & 7) + 32 (q >> 3) and the three that follow 8 apart, 16 lanes a row.
 struct Across {
   const uint8_t* base;
-  uint32_t off[2];
-  uint32_t row_bytes;
+  uint32_t off, row_bytes, col, left;
   int rows;
   __device__ __forceinline__ void set(const Lane& l, const void* p, uint32_t bytes, int n, int f0) {
-    base = static_cast<const uint8_t*>(p);
-    row_bytes = bytes;
-    rows = n;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t col = (uint32_t)f0 * 2 + (uint32_t)across_seg(l) * 16;
-      off[j] = col < bytes ? (uint32_t)across_row(l, j) * bytes + col : kOutside;
-    }
+    base = uniform(p);
+    row_bytes = uniform(bytes);
+    rows = uniform(n);
+    col = uniform((uint32_t)f0 * 2);
+    const uint32_t row = (uint32_t)(((2 * l.wave) & 7) + 32 * (l.wave >> 2) + 8 * l.g);
+    off = row * bytes + (uint32_t)((l.lane & 15) ^ (3 * (l.g & 1))) * 16;
   }
-  __device__ __forceinline__ void issue(const Lane& l, int step, uint8_t* stage) {
-    // the stage's rows alone: any number of them, of matrices of any size, and the rest zeros
-    const int left = min(kStep, rows - step * kStep);
-    const Rsrc r = make_rsrc(base + (size_t)step * kStep * row_bytes, (uint32_t)left * row_bytes);
+  // The descriptor holds the block's rows alone: any number of them, of matrices of any size,
+  // and the rest zeros.  Blocks come in order: the base moves on with them.
+  __device__ __forceinline__ void at(int block, bool live) {
+    if (block > 0) base += (size_t)kBlock * row_bytes;
+    left = uniform(live ? (uint32_t)min(kBlock, rows - block * kBlock) * row_bytes : 0);
+  }
+  __device__ __forceinline__ void issue(const Lane& l, int h, uint8_t* unit) const {
+    const Rsrc r = make_rsrc(base, left);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) load_lds16(r, off[j], 0, stage + (2 * l.wave + j) * kChunk);
+    for (int j = 0; j < 2; ++j)
+      load_lds16(r, off, (uint32_t)j * row_bytes + col + (uint32_t)h * (kHalf * 2),
+                 unit + (2 * l.wave + j) * kChunk);
   }
 };
 
@@ -189,8 +269,10 @@ __device__ __forceinline__ uint32_t divided(const Divider& d, uint32_t p) {
 }
 
 // ------------------------------------------------------------------ reading fragments
+//
+// [ks]: the two steps of 32 of a block
 
-// 8 values of the contraction for this lane's column, from byte `at` and 4 chunks further
+// 8 values of the contraction for this lane's column, from byte `at` and 4 rows further
 __device__ __forceinline__ u32x4 read_across(const uint8_t* at) {
   const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsVec4)at);
   const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((LdsVec4)(at + 4 * kChunk));
@@ -198,179 +280,294 @@ __device__ __forceinline__ u32x4 read_across(const uint8_t* at) {
   return u32x4{a.x, a.y, b.x, b.y};
 }
 
-// the byte of a stage of which this lane's transposing reads of row group g, row r, start
-__device__ __forceinline__ int across_at(const Lane& l) {
-  return ((l.m >> 2) + 8 * (l.g >> 1)) * kChunk + (l.g & 1) * (kTile * 2);
-}
-
+// 4 tiles of features
 template <bool kIsAcross>
-__device__ __forceinline__ void read_features(const Lane& l, const uint8_t* stage, u32x4 (&f)[TM]) {
+__device__ __forceinline__ void read_features(const Lane& l, const uint8_t* unit, u32x4 (&f)[2][4]) {
   if constexpr (kIsAcross) {
-    const int c = l.m & 3;   // the 4 features this lane points at
-    const int at = across_at(l) + l.wm * 256 + ((c ^ (3 * (l.g & 1))) << 4) + ((c & 1) << 3);
-    const uint8_t* even = stage + at;
-    const uint8_t* odd = stage + (at ^ 8);
+    const int r = l.m >> 2, c = l.m & 3;   // the row and the 4 features this lane points at
+    const int at = r * kChunk + l.g * (kHalf * 2) + l.wm * 128 + ((c ^ (3 * (l.g & 1))) << 4) +
+                   ((c & 1) << 3);
+    const uint8_t* even = unit + at;
+    const uint8_t* odd = unit + (at ^ 8);
 #pragma unroll
-    for (int tm = 0; tm < TM; ++tm) f[tm] = read_across((tm & 1 ? odd : even) + (tm >> 1) * 64);
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        f[ks][t] = read_across((t & 1 ? odd : even) + (t >> 1) * 64 + ks * 8 * kChunk);
   } else {
-    const int at = (l.wm * 128 + l.m) * 64 + ((l.g ^ ((l.m >> 1) & 3)) << 4);
+    const int at = (l.wm * 64 + l.m) * 128 + ((l.g ^ ((l.m >> 1) & 7)) << 4);
 #pragma unroll
-    for (int tm = 0; tm < TM; ++tm) f[tm] = *reinterpret_cast<const u32x4*>(stage + at + tm * 1024);
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        f[ks][t] = *reinterpret_cast<const u32x4*>(unit + (at ^ (ks * 64)) + t * 2048);
   }
 }
 
-// the rows of wavefront column wn: tiles of 16 wn, wn + 4, ...
-template <bool kIsAcross, int TN>
-__device__ __forceinline__ void read_rows(const Lane& l, const uint8_t* stage, u32x4 (&f)[TN]) {
+// 2 tiles of rows
+template <bool kIsAcross>
+__device__ __forceinline__ void read_rows(const Lane& l, const uint8_t* unit, u32x4 (&f)[2][2]) {
   if constexpr (kIsAcross) {
-    const int c = l.m & 3;
-    const int at = across_at(l) + (((2 * l.wn + (c >> 1)) ^ (3 * (l.g & 1))) << 4) + ((c & 1) << 3);
+    const int r = l.m >> 2, c = l.m & 3;
+    const int at = r * kChunk + l.g * (kHalf * 2) +
+                   (((2 * l.wn + (c >> 1)) ^ (3 * (l.g & 1))) << 4) + ((c & 1) << 3);
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn) f[tn] = read_across(stage + at + tn * 128);
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int t = 0; t < 2; ++t) f[ks][t] = read_across(unit + at + t * 128 + ks * 8 * kChunk);
   } else {
-    const int at = (l.wn * 16 + l.m) * 64 + ((l.g ^ ((l.m >> 1) & 3)) << 4);
+    const int at = (l.wn * 16 + l.m) * 128 + ((l.g ^ ((l.m >> 1) & 7)) << 4);
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn) f[tn] = *reinterpret_cast<const u32x4*>(stage + at + tn * 4096);
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        f[ks][t] = *reinterpret_cast<const u32x4*>(unit + (at ^ (ks * 64)) + t * 8192);
   }
 }
 
-// ------------------------------------------------------------------ the product
+// ------------------------------------------------------------------ the stream
 //
-// Step t works on fragments read before it while those of step t + 1 are read.  Before its
-// barrier: stage t + 1 has landed (the loads of later stages may stay in flight) and this
-// wavefront's reads of stage t are done; after it stage t's slot is free for stage t + 4.
-// The next item may fill the ring at once: every read was waited for at the last barrier.
+// Phase of block s    reads           refills (with s + 2)
+//   0  (A0,Bf)        A0 of s         Bf
+//   1  (A0,Bg)        Bg of s         A0
+//   2  (A1,Bg)        A1 of s         Bg
+//   3  (A1,Bf)        Bg of s + 1     A1
+//
+// A phase is two turns: loads and reads, then the 16 ops.  The wavefronts 4 .. 7 are a turn
+// behind 0 .. 3, with whom they share the SIMDs, so that one wavefront of a SIMD has the matrix
+// pipe while the other reads (with all eight in step, and reads a phase ahead of their use, the
+// pipe stood still around each barrier: busy half the time, measured).  A barrier ends each turn.
+// A slot is refilled in the phase after the one that reads it, when the wavefronts behind have
+// read it too; what a phase reads has landed, for every wavefront, at the end of the turn of
+// loads before: all but the last six units' loads, 12 of a wavefront.
+//
+// A job's items have an even number of blocks (a last one that is not worked on), so that slots
+// and f, g are known at compile time.
+//
+// Each unit's slot is an LDS variable of its own, so that a read is known to wait for the loads
+// into its own slot alone: the compiler otherwise has a transposing read wait for all of them
+// (measured in a ring of four stages: 620 against 990 TFLOP/s).
+//
+// Job: kAAcross, kBAcross; first(), next(it), kEnd: its items; blocks(it); two(it): whether the
+// rows' second half holds any; load(it, a, b): sets the loaders; store(it, acc).
+template <class Job>
+__device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) {
+  constexpr bool kAA = Job::kAAcross, kBA = Job::kBAcross;
+  typename Job::A la;
+  typename Job::B lb;
+  using Z = std::integral_constant<int, 0>;
+  using O = std::integral_constant<int, 1>;
+  auto unit_a = [&](auto h, auto slot) __attribute__((always_inline)) -> uint8_t* {
+    constexpr int k = 2 * decltype(h)::value + decltype(slot)::value;
+    if constexpr (k == 0) return u.a00;
+    else if constexpr (k == 1) return u.a01;
+    else if constexpr (k == 2) return u.a10;
+    else return u.a11;
+  };
+  auto unit_b = [&](auto h, auto slot) __attribute__((always_inline)) -> uint8_t* {
+    constexpr int k = 2 * decltype(h)::value + decltype(slot)::value;
+    if constexpr (k == 0) return u.b00;
+    else if constexpr (k == 1) return u.b01;
+    else if constexpr (k == 2) return u.b10;
+    else return u.b11;
+  };
 
-// The ring's slots come as pointers that do not alias, so that a read waits for the direct loads
-// into its own slot alone: the compiler otherwise has every transposing read wait for all of them
-// (measured: 620 TFLOP/s where both operands are read so, against the figures below).
-template <bool kAAcross, bool kBAcross, int TN, class LA, class LB>
-__device__ __forceinline__ void product(const Lane& l, uint8_t* __restrict__ a0,
-                                        uint8_t* __restrict__ a1, uint8_t* __restrict__ a2,
-                                        uint8_t* __restrict__ a3, uint8_t* __restrict__ b0,
-                                        uint8_t* __restrict__ b1, uint8_t* __restrict__ b2,
-                                        uint8_t* __restrict__ b3, LA& la, LB& lb, int nk,
-                                        f32x4 (&acc)[TM][TN]) {
-#pragma unroll
-  for (int tm = 0; tm < TM; ++tm)
-#pragma unroll
-    for (int tn = 0; tn < TN; ++tn) acc[tm][tn] = f32x4{0.f, 0.f, 0.f, 0.f};
-  if (nk == 0) return;
+  // the loads' place in the stream: block `at` of item `item`
+  int item = job.first(), at = -1, blocks = 0, even = 0;
+  if (item == Job::kEnd) return;
+  auto enter = [&]() __attribute__((always_inline)) {
+    blocks = job.blocks(item);
+    even = (blocks + 1) & ~1;
+    if (even > 0) job.load(l.again(), item, la, lb);
+  };
+  enter();
+  // may_end: an item may end here
+  auto advance = [&](auto may_end) __attribute__((always_inline)) {
+    ++at;
+    if constexpr (decltype(may_end)::value) {
+      while (at >= even && item != Job::kEnd) {
+        item = uniform(job.next(item));
+        at = 0;
+        if (item != Job::kEnd) enter();
+      }
+    }
+    const bool live = item != Job::kEnd && at < blocks;
+    la.at(at, live);
+    lb.at(at, live);
+  };
 
-  u32x4 fa[2][TM], fb[2][TN];
-  auto slot_a = [&](auto s) -> uint8_t* {
-    constexpr int k = decltype(s)::value % kStages;
-    if constexpr (k == 0) return a0;
-    else if constexpr (k == 1) return a1;
-    else if constexpr (k == 2) return a2;
-    else return a3;
-  };
-  auto slot_b = [&](auto s) -> uint8_t* {
-    constexpr int k = decltype(s)::value % kStages;
-    if constexpr (k == 0) return b0;
-    else if constexpr (k == 1) return b1;
-    else if constexpr (k == 2) return b2;
-    else return b3;
-  };
-  auto issue = [&](int t, auto s) {
-    la.issue(l, t, slot_a(s));
-    lb.issue(l, t, slot_b(s));
-  };
-  auto read = [&](auto s) {
-    constexpr int k = decltype(s)::value;
-    read_features<kAAcross>(l, slot_a(s), fa[k & 1]);
-    read_rows<kBAcross, TN>(l, slot_b(s), fb[k & 1]);
-  };
-  auto ops = [&](auto s) {
-    constexpr int k = decltype(s)::value & 1;
+  u32x4 fa[2][4], fb[2][2][2];   // [ks][tile], [half][ks][tile]
+  f32x4 acc[TM][TN];
+
+  advance(std::true_type{});
+  lb.issue(l, 0, u.b00);
+  la.issue(l, 0, u.a00);
+  lb.issue(l, 1, u.b10);
+  la.issue(l, 1, u.a10);
+  advance(std::false_type{});
+  lb.issue(l, 1, u.b11);
+  la.issue(l, 0, u.a01);
+  lb.issue(l, 0, u.b01);
+  la.issue(l, 1, u.a11);
+  wait_vm<0>();
+  barrier();
+  read_rows<kBA>(l, u.b00, fb[0]);
+  wait_lgkm0();
+  barrier();
+
+  auto ops = [&](auto ha, auto hb, auto first) __attribute__((always_inline)) {
+    constexpr int i = decltype(ha)::value, j = decltype(hb)::value;
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn)
+    for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int tm = 0; tm < TM; ++tm)
-        acc[tm][tn] = mfma16x16x32(fa[k][tm], fb[k][tn], acc[tm][tn]);
+      for (int tn = 0; tn < 2; ++tn)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          f32x4& c = acc[4 * i + t][2 * j + tn];
+          c = mfma16x16x32(fa[ks][t], fb[j][ks][tn],
+                           decltype(first)::value && ks == 0 ? f32x4{0.f, 0.f, 0.f, 0.f} : c);
+        }
   };
-  // step t, of slot s: the steady form (t + 4 < nk) has no conditions
-  auto steady = [&](int t, auto s) {
-    constexpr int k = decltype(s)::value;
-    wait_vm<8>();
+  // the end of a turn of loads and reads, the ops, and the end of theirs
+  auto work = [&](auto ha, auto hb, auto any, auto first, auto landed) __attribute__((always_inline)) {
+    if constexpr (!decltype(landed)::value) wait_vm<12>();
     wait_lgkm0();
+    __builtin_amdgcn_sched_barrier(0);
     barrier();
-    issue(t + 4, s);
-    read(std::integral_constant<int, k + 1>{});
-    ops(s);
-    // the direct loads, then the reads one by one between the first ops, and no op moved
-    // past the next barrier, whose wait would then find the matrix pipe empty
-    constexpr int kReads = TM * (kAAcross ? 2 : 1) + TN * (kBAcross ? 2 : 1);
-    constexpr int kOps = TM * TN;
-    __builtin_amdgcn_sched_group_barrier(0x020, 4, 0);       // VMEM
-#pragma unroll
-    for (int i = 0; i < (kReads < kOps ? kReads : kOps); ++i) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);     // MFMA
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);     // DS read
+    if constexpr (decltype(any)::value) {
+      __builtin_amdgcn_s_setprio(1);
+      ops(ha, hb, first);
+      __builtin_amdgcn_s_setprio(0);
     }
     __builtin_amdgcn_sched_barrier(0);
-  };
-  auto last = [&](int t, auto s) {
-    constexpr int k = decltype(s)::value;
-    if (t + 3 < nk) wait_vm<8>();
-    else if (t + 2 < nk) wait_vm<4>();
-    else wait_vm<0>();
-    wait_lgkm0();
     barrier();
-    if (t + 4 < nk) issue(t + 4, s);
-    if (t + 1 < nk) read(std::integral_constant<int, k + 1>{});
-    ops(s);
-    __builtin_amdgcn_sched_barrier(0);
   };
-  using C0 = std::integral_constant<int, 0>;
-  using C1 = std::integral_constant<int, 1>;
-  using C2 = std::integral_constant<int, 2>;
-  using C3 = std::integral_constant<int, 3>;
+  // a block in slot `s`, whose Bf is half s; `two`: its second half of rows is worked on; `any`:
+  // it is no block of zeros; `fresh`: one of an item's first two, whose loads have landed but
+  // those of the last two phases
+  auto block = [&](auto s_c, auto two_c, auto any_c, auto fresh_c) __attribute__((always_inline)) {
+    constexpr int s = decltype(s_c)::value, f = s;
+    constexpr bool two = decltype(two_c)::value, any = decltype(any_c)::value;
+    constexpr bool fresh = decltype(fresh_c)::value;
+    using S = std::integral_constant<int, s>;
+    using N = std::integral_constant<int, s ^ 1>;
+    using F = std::integral_constant<int, f>;
+    using G = std::integral_constant<int, f ^ 1>;
+    using DoF = std::integral_constant<bool, any && (two || f == 0)>;
+    using DoG = std::integral_constant<bool, any && (two || f == 1)>;
+    using First = std::integral_constant<bool, fresh && s == 0>;
+    using Early = std::integral_constant<bool, fresh>;
+    using Late = std::integral_constant<bool, fresh && s == 0>;
+    advance(std::integral_constant<bool, s == 0>{});
+    lb.issue(l, f, unit_b(F{}, S{}));
+    read_features<kAA>(l, unit_a(Z{}, S{}), fa);
+    work(Z{}, F{}, DoF{}, First{}, Early{});
 
-  issue(0, C0{});
-  if (nk > 1) issue(1, C1{});
-  if (nk > 2) issue(2, C2{});
-  if (nk > 3) issue(3, C3{});
-  if (nk > 3) wait_vm<12>();
-  else if (nk == 3) wait_vm<8>();
-  else if (nk == 2) wait_vm<4>();
-  else wait_vm<0>();
-  barrier();
-  read(C0{});
-  int t = 0;
-  for (; t + 7 < nk; t += 4) {
-    steady(t, C0{});
-    steady(t + 1, C1{});
-    steady(t + 2, C2{});
-    steady(t + 3, C3{});
+    la.issue(l, 0, unit_a(Z{}, S{}));
+    read_rows<kBA>(l, unit_b(G{}, S{}), fb[f ^ 1]);
+    work(Z{}, G{}, DoG{}, First{}, Early{});
+
+    lb.issue(l, f ^ 1, unit_b(G{}, S{}));
+    read_features<kAA>(l, unit_a(O{}, S{}), fa);
+    work(O{}, G{}, DoG{}, First{}, Late{});
+
+    la.issue(l, 1, unit_a(O{}, S{}));
+    read_rows<kBA>(l, unit_b(G{}, N{}), fb[f ^ 1]);
+    work(O{}, F{}, DoF{}, First{}, Late{});
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  auto work_item = [&](int n, auto two) __attribute__((always_inline)) {
+    block(Z{}, two, Yes{}, Yes{});
+    if (n > 1) block(O{}, two, Yes{}, Yes{});
+    else block(O{}, two, No{}, Yes{});
+    int b = 2;
+    for (; b + 1 < n; b += 2) {
+      block(Z{}, two, Yes{}, No{});
+      block(O{}, two, Yes{}, No{});
+    }
+    if (b < n) {
+      block(Z{}, two, Yes{}, No{});
+      block(O{}, two, No{}, No{});
+    }
+  };
+
+  for (int it = job.first(); it != Job::kEnd; it = job.next(it)) {
+    const int n = job.blocks(it);
+    const bool two = job.two(it);
+    if (n == 0 || !two) {
+#pragma unroll
+      for (int tm = 0; tm < TM; ++tm)
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) acc[tm][tn] = f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    if (n > 0) {
+      if (l.wm == 1) barrier();   // a turn behind
+      if (two) work_item(n, Yes{});
+      else work_item(n, No{});
+      if (l.wm == 0) barrier();   // in step again, to store together
+    }
+    // what is in flight lands before the stores, so that an item's first phases wait for neither
+    wait_vm<0>();
+    job.store(l.again(), it, acc);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  // 1 to 7 steps left
-  last(t, C0{});
-  if (t + 1 < nk) last(t + 1, C1{});
-  if (t + 2 < nk) last(t + 2, C2{});
-  if (t + 3 < nk) last(t + 3, C3{});
-  if (t + 4 < nk) last(t + 4, C0{});
-  if (t + 5 < nk) last(t + 5, C1{});
-  if (t + 6 < nk) last(t + 6, C2{});
+  wait_vm<0>();   // no load into LDS outlives the workgroup
 }
 
 // ------------------------------------------------------------------ storing
 
-__device__ __forceinline__ u32x4 bf16x8_of(const float* v) {
-  u32x4 q;
-  q.x = pack_bf16x2(v[0], v[1]);
-  q.y = pack_bf16x2(v[2], v[3]);
-  q.z = pack_bf16x2(v[4], v[5]);
-  q.w = pack_bf16x2(v[6], v[7]);
-  return q;
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// two values as bf16, rounded to nearest even, in one instruction
+__device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
 __device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  *reinterpret_cast<u32x4*>(p) = bf16x8_of(v);
+  *reinterpret_cast<u32x4*>(p) = u32x4{bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]),
+                                       bf16x2_of(v[4], v[5]), bf16x2_of(v[6], v[7])};
 }
-__device__ __forceinline__ void store8(float* p, const float* v) {
-  reinterpret_cast<f32x4*>(p)[0] = f32x4{v[0], v[1], v[2], v[3]};
-  reinterpret_cast<f32x4*>(p)[1] = f32x4{v[4], v[5], v[6], v[7]};
+
+__device__ __forceinline__ void store16(Rsrc r, uint32_t lane_off, uint32_t off, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)lane_off, (int)uniform(off), 0);
+}
+
+// A lane's 8 sums of a pair of tiles, in the order of their features, at byte off
+__device__ __forceinline__ void store_pair(Rsrc r, uint32_t off, uint32_t d, bool odd, f32x4 a,
+                                           f32x4 b, const uint16_t*) {
+  const uint32_t a0 = bf16x2_of(a.x, a.y), a1 = bf16x2_of(a.z, a.w);
+  const uint32_t b0 = bf16x2_of(b.x, b.y), b1 = bf16x2_of(b.z, b.w);
+  store16(r, off, d, odd ? u32x4{b0, b1, a0, a1} : u32x4{a0, a1, b0, b1});
+}
+__device__ __forceinline__ void store_pair(Rsrc r, uint32_t off, uint32_t d, bool odd, f32x4 a,
+                                           f32x4 b, const float*) {
+  store16(r, off + (odd ? 16 : 0), d, __builtin_bit_cast(u32x4, a));
+  store16(r, off + (odd ? 0 : 16), d, __builtin_bit_cast(u32x4, b));
+}
+
+// The tile at out, of rows of F values: `rows` of its rows and `cols` of its columns are there.
+// Stores go through descriptors: a lane's own offset for all of them, and rows past the last
+// refused by range.
+template <class T>
+__device__ __forceinline__ void store_tile(const Lane& l, const f32x4 (&acc)[TM][TN], T* out, int F,
+                                           int rows, int cols) {
+  constexpr uint32_t e = sizeof(T);
+  const uint32_t row_bytes = (uint32_t)F * e;
+  const uint32_t off = (uint32_t)(l.wn * 16 + l.m) * row_bytes + (uint32_t)(64 * l.wm + 8 * l.g) * e;
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(out);
+  // up to the end of the last row
+  const uint32_t all = (uint32_t)(rows - 1) * row_bytes + (uint32_t)min(cols, kTile) * e;
+#pragma unroll
+  for (int p = 0; p < TM / 2; ++p) {
+    const int f = kHalf * (p >> 1) + 32 * (p & 1);
+    const Rsrc r = make_rsrc(base, f + 64 * l.wm < cols ? all : 0);
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn)
+      store_pair(r, off + (uint32_t)f * e, (uint32_t)(64 * tn) * row_bytes, l.g & 1,
+                 acc[2 * p][tn], acc[2 * p + 1][tn], out);
+  }
 }
 
 __device__ __forceinline__ void load8(const uint16_t* p, float* v) {
@@ -433,104 +630,6 @@ __device__ __forceinline__ void kept8(const Args& a, size_t row, int col, float*
     load8(a.h + at, v);
 }
 
-// One item of the products over rows: features f0 .. of the tile, rows row0 .. row0 + n - 1 of
-// expert e, n <= 64 TN.
-template <Op kOp, bool kFp8, int TN, class Sm>
-__device__ __forceinline__ void rows_item(const Args& a, const Lane& l, Sm& sm, int e, int f0,
-                                          int64_t row0, int n) {
-  const int H = a.r.H, I = a.r.I;
-  f32x4 acc[TM][TN];
-  Along rows;
-  // rows: of x by token, or of the row buffer
-  const int Kdim = kOp == kGateUp || kOp == kDAct ? H : kOp == kDown ? I : 2 * I;
-  const uint32_t row_bytes = (uint32_t)Kdim * 2;
-  if (kOp == kGateUp && a.r.counts) {
-    rows.set(l, make_rsrc(a.in, (uint32_t)a.r.tokens * row_bytes), [&](int j) -> uint32_t {
-      const int t = sm.tok[j];
-      return t < 0 ? kOutside : (uint32_t)t * row_bytes;
-    });
-  } else {
-    rows.set(l, make_rsrc(a.in + (size_t)row0 * Kdim, (uint32_t)n * row_bytes),
-             [&](int j) -> uint32_t { return j < n ? (uint32_t)j * row_bytes : kOutside; });
-  }
-  const int nk = Kdim / kStep;
-  if constexpr (kOp == kGateUp || kOp == kDown) {
-    Along feats;
-    const size_t mat = (kOp == kGateUp ? (size_t)2 : (size_t)1) * I * H;
-    const uint16_t* w = a.w + (size_t)e * mat;
-    feats.set(l, make_rsrc(w, (uint32_t)(mat * 2)), [&](int r) -> uint32_t {
-      const int tm = (r >> 4) & 7, c = (r >> 2) & 3, j = r & 3;
-      int f;
-      if (kOp == kGateUp) {
-        // of four MFMA tiles two are gate's and two up's, of the same 32 columns
-        f = f0 + 64 * (r >> 7) + (feature(0, tm & 1, c, j) + 32 * (tm >> 2));
-        if (f >= I) return kOutside;
-        if (tm & 2) f += I;
-      } else {
-        f = f0 + feature(r >> 7, tm, c, j);
-        if (f >= H) return kOutside;
-      }
-      return (uint32_t)f * row_bytes;
-    });
-    product<false, false, TN>(l, sm.a[0], sm.a[1], sm.a[2], sm.a[3], sm.b[0], sm.b[1],
-                             sm.b[2], sm.b[3], feats, rows, nk, acc);
-  } else {
-    Across feats;
-    const int F = kOp == kDAct ? I : H;
-    feats.set(l, a.w + (size_t)e * Kdim * F, (uint32_t)F * 2, Kdim, f0);
-    product<true, false, TN>(l, sm.a[0], sm.a[1], sm.a[2], sm.a[3], sm.b[0], sm.b[1],
-                             sm.b[2], sm.b[3], feats, rows, nk, acc);
-  }
-
-#pragma unroll
-  for (int tn = 0; tn < TN; ++tn) {
-    const int j = (l.wn + 4 * tn) * 16 + l.m;
-    const bool in = j < n;
-    const size_t row = (size_t)(row0 + j);
-    if constexpr (kOp == kGateUp) {
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int i = f0 + 64 * l.wm + 32 * q + 8 * l.g;
-        float gv[8], uv[8], av[8];
-        in_order(l.g, acc[4 * q][tn], acc[4 * q + 1][tn], gv);
-        in_order(l.g, acc[4 * q + 2][tn], acc[4 * q + 3][tn], uv);
-#pragma unroll
-        for (int x = 0; x < 8; ++x) av[x] = silu(gv[x]) * uv[x];
-        const bool here = in && i < I;
-        keep8<kFp8>(a, row, i, gv, l.g == 0, here);
-        keep8<kFp8>(a, row, I + i, uv, l.g == 0, here);
-        if (here) store8(a.act + row * I + i, av);
-      }
-    } else {
-#pragma unroll
-      for (int p = 0; p < TM / 2; ++p) {
-        const int f = f0 + 128 * l.wm + 32 * p + 8 * l.g;
-        float v[8];
-        in_order(l.g, acc[2 * p][tn], acc[2 * p + 1][tn], v);
-        if constexpr (kOp == kDAct) {
-          if (in && f < I) {
-            float gv[8], uv[8], av[8], dg[8], du[8];
-            kept8<kFp8>(a, row, f, gv);
-            kept8<kFp8>(a, row, I + f, uv);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-              const float s = sigmoid(gv[x]), gs = gv[x] * s;
-              av[x] = gs * uv[x];
-              dg[x] = v[x] * uv[x] * (s * (1.0f + gv[x] * (1.0f - s)));
-              du[x] = v[x] * gs;
-            }
-            store8(a.act + row * I + f, av);
-            store8(a.dh + row * (2 * (size_t)I) + f, dg);
-            store8(a.dh + row * (2 * (size_t)I) + I + f, du);
-          }
-        } else {
-          if (in && f < H) store8(a.out + row * H + f, v);
-        }
-      }
-    }
-  }
-}
-
 // the rows of expert e, inside the row buffers whatever the plan says
 __device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int64_t* row0) {
   *row0 = 0;
@@ -542,18 +641,30 @@ __device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int64_t* r
   return (int)(n < 0 ? 0 : n < r.rows - off ? n : r.rows - off);
 }
 
-// Persistent workgroups over (expert, feature tile, span of up to 256 rows), spans fastest, one
-// run of items per XCD (workgroup b runs on XCD b % 8), so that the spans that share a weight
-// tile run side by side on one L2.
+// One of the products over rows.  Items: (expert, feature tile, span of up to 256 rows), spans
+// fastest, one run of them per XCD (workgroup b runs on XCD b % 8) that its workgroups take in
+// turn, so that the spans that share a weight tile run side by side on one L2.
 template <Op kOp, bool kFp8>
-__global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
-  __shared__ __attribute__((aligned(1024))) Smem<kOp == kDAct || kOp == kDX, false> sm;
-  const Lane l;
-  const int nexp = a.r.counts ? a.r.E : 1;
-  const int per_tile = kOp == kGateUp ? kTile / 2 : kTile;
-  const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
-  const int ntiles = (F + per_tile - 1) / per_tile;
-  {
+struct RowsJob {
+  static constexpr bool kAAcross = kOp == kDAct || kOp == kDX, kBAcross = false;
+  using A = typename std::conditional<kAAcross, Across, Along>::type;
+  using B = typename std::conditional<kOp == kGateUp, Gathered, Along>::type;
+  static constexpr int kEnd = -1;
+  static constexpr int kFeatures = kOp == kGateUp ? kTile / 2 : kTile;   // of the result
+  const Args& a;
+  const int* pre;
+  int nexp, hi, start, step;
+
+  struct Item {
+    int e, f0, n;
+    int64_t row0;
+  };
+
+  __device__ __forceinline__ RowsJob(const Args& args, const Lane& l, Smem& sm)
+      : a(args), pre(sm.pre) {
+    nexp = a.r.counts ? a.r.E : 1;
+    const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
+    const int ntiles = (F + kFeatures - 1) / kFeatures;
     int u = 0;
     if (l.tid < nexp) {
       int64_t row0;
@@ -573,46 +684,149 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
     if (l.tid < nexp) sm.pre[l.tid + 1] = before + incl;
     if (l.tid == 0) sm.pre[0] = 0;
     __syncthreads();
+    const int total = uniform(pre[nexp]);
+    const int xcd = (int)blockIdx.x % 8, per = (total + 7) / 8;
+    step = (int)gridDim.x / 8;
+    start = xcd * per + (int)blockIdx.x / 8;
+    hi = min(total, (xcd + 1) * per);
   }
-  const int total = __builtin_amdgcn_readfirstlane(sm.pre[nexp]);
-  const int nc = (int)gridDim.x / 8;
-  const int xcd = (int)blockIdx.x % 8, c = (int)blockIdx.x / 8;
-  const int per = (total + 7) / 8;
-  const int hi = min(total, (xcd + 1) * per);
-  for (int it = xcd * per + c; it < hi; it += nc) {
+  __device__ __forceinline__ int first() const { return start < hi ? start : kEnd; }
+  __device__ __forceinline__ int next(int it) const { return it + step < hi ? it + step : kEnd; }
+
+  __device__ __forceinline__ Item item(int it) const {
     int lo = 0, up = nexp;   // the last expert with pre[e] <= it
     while (up - lo > 1) {
       const int mid = (lo + up) >> 1;
-      if (__builtin_amdgcn_readfirstlane(sm.pre[mid]) <= it) lo = mid;
+      if (uniform(pre[mid]) <= it) lo = mid;
       else up = mid;
     }
-    const int e = lo;
-    int64_t first;
-    const int n = __builtin_amdgcn_readfirstlane(expert_rows(a.r, e, &first));
+    Item x;
+    x.e = lo;
+    int64_t row0;
+    const int n = uniform(expert_rows(a.r, lo, &row0));
     const int spans = (n + kTile - 1) / kTile;
-    const int at = it - __builtin_amdgcn_readfirstlane(sm.pre[e]);
-    const int tile = at / spans, span = at - tile * spans;
-    const int64_t row0 = __builtin_amdgcn_readfirstlane((int)first) + (int64_t)span * kTile;
-    const int nrows = min(kTile, n - span * kTile);
-    if (kOp == kGateUp && a.r.counts) {
-      __syncthreads();   // the previous item's loads have their tokens
-      if (l.tid < kTile) {
-        const int p = l.tid < nrows ? a.r.sorted_ids[row0 + l.tid] : -1;
-        const uint32_t t = divided(a.div, (uint32_t)p & 0x7fffffffu);
-        sm.tok[l.tid] = p >= 0 && t < (uint64_t)a.r.tokens ? (int)t : -1;
-      }
-      __syncthreads();
-    }
-    const int f0 = tile * per_tile;
-    if (nrows > 128) rows_item<kOp, kFp8, 4>(a, l, sm, e, f0, row0, nrows);
-    else if (nrows > 64) rows_item<kOp, kFp8, 2>(a, l, sm, e, f0, row0, nrows);
-    else rows_item<kOp, kFp8, 1>(a, l, sm, e, f0, row0, nrows);
+    const int at = it - uniform(pre[lo]);
+    const int tile = uniform(at / spans), span = at - tile * spans;
+    x.f0 = tile * kFeatures;
+    x.row0 = uniform((int)row0) + (int64_t)span * kTile;
+    x.n = min(kTile, n - span * kTile);
+    return x;
   }
+
+  __device__ __forceinline__ int contraction() const {
+    return kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
+  }
+  __device__ __forceinline__ int blocks(int) const { return contraction() / kBlock; }
+  __device__ __forceinline__ bool two(int it) const { return item(it).n > kHalf; }
+
+  __device__ __forceinline__ void load(const Lane& l, int it, A& la, B& lb) const {
+    const Item x = item(it);
+    const int H = a.r.H, I = a.r.I, K = contraction();
+    const uint32_t row_bytes = (uint32_t)K * 2;
+    if constexpr (kOp == kGateUp) {
+      if (a.r.counts) {
+        lb.set(l, a.in, (uint32_t)a.r.tokens * row_bytes, [&](int j) -> uint32_t {
+          const int p = j < x.n ? a.r.sorted_ids[x.row0 + j] : -1;
+          const uint32_t t = divided(a.div, (uint32_t)p & 0x7fffffffu);
+          return p >= 0 && t < (uint64_t)a.r.tokens ? t * row_bytes : kOutside;
+        });
+      } else {
+        lb.set(l, a.in + (size_t)x.row0 * K, (uint32_t)x.n * row_bytes,
+               [&](int j) -> uint32_t { return (uint32_t)j * row_bytes; });
+      }
+    } else {
+      lb.set(l, a.in + (size_t)x.row0 * K, (uint32_t)x.n * row_bytes, kHalf * row_bytes,
+             [&](int j) -> uint32_t { return (uint32_t)j * row_bytes; });
+    }
+    if constexpr (kAAcross) {
+      const int F = kOp == kDAct ? I : H;
+      la.set(l, a.w + (size_t)x.e * K * F, (uint32_t)F * 2, K, x.f0);
+    } else {
+      const size_t mat = (kOp == kGateUp ? (size_t)2 : (size_t)1) * I * H;
+      const size_t before = (size_t)x.f0 * K;
+      // of a half's four MFMA tiles (gate/up) two are gate's and two up's, of the same 32 columns
+      la.set(l, a.w + (size_t)x.e * mat + before, (uint32_t)((mat - before) * 2),
+             kFeatures / 2 * row_bytes, [&](int r) -> uint32_t {
+               const int wm = r >> 6, t = (r >> 4) & 3, c = (r >> 2) & 3, j = r & 3;
+               const int f = kOp == kGateUp ? 32 * wm + feature(t & 1, c, j) + (t & 2 ? I : 0)
+                                            : 64 * wm + feature(t, c, j);
+               return (uint32_t)f * row_bytes;
+             });
+    }
+  }
+
+  __device__ __forceinline__ void store(const Lane& l, int it, f32x4 (&acc)[TM][TN]) const {
+    const Item x = item(it);
+    const int H = a.r.H, I = a.r.I;
+    if constexpr (kOp == kDown || kOp == kDX) {
+      store_tile(l, acc, a.out + (size_t)x.row0 * H + x.f0, H, x.n, H - x.f0);
+      return;
+    }
+#pragma unroll
+    for (int tn = 0; tn < TN; ++tn) {
+      const int j = tile_row(l, tn);
+      const bool in = j < x.n;
+      const size_t row = (size_t)(x.row0 + j);
+      if constexpr (kOp == kGateUp) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = x.f0 + 64 * h + 32 * l.wm + 8 * l.g;
+          float gv[8], uv[8], av[8];
+          in_order(l.g, acc[4 * h][tn], acc[4 * h + 1][tn], gv);
+          in_order(l.g, acc[4 * h + 2][tn], acc[4 * h + 3][tn], uv);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) av[q] = silu(gv[q]) * uv[q];
+          const bool here = in && i < I;
+          keep8<kFp8>(a, row, i, gv, l.g == 0, here);
+          keep8<kFp8>(a, row, I + i, uv, l.g == 0, here);
+          if (here) store8(a.act + row * I + i, av);
+        }
+      } else if constexpr (kOp == kDAct) {
+#pragma unroll
+        for (int p = 0; p < TM / 2; ++p) {
+          const int f = x.f0 + pair_feature(l, p);
+          float v[8];
+          in_order(l.g, acc[2 * p][tn], acc[2 * p + 1][tn], v);
+          {
+            if (in && f < I) {
+              float gv[8], uv[8], av[8], dg[8], du[8];
+              kept8<kFp8>(a, row, f, gv);
+              kept8<kFp8>(a, row, I + f, uv);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) {
+                const float s = sigmoid(gv[q]), gs = gv[q] * s;
+                av[q] = gs * uv[q];
+                dg[q] = v[q] * uv[q] * (s * (1.0f + gv[q] * (1.0f - s)));
+                du[q] = v[q] * gs;
+              }
+              store8(a.act + row * I + f, av);
+              store8(a.dh + row * (2 * (size_t)I) + f, dg);
+              store8(a.dh + row * (2 * (size_t)I) + I + f, du);
+            }
+          }
+        }
+      }
+    }
+  }
+};
+
+template <Op kOp, bool kFp8>
+__global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
+  TRAIN_UNITS;
+  __shared__ Smem sm;
+  const Lane l(threadIdx.x);
+  RowsJob<kOp, kFp8> job(a, l, sm);
+  stream(l, job, units);
 }
 
 // Gradients of the weights: [E][N][M] from rows of M features (the side along memory of the
 // result) and rows of N.  An item is one 256 x 256 tile of one expert's matrix, its
 // contraction the expert's rows; an expert without rows gets zeros.
+//
+// Experts come by falling numbers of rows, the tiles of each dealt to the 8 XCDs in runs of
+// equal length, so that skewed routing leaves no XCD with the busy experts and the short
+// items fill in at the end (contiguous experts per XCD: Qwen2-shaped dW13 of 3001 tokens with
+// skewed routing 2.4 ms).
 struct WeightArgs {
   TrainRows r;
   const uint16_t* m_rows;
@@ -622,48 +836,102 @@ struct WeightArgs {
 };
 
 template <class TOut>
-__global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
-  __shared__ __attribute__((aligned(1024))) Smem<true, true> sm;
-  const Lane l;
-  const int E = a.r.counts ? a.r.E : 1;
-  const int tm_n = (a.M + kTile - 1) / kTile, tn_n = (a.N + kTile - 1) / kTile;
-  const int64_t each = (int64_t)tm_n * tn_n, total = E * each;
-  const int nc = (int)gridDim.x / 8;
-  const int xcd = (int)blockIdx.x % 8, c = (int)blockIdx.x / 8;
-  const int64_t per = (total + 7) / 8;
-  const int64_t hi = total < (xcd + 1) * per ? total : (xcd + 1) * per;
-  for (int64_t it = xcd * per + c; it < hi; it += nc) {
-    // tiles in bands of 4 along N, so that those at work together share their operands
-    const int e = (int)(it / each);
-    const int at = (int)(it - e * each);
-    const int band = at / (4 * tm_n), in_band = at - band * 4 * tm_n;
-    const int width = min(4, tn_n - 4 * band);
-    const int tm = in_band / width, tn = 4 * band + in_band - tm * width;
-    const int m0 = tm * kTile, n0 = tn * kTile;
-    int64_t first;
-    const int n = __builtin_amdgcn_readfirstlane(expert_rows(a.r, e, &first));
-    const int64_t row0 = __builtin_amdgcn_readfirstlane((int)first);
-    const int nk = (n + kStep - 1) / kStep;
-    f32x4 acc[TM][4];
-    Across nr;
-    nr.set(l, a.n_rows + (size_t)row0 * a.N, (uint32_t)a.N * 2, n, n0);
-    Across mr;
-    mr.set(l, a.m_rows + (size_t)row0 * a.M, (uint32_t)a.M * 2, n, m0);
-    product<true, true, 4>(l, sm.a[0], sm.a[1], sm.a[2], sm.a[3], sm.b[0], sm.b[1], sm.b[2],
-                           sm.b[3], mr, nr, nk, acc);
-    TOut* out = static_cast<TOut*>(a.out) + (size_t)e * a.M * a.N;
-#pragma unroll
-    for (int tn4 = 0; tn4 < 4; ++tn4) {
-      const int j = n0 + (l.wn + 4 * tn4) * 16 + l.m;
-#pragma unroll
-      for (int p = 0; p < TM / 2; ++p) {
-        const int f = m0 + 128 * l.wm + 32 * p + 8 * l.g;
-        float v[8];
-        in_order(l.g, acc[2 * p][tn4], acc[2 * p + 1][tn4], v);
-        if (j < a.N && f < a.M) store8(out + (size_t)j * a.M + f, v);
-      }
+struct WeightsJob {
+  static constexpr bool kAAcross = true, kBAcross = true;
+  using A = Across;
+  using B = Across;
+  static constexpr int kEnd = -1;
+  const WeightArgs& a;
+  const int* by_rank;
+  int E, tm_n, tn_n, each, run, hi, start, step, xcd;
+
+  struct Item {
+    int e, m0, n0, n;
+    int64_t row0;
+  };
+
+  __device__ __forceinline__ WeightsJob(const WeightArgs& args, const Lane& l, Smem& sm)
+      : a(args), by_rank(sm.pre) {
+    E = a.r.counts ? a.r.E : 1;
+    int* rows = sm.rows;
+    int64_t row0;
+    const int n = l.tid < E ? expert_rows(a.r, l.tid, &row0) : 0;
+    if (l.tid < E) rows[l.tid] = n;
+    __syncthreads();
+    if (l.tid < E) {
+      int rank = 0;
+      for (int e = 0; e < E; ++e) rank += rows[e] > n || (rows[e] == n && e < l.tid);
+      sm.pre[rank] = l.tid;
     }
+    __syncthreads();
+    tm_n = (a.M + kTile - 1) / kTile;
+    tn_n = (a.N + kTile - 1) / kTile;
+    each = tm_n * tn_n;
+    if (E * (int64_t)each <= (int64_t)gridDim.x) {   // an item a workgroup
+      run = each;
+      xcd = -1;
+      start = (int)blockIdx.x;
+      step = (int)gridDim.x;
+    } else {
+      run = (each + 7) / 8;
+      xcd = (int)blockIdx.x % 8;
+      start = (int)blockIdx.x / 8;
+      step = (int)gridDim.x / 8;
+    }
+    hi = E * run;
   }
+  // the tile of place it in this XCD's order; >= each: none
+  __device__ __forceinline__ int tile_of(int it, int* e) const {
+    const int rank = uniform(it / run);
+    *e = uniform(by_rank[rank]);
+    const int at = it - rank * run;
+    return xcd < 0 ? at : ((xcd + *e) & 7) * run + at;
+  }
+  __device__ __forceinline__ int held(int it) const {
+    int e;
+    while (it < hi && tile_of(it, &e) >= each) it += step;
+    return it < hi ? it : kEnd;
+  }
+  __device__ __forceinline__ int first() const { return held(start); }
+  __device__ __forceinline__ int next(int it) const { return held(it + step); }
+
+  __device__ __forceinline__ Item item(int it) const {
+    Item x;
+    const int at = tile_of(it, &x.e);
+    // tiles in bands of 4 along N, so that those at work together share their operands
+    const int band = uniform(at / (4 * tm_n)), in_band = at - band * 4 * tm_n;
+    const int width = min(4, tn_n - 4 * band);
+    const int tm = uniform(in_band / width);
+    x.m0 = tm * kTile;
+    x.n0 = (4 * band + in_band - tm * width) * kTile;
+    int64_t row0;
+    x.n = uniform(expert_rows(a.r, x.e, &row0));
+    x.row0 = uniform((int)row0);
+    return x;
+  }
+  __device__ __forceinline__ int blocks(int it) const {
+    return (item(it).n + kBlock - 1) / kBlock;
+  }
+  __device__ __forceinline__ bool two(int) const { return true; }
+  __device__ __forceinline__ void load(const Lane& l, int it, Across& la, Across& lb) const {
+    const Item x = item(it);
+    la.set(l, a.m_rows + (size_t)x.row0 * a.M, (uint32_t)a.M * 2, x.n, x.m0);
+    lb.set(l, a.n_rows + (size_t)x.row0 * a.N, (uint32_t)a.N * 2, x.n, x.n0);
+  }
+  __device__ __forceinline__ void store(const Lane& l, int it, f32x4 (&acc)[TM][TN]) const {
+    const Item x = item(it);
+    store_tile(l, acc, static_cast<TOut*>(a.out) + ((size_t)x.e * a.N + x.n0) * a.M + x.m0, a.M,
+               min(kTile, a.N - x.n0), a.M - x.m0);
+  }
+};
+
+template <class TOut>
+__global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
+  TRAIN_UNITS;
+  __shared__ Smem sm;
+  const Lane l(threadIdx.x);
+  WeightsJob<TOut> job(a, l, sm);
+  stream(l, job, units);
 }
 
 // compute units of the device current at the first call, as a multiple of the 8 XCDs

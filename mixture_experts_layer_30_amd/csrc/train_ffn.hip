@@ -70,11 +70,11 @@ struct Units {
   uint8_t *a00, *a01, *a10, *a11, *b00, *b01, *b10, *b11;
 };
 
-// what a job keeps in LDS
+// what a job keeps in LDS: the experts' rows, and its own order of the items
 struct Smem {
-  int pre[kMaxE + 1];
-  int wsum[kWaves];
-  int rows[kMaxE];
+  int first[kMaxE], rows[kMaxE];
+  int pre[kMaxE + 1], pre_light[kMaxE + 1];
+  int wsum[2][kWaves];
 };
 
 enum Op { kGateUp, kDown, kDAct, kDX };
@@ -348,8 +348,9 @@ __device__ __forceinline__ void read_rows(const Lane& l, const uint8_t* unit, u3
 // into its own slot alone: the compiler otherwise has a transposing read wait for all of them
 // (measured in a ring of four stages: 620 against 990 TFLOP/s).
 //
-// Job: kAAcross, kBAcross; first(), next(it), kEnd: its items; blocks(it); two(it): whether the
-// rows' second half holds any; load(it, a, b): sets the loaders; store(it, acc).
+// Job: kAAcross, kBAcross; first(), next(it), kEnd: the places of this workgroup's items;
+// item(it); and of an item blocks(); two(): whether the rows' second half holds any; load(a, b):
+// sets the loaders; store(acc).
 template <class Job>
 __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) {
   constexpr bool kAA = Job::kAAcross, kBA = Job::kBAcross;
@@ -376,9 +377,10 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
   int item = job.first(), at = -1, blocks = 0, even = 0;
   if (item == Job::kEnd) return;
   auto enter = [&]() __attribute__((always_inline)) {
-    blocks = job.blocks(item);
+    const typename Job::Item x = job.item(item);
+    blocks = job.blocks(x);
     even = (blocks + 1) & ~1;
-    if (even > 0) job.load(l.again(), item, la, lb);
+    if (even > 0) job.load(l.again(), x, la, lb);
   };
   enter();
   // may_end: an item may end here
@@ -442,19 +444,17 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
     __builtin_amdgcn_sched_barrier(0);
     barrier();
   };
-  // a block in slot `s`, whose Bf is half s; `two`: its second half of rows is worked on; `any`:
-  // it is no block of zeros; `fresh`: one of an item's first two, whose loads have landed but
-  // those of the last two phases
-  auto block = [&](auto s_c, auto two_c, auto any_c, auto fresh_c) __attribute__((always_inline)) {
+  // a block in slot `s`, whose Bf is half s; `two`: its second half of rows is worked on;
+  // `fresh`: one of an item's first two, whose loads have landed but those of the last two phases
+  auto block = [&](auto s_c, auto two_c, auto fresh_c) __attribute__((always_inline)) {
     constexpr int s = decltype(s_c)::value, f = s;
-    constexpr bool two = decltype(two_c)::value, any = decltype(any_c)::value;
-    constexpr bool fresh = decltype(fresh_c)::value;
+    constexpr bool two = decltype(two_c)::value, fresh = decltype(fresh_c)::value;
     using S = std::integral_constant<int, s>;
     using N = std::integral_constant<int, s ^ 1>;
     using F = std::integral_constant<int, f>;
     using G = std::integral_constant<int, f ^ 1>;
-    using DoF = std::integral_constant<bool, any && (two || f == 0)>;
-    using DoG = std::integral_constant<bool, any && (two || f == 1)>;
+    using DoF = std::integral_constant<bool, two || f == 0>;
+    using DoG = std::integral_constant<bool, two || f == 1>;
     using First = std::integral_constant<bool, fresh && s == 0>;
     using Early = std::integral_constant<bool, fresh>;
     using Late = std::integral_constant<bool, fresh && s == 0>;
@@ -475,26 +475,45 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
     read_rows<kBA>(l, unit_b(G{}, N{}), fb[f ^ 1]);
     work(O{}, F{}, DoF{}, First{}, Late{});
   };
+  // the block of zeros (slot 1) that makes an odd number even: its refills and the read of the
+  // next block's Bf, which was loaded a block before, three units ago
+  auto hollow = [&]() __attribute__((always_inline)) {
+    wait_vm<6>();
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    barrier();
+    advance(std::false_type{});
+    lb.issue(l, 1, u.b11);
+    la.issue(l, 0, u.a01);
+    lb.issue(l, 0, u.b01);
+    la.issue(l, 1, u.a11);
+    read_rows<kBA>(l, u.b00, fb[0]);
+    wait_vm<12>();
+    wait_lgkm0();
+    __builtin_amdgcn_sched_barrier(0);
+    barrier();
+    barrier();
+  };
   using Yes = std::true_type;
   using No = std::false_type;
   auto work_item = [&](int n, auto two) __attribute__((always_inline)) {
-    block(Z{}, two, Yes{}, Yes{});
-    if (n > 1) block(O{}, two, Yes{}, Yes{});
-    else block(O{}, two, No{}, Yes{});
+    block(Z{}, two, Yes{});
     int b = 2;
-    for (; b + 1 < n; b += 2) {
-      block(Z{}, two, Yes{}, No{});
-      block(O{}, two, Yes{}, No{});
+    if (n > 1) {
+      block(O{}, two, Yes{});
+      for (; b + 1 < n; b += 2) {
+        block(Z{}, two, No{});
+        block(O{}, two, No{});
+      }
+      if (b < n) block(Z{}, two, No{});
     }
-    if (b < n) {
-      block(Z{}, two, Yes{}, No{});
-      block(O{}, two, No{}, No{});
-    }
+    if (n & 1) hollow();
   };
 
   for (int it = job.first(); it != Job::kEnd; it = job.next(it)) {
-    const int n = job.blocks(it);
-    const bool two = job.two(it);
+    const typename Job::Item x = job.item(it);
+    const int n = job.blocks(x);
+    const bool two = job.two(x);
     if (n == 0 || !two) {
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm)
@@ -509,7 +528,7 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
     }
     // what is in flight lands before the stores, so that an item's first phases wait for neither
     wait_vm<0>();
-    job.store(l.again(), it, acc);
+    job.store(l.again(), x, acc);
     __builtin_amdgcn_sched_barrier(0);
   }
   wait_vm<0>();   // no load into LDS outlives the workgroup
@@ -631,19 +650,50 @@ __device__ __forceinline__ void kept8(const Args& a, size_t row, int col, float*
 }
 
 // the rows of expert e, inside the row buffers whatever the plan says
-__device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int64_t* row0) {
+__device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int* row0) {
   *row0 = 0;
   if (!r.counts || r.tokens == 0) return (int)r.tokens;   // without tokens the plan holds nothing
   const int64_t off = r.offsets[e];
   const int64_t n = r.counts[e];
   if (off < 0 || off >= r.rows) return 0;
-  *row0 = off;
+  *row0 = (int)off;
   return (int)(n < 0 ? 0 : n < r.rows - off ? n : r.rows - off);
+}
+
+// exclusive sums of u over the threads, in pre[0 ..]; the number of threads >= that of values
+__device__ __forceinline__ void prefix(const Lane& l, int u, int values, int* pre, int* wsum) {
+  int incl = u;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int v = __shfl_up(incl, d, kWave);
+    if (l.lane >= d) incl += v;
+  }
+  if (l.lane == kWave - 1) wsum[l.wave] = incl;
+  __syncthreads();
+  int before = 0;
+#pragma unroll
+  for (int v = 0; v < kWaves; ++v) before += v < l.wave ? wsum[v] : 0;
+  if (l.tid < values) pre[l.tid + 1] = before + incl;
+  if (l.tid == 0) pre[0] = 0;
+}
+
+// the last of n with pre[i] <= at
+__device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
+  int lo = 0, up = n;
+  while (up - lo > 1) {
+    const int mid = (lo + up) >> 1;
+    if (uniform(pre[mid]) <= at) lo = mid;
+    else up = mid;
+  }
+  return lo;
 }
 
 // One of the products over rows.  Items: (expert, feature tile, span of up to 256 rows), spans
 // fastest, one run of them per XCD (workgroup b runs on XCD b % 8) that its workgroups take in
-// turn, so that the spans that share a weight tile run side by side on one L2.
+// turn, so that the spans that share a weight tile run side by side on one L2.  Experts of up to
+// 128 rows come after all others, whose items take twice as long (Qwen2-shaped da and dx of 3001
+// tokens with skewed routing: 517 -> 472 and 817 -> 742 us).  Where a run's last round would leave
+// half the workgroups or more without an item, its items are cut into two of 128 rows.
 template <Op kOp, bool kFp8>
 struct RowsJob {
   static constexpr bool kAAcross = kOp == kDAct || kOp == kDX, kBAcross = false;
@@ -652,75 +702,83 @@ struct RowsJob {
   static constexpr int kEnd = -1;
   static constexpr int kFeatures = kOp == kGateUp ? kTile / 2 : kTile;   // of the result
   const Args& a;
-  const int* pre;
-  int nexp, hi, start, step;
+  const Smem& sm;
+  int nexp, step, xcd;
+  int full0, full, cut, light0;   // this XCD's items: its first, whole, in two; its first short one
+  int hi;
 
   struct Item {
     int e, f0, n;
     int64_t row0;
   };
 
-  __device__ __forceinline__ RowsJob(const Args& args, const Lane& l, Smem& sm)
-      : a(args), pre(sm.pre) {
+  __device__ __forceinline__ RowsJob(const Args& args, const Lane& l, Smem& m) : a(args), sm(m) {
     nexp = a.r.counts ? a.r.E : 1;
     const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
     const int ntiles = (F + kFeatures - 1) / kFeatures;
-    int u = 0;
+    int n = 0, row0 = 0;
     if (l.tid < nexp) {
-      int64_t row0;
-      u = ntiles * ((expert_rows(a.r, l.tid, &row0) + kTile - 1) / kTile);
+      n = expert_rows(a.r, l.tid, &row0);
+      m.first[l.tid] = row0;
+      m.rows[l.tid] = n;
     }
-    int incl = u;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const int v = __shfl_up(incl, d, kWave);
-      if (l.lane >= d) incl += v;
-    }
-    if (l.lane == kWave - 1) sm.wsum[l.wave] = incl;
+    prefix(l, n > kHalf ? ntiles * spans(n) : 0, nexp, m.pre, m.wsum[0]);
+    prefix(l, n > 0 && n <= kHalf ? ntiles : 0, nexp, m.pre_light, m.wsum[1]);
     __syncthreads();
-    int before = 0;
-#pragma unroll
-    for (int v = 0; v < kWaves; ++v) before += v < l.wave ? sm.wsum[v] : 0;
-    if (l.tid < nexp) sm.pre[l.tid + 1] = before + incl;
-    if (l.tid == 0) sm.pre[0] = 0;
-    __syncthreads();
-    const int total = uniform(pre[nexp]);
-    const int xcd = (int)blockIdx.x % 8, per = (total + 7) / 8;
+    const int all = uniform(m.pre[nexp]), lights = uniform(m.pre_light[nexp]);
     step = (int)gridDim.x / 8;
-    start = xcd * per + (int)blockIdx.x / 8;
-    hi = min(total, (xcd + 1) * per);
+    xcd = (int)blockIdx.x % 8;
+    const int per = (all + 7) / 8, per_light = (lights + 7) / 8;
+    full0 = xcd * per;
+    light0 = xcd * per_light;
+    full = max(0, min(per, all - full0));
+    const int over = uniform(full % step);
+    cut = 2 * over <= step ? over : 0;
+    full -= cut;
+    hi = full + 2 * cut + max(0, min(per_light, lights - light0));
   }
-  __device__ __forceinline__ int first() const { return start < hi ? start : kEnd; }
+  static __device__ __forceinline__ int spans(int n) { return (n + kTile - 1) / kTile; }
+
+  __device__ __forceinline__ int first() const {
+    const int it = (int)blockIdx.x / 8;
+    return it < hi ? it : kEnd;
+  }
   __device__ __forceinline__ int next(int it) const { return it + step < hi ? it + step : kEnd; }
 
   __device__ __forceinline__ Item item(int it) const {
-    int lo = 0, up = nexp;   // the last expert with pre[e] <= it
-    while (up - lo > 1) {
-      const int mid = (lo + up) >> 1;
-      if (uniform(pre[mid]) <= it) lo = mid;
-      else up = mid;
-    }
     Item x;
-    x.e = lo;
-    int64_t row0;
-    const int n = uniform(expert_rows(a.r, lo, &row0));
-    const int spans = (n + kTile - 1) / kTile;
-    const int at = it - uniform(pre[lo]);
-    const int tile = uniform(at / spans), span = at - tile * spans;
+    int tile, skip;
+    if (it < full + 2 * cut) {
+      const int half = it < full ? 0 : (it - full) & 1;
+      const int q = full0 + (it < full ? it : full + ((it - full) >> 1));
+      x.e = last_at_most(sm.pre, nexp, q);
+      const int n = uniform(sm.rows[x.e]), each = spans(n);
+      const int at = q - uniform(sm.pre[x.e]);
+      tile = uniform(at / each);
+      skip = (at - tile * each) * kTile + half * kHalf;
+      x.n = max(0, min(it < full ? kTile : kHalf, n - skip));
+    } else {
+      const int q = light0 + it - full - 2 * cut;
+      x.e = last_at_most(sm.pre_light, nexp, q);
+      const int n = uniform(sm.rows[x.e]);
+      tile = q - uniform(sm.pre_light[x.e]);
+      x.n = n;
+      skip = 0;
+    }
     x.f0 = tile * kFeatures;
-    x.row0 = uniform((int)row0) + (int64_t)span * kTile;
-    x.n = min(kTile, n - span * kTile);
+    x.row0 = uniform(sm.first[x.e]) + (int64_t)skip;
     return x;
   }
 
   __device__ __forceinline__ int contraction() const {
     return kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
   }
-  __device__ __forceinline__ int blocks(int) const { return contraction() / kBlock; }
-  __device__ __forceinline__ bool two(int it) const { return item(it).n > kHalf; }
+  __device__ __forceinline__ int blocks(const Item& x) const {
+    return x.n > 0 ? contraction() / kBlock : 0;
+  }
+  __device__ __forceinline__ bool two(const Item& x) const { return x.n > kHalf; }
 
-  __device__ __forceinline__ void load(const Lane& l, int it, A& la, B& lb) const {
-    const Item x = item(it);
+  __device__ __forceinline__ void load(const Lane& l, const Item& x, A& la, B& lb) const {
     const int H = a.r.H, I = a.r.I, K = contraction();
     const uint32_t row_bytes = (uint32_t)K * 2;
     if constexpr (kOp == kGateUp) {
@@ -755,9 +813,9 @@ struct RowsJob {
     }
   }
 
-  __device__ __forceinline__ void store(const Lane& l, int it, f32x4 (&acc)[TM][TN]) const {
-    const Item x = item(it);
+  __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN]) const {
     const int H = a.r.H, I = a.r.I;
+    if (x.n == 0) return;
     if constexpr (kOp == kDown || kOp == kDX) {
       store_tile(l, acc, a.out + (size_t)x.row0 * H + x.f0, H, x.n, H - x.f0);
       return;
@@ -842,7 +900,7 @@ struct WeightsJob {
   using B = Across;
   static constexpr int kEnd = -1;
   const WeightArgs& a;
-  const int* by_rank;
+  const Smem& sm;   // pre: the experts by rank
   int E, tm_n, tn_n, each, run, hi, start, step, xcd;
 
   struct Item {
@@ -850,18 +908,20 @@ struct WeightsJob {
     int64_t row0;
   };
 
-  __device__ __forceinline__ WeightsJob(const WeightArgs& args, const Lane& l, Smem& sm)
-      : a(args), by_rank(sm.pre) {
+  __device__ __forceinline__ WeightsJob(const WeightArgs& args, const Lane& l, Smem& m)
+      : a(args), sm(m) {
     E = a.r.counts ? a.r.E : 1;
-    int* rows = sm.rows;
-    int64_t row0;
-    const int n = l.tid < E ? expert_rows(a.r, l.tid, &row0) : 0;
-    if (l.tid < E) rows[l.tid] = n;
+    int n = 0, row0 = 0;
+    if (l.tid < E) {
+      n = expert_rows(a.r, l.tid, &row0);
+      m.first[l.tid] = row0;
+      m.rows[l.tid] = n;
+    }
     __syncthreads();
     if (l.tid < E) {
       int rank = 0;
-      for (int e = 0; e < E; ++e) rank += rows[e] > n || (rows[e] == n && e < l.tid);
-      sm.pre[rank] = l.tid;
+      for (int e = 0; e < E; ++e) rank += m.rows[e] > n || (m.rows[e] == n && e < l.tid);
+      m.pre[rank] = l.tid;
     }
     __syncthreads();
     tm_n = (a.M + kTile - 1) / kTile;
@@ -883,7 +943,7 @@ struct WeightsJob {
   // the tile of place it in this XCD's order; >= each: none
   __device__ __forceinline__ int tile_of(int it, int* e) const {
     const int rank = uniform(it / run);
-    *e = uniform(by_rank[rank]);
+    *e = uniform(sm.pre[rank]);
     const int at = it - rank * run;
     return xcd < 0 ? at : ((xcd + *e) & 7) * run + at;
   }
@@ -904,22 +964,19 @@ struct WeightsJob {
     const int tm = uniform(in_band / width);
     x.m0 = tm * kTile;
     x.n0 = (4 * band + in_band - tm * width) * kTile;
-    int64_t row0;
-    x.n = uniform(expert_rows(a.r, x.e, &row0));
-    x.row0 = uniform((int)row0);
+    x.n = uniform(sm.rows[x.e]);
+    x.row0 = uniform(sm.first[x.e]);
     return x;
   }
-  __device__ __forceinline__ int blocks(int it) const {
-    return (item(it).n + kBlock - 1) / kBlock;
+  __device__ __forceinline__ int blocks(const Item& x) const {
+    return (x.n + kBlock - 1) / kBlock;
   }
-  __device__ __forceinline__ bool two(int) const { return true; }
-  __device__ __forceinline__ void load(const Lane& l, int it, Across& la, Across& lb) const {
-    const Item x = item(it);
+  __device__ __forceinline__ bool two(const Item&) const { return true; }
+  __device__ __forceinline__ void load(const Lane& l, const Item& x, Across& la, Across& lb) const {
     la.set(l, a.m_rows + (size_t)x.row0 * a.M, (uint32_t)a.M * 2, x.n, x.m0);
     lb.set(l, a.n_rows + (size_t)x.row0 * a.N, (uint32_t)a.N * 2, x.n, x.n0);
   }
-  __device__ __forceinline__ void store(const Lane& l, int it, f32x4 (&acc)[TM][TN]) const {
-    const Item x = item(it);
+  __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN]) const {
     store_tile(l, acc, static_cast<TOut*>(a.out) + ((size_t)x.e * a.N + x.n0) * a.M + x.m0, a.M,
                min(kTile, a.N - x.n0), a.M - x.m0);
   }
@@ -963,13 +1020,13 @@ template <Op kOp, bool kFp8>
 hipError_t launch_rows(const Args& a, hipStream_t s) {
   const int per_tile = kOp == kGateUp ? kTile / 2 : kTile;
   const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
-  // spans: one for each 256 rows, and a short one an expert
+  // spans: one for each 256 rows, and a short one an expert; twice, as items may be cut in two
   const int64_t pairs = a.r.counts ? a.r.tokens * a.r.K : a.r.tokens;
   const int64_t spans = pairs / kTile + (a.r.counts ? (a.r.E < pairs ? a.r.E : pairs) : 1);
   const int64_t items = spans * ((F + per_tile - 1) / per_tile);
   if (pairs == 0) return hipSuccess;
   if (items >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((rows_kernel<kOp, kFp8>), dim3(grid_of(items)), dim3(kThreads), 0, s, a);
+  hipLaunchKernelGGL((rows_kernel<kOp, kFp8>), dim3(grid_of(2 * items)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
 

@@ -118,8 +118,8 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
                             x_rows, s);
     xr = x_rows;
   }
-  if (e == hipSuccess && dw13) e = moe::launch_train_dw13(r, xr, dh, dw13, dwdt == MOE_F32, s);
-  if (e == hipSuccess && dw2) e = moe::launch_train_dw2(r, act, dy, dw2, dwdt == MOE_F32, s);
+  if (e == hipSuccess && (dw13 || dw2))
+    e = moe::launch_train_dw(r, xr, dh, dw13, act, dy, dw2, dwdt == MOE_F32, s);
   return hip_status(e, what);
 }
 

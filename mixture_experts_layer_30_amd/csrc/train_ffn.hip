@@ -152,11 +152,6 @@ __device__ __forceinline__ void in_order(int g, f32x4 even, f32x4 odd, float* v)
   v[4] = hi.x; v[5] = hi.y; v[6] = hi.z; v[7] = hi.w;
 }
 
-// the first feature of the 8 of pair p (of 4) of a lane's tiles
-__device__ __forceinline__ int pair_feature(const Lane& l, int p) {
-  return kHalf * (p >> 1) + 64 * l.wm + 32 * (p & 1) + 8 * l.g;
-}
-
 // the row of a lane's sums in MFMA tile tn
 __device__ __forceinline__ int tile_row(const Lane& l, int tn) { return (l.wn + 4 * tn) * 16 + l.m; }
 
@@ -544,13 +539,16 @@ __device__ __forceinline__ uint32_t bf16x2_of(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{lo, hi}, bf16x2));
 }
 
-__device__ __forceinline__ void store8(uint16_t* p, const float* v) {
-  *reinterpret_cast<u32x4*>(p) = u32x4{bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]),
-                                       bf16x2_of(v[4], v[5]), bf16x2_of(v[6], v[7])};
+__device__ __forceinline__ u32x4 bf16x8_of(const float* v) {
+  return u32x4{bf16x2_of(v[0], v[1]), bf16x2_of(v[2], v[3]), bf16x2_of(v[4], v[5]),
+               bf16x2_of(v[6], v[7])};
 }
 
-__device__ __forceinline__ void store16(Rsrc r, uint32_t lane_off, uint32_t off, u32x4 v) {
-  __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)lane_off, (int)uniform(off), 0);
+// The whole offset in the lane's register, none in a scalar one: after a 16-byte store with a
+// scalar offset the next instruction may overwrite the data before its last lanes are read
+// (seen as wrong values in lanes 12 .. 15 of 16), and the compiler keeps them apart without one.
+__device__ __forceinline__ void store16(Rsrc r, uint32_t off, u32x4 v) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, (int)off, 0, 0);
 }
 
 // A lane's 8 sums of a pair of tiles, in the order of their features, at byte off
@@ -558,12 +556,12 @@ __device__ __forceinline__ void store_pair(Rsrc r, uint32_t off, uint32_t d, boo
                                            f32x4 b, const uint16_t*) {
   const uint32_t a0 = bf16x2_of(a.x, a.y), a1 = bf16x2_of(a.z, a.w);
   const uint32_t b0 = bf16x2_of(b.x, b.y), b1 = bf16x2_of(b.z, b.w);
-  store16(r, off, d, odd ? u32x4{b0, b1, a0, a1} : u32x4{a0, a1, b0, b1});
+  store16(r, off + d, odd ? u32x4{b0, b1, a0, a1} : u32x4{a0, a1, b0, b1});
 }
 __device__ __forceinline__ void store_pair(Rsrc r, uint32_t off, uint32_t d, bool odd, f32x4 a,
                                            f32x4 b, const float*) {
-  store16(r, off + (odd ? 16 : 0), d, __builtin_bit_cast(u32x4, a));
-  store16(r, off + (odd ? 0 : 16), d, __builtin_bit_cast(u32x4, b));
+  store16(r, off + d + (odd ? 16 : 0), __builtin_bit_cast(u32x4, a));
+  store16(r, off + d + (odd ? 0 : 16), __builtin_bit_cast(u32x4, b));
 }
 
 // The tile at out, of rows of F values: `rows` of its rows and `cols` of its columns are there.
@@ -589,8 +587,7 @@ __device__ __forceinline__ void store_tile(const Lane& l, const f32x4 (&acc)[TM]
   }
 }
 
-__device__ __forceinline__ void load8(const uint16_t* p, float* v) {
-  const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+__device__ __forceinline__ void bf16x8_to(u32x4 q, float* v) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -619,35 +616,88 @@ struct Args {
   uint8_t* scales;
 };
 
-// 8 neighbours of the kept values of one row: columns col .. col + 7 of 2I
-template <bool kFp8>
-__device__ __forceinline__ void keep8(const Args& a, size_t row, int col, const float* v,
-                                      bool first, bool in) {
-  const size_t at = row * (size_t)(2 * a.r.I) + col;
-  if constexpr (kFp8) {
-    float most = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) most = abs_max(most, v[j]);
-    const int byte = scale_byte(column_max(most));   // every lane takes part
-    if (in) {
-      *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.h) + at) =
-          pack_e4m3x8(v, inverse_scale(byte));
-      if (first) a.scales[at / 32] = (uint8_t)byte;
-    }
-  } else {
-    if (in) store8(a.h + at, v);
+// A row buffer from a span's first row on, of `cols` values a row, as a lane sees it: byte
+// offsets of its row and columns in one descriptor, rows past the span's last refused by range.
+template <class T>
+struct Rows {
+  const uint8_t* base;
+  uint32_t row_bytes, all, off;
+  // row, col: this lane's first; n: the span's rows
+  __device__ __forceinline__ Rows(const T* p, size_t row0, int cols, int n, int row, int col) {
+    row_bytes = (uint32_t)cols * (uint32_t)sizeof(T);
+    base = reinterpret_cast<const uint8_t*>(p + row0 * cols);
+    all = (uint32_t)n * row_bytes;
+    off = (uint32_t)row * row_bytes + (uint32_t)col * (uint32_t)sizeof(T);
   }
-}
+  // `there`: the columns are no further than the edge (the same for the wavefront)
+  __device__ __forceinline__ Rsrc rsrc(bool there) const { return make_rsrc(base, there ? all : 0); }
+};
 
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+// The gate and up values kept: two Rows of them, and of their scales
 template <bool kFp8>
-__device__ __forceinline__ void kept8(const Args& a, size_t row, int col, float* v) {
-  const size_t at = row * (size_t)(2 * a.r.I) + col;
-  if constexpr (kFp8)
-    unpack_e4m3x8(*reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(a.h) + at),
-                  scale_of(a.scales[at / 32]), v);
-  else
-    load8(a.h + at, v);
-}
+struct Kept {
+  typedef typename std::conditional<kFp8, uint8_t, uint16_t>::type Code;
+  Rows<Code> h;
+  Rows<uint8_t> s;
+  uint32_t up, up_s;   // from gate to up
+  __device__ __forceinline__ Kept(const void* values, const uint8_t* scales, size_t row0, int I,
+                                  int n, int row, int col)
+      : h(static_cast<const Code*>(values), row0, 2 * I, n, row, col),
+        s(scales, row0, 2 * I / 32, n, row, col / 32) {
+    up = (uint32_t)I * (uint32_t)sizeof(Code);
+    up_s = (uint32_t)I / 32;
+  }
+  // 8 neighbours of row + 64 tn, col + add (a multiple of 32), of gate (which 0) or up (1)
+  __device__ __forceinline__ uint32_t at(int tn, int which) const {
+    return (uint32_t)(64 * tn) * h.row_bytes + (which ? up : 0);
+  }
+  __device__ __forceinline__ uint32_t at_s(int tn, int which) const {
+    return (uint32_t)(64 * tn) * s.row_bytes + (which ? up_s : 0);
+  }
+  __device__ __forceinline__ void keep(const Lane& l, bool there, int tn, int add, int which,
+                                       const float* v) const {
+    if constexpr (kFp8) {
+      float most = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) most = abs_max(most, v[j]);
+      const int byte = scale_byte(column_max(most));   // every lane takes part
+      const uint2 c = pack_e4m3x8(v, inverse_scale(byte));
+      __builtin_amdgcn_raw_buffer_store_b64(u32x2{c.x, c.y}, h.rsrc(there), (int)(h.off + add),
+                                            (int)uniform(at(tn, which)), 0);
+      // one lane of the four that share a block has its offset, the others none
+      __builtin_amdgcn_raw_buffer_store_b8((uint8_t)byte, s.rsrc(there),
+                                           (int)(l.g == 0 ? s.off + add / 32 : kOutside),
+                                           (int)uniform(at_s(tn, which)), 0);
+    } else {
+      store16(h.rsrc(there), h.off + add * 2 + at(tn, which), bf16x8_of(v));
+    }
+  }
+  struct Raw {
+    u32x4 q;
+    int byte;
+  };
+  __device__ __forceinline__ Raw read(bool there, int tn, int add, int which) const {
+    Raw r;
+    if constexpr (kFp8) {
+      const u32x2 c = __builtin_amdgcn_raw_buffer_load_b64(h.rsrc(there), (int)(h.off + add),
+                                                           (int)uniform(at(tn, which)), 0);
+      r.q = u32x4{c.x, c.y, 0, 0};
+      r.byte = __builtin_amdgcn_raw_buffer_load_b8(s.rsrc(there), (int)(s.off + add / 32),
+                                                   (int)uniform(at_s(tn, which)), 0);
+    } else {
+      r.q = __builtin_amdgcn_raw_buffer_load_b128(h.rsrc(there), (int)(h.off + add * 2),
+                                                  (int)uniform(at(tn, which)), 0);
+      r.byte = 0;
+    }
+    return r;
+  }
+  __device__ __forceinline__ void values(const Raw& r, float* v) const {
+    if constexpr (kFp8) unpack_e4m3x8(uint2{r.q.x, r.q.y}, scale_of(r.byte & 255), v);
+    else bf16x8_to(r.q, v);
+  }
+};
 
 // the rows of expert e, inside the row buffers whatever the plan says
 __device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int* row0) {
@@ -820,48 +870,59 @@ struct RowsJob {
       store_tile(l, acc, a.out + (size_t)x.row0 * H + x.f0, H, x.n, H - x.f0);
       return;
     }
+    const int row = tile_row(l, 0);
+    if constexpr (kOp == kGateUp) {
+      const int i = x.f0 + 32 * l.wm + 8 * l.g;   // + 64 in the second half
+      const Kept<kFp8> kept(a.h, a.scales, (size_t)x.row0, I, x.n, row, i);
+      const Rows<uint16_t> act(a.act, (size_t)x.row0, I, x.n, row, i);
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn) {
-      const int j = tile_row(l, tn);
-      const bool in = j < x.n;
-      const size_t row = (size_t)(x.row0 + j);
-      if constexpr (kOp == kGateUp) {
+      for (int h = 0; h < 2; ++h) {
+        const bool there = x.f0 + 64 * h + 32 * l.wm < I;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = x.f0 + 64 * h + 32 * l.wm + 8 * l.g;
+        for (int tn = 0; tn < TN; ++tn) {
           float gv[8], uv[8], av[8];
           in_order(l.g, acc[4 * h][tn], acc[4 * h + 1][tn], gv);
           in_order(l.g, acc[4 * h + 2][tn], acc[4 * h + 3][tn], uv);
 #pragma unroll
           for (int q = 0; q < 8; ++q) av[q] = silu(gv[q]) * uv[q];
-          const bool here = in && i < I;
-          keep8<kFp8>(a, row, i, gv, l.g == 0, here);
-          keep8<kFp8>(a, row, I + i, uv, l.g == 0, here);
-          if (here) store8(a.act + row * I + i, av);
+          kept.keep(l, there, tn, 64 * h, 0, gv);
+          kept.keep(l, there, tn, 64 * h, 1, uv);
+          store16(act.rsrc(there), act.off + 128 * h + (uint32_t)(64 * tn) * act.row_bytes,
+                  bf16x8_of(av));
         }
-      } else if constexpr (kOp == kDAct) {
+      }
+    } else if constexpr (kOp == kDAct) {
+      const int f = x.f0 + 64 * l.wm + 8 * l.g;   // + 128 in the second half, + 32 in odd pairs
+      const Kept<kFp8> kept(a.h, a.scales, (size_t)x.row0, I, x.n, row, f);
+      const Rows<uint16_t> act(a.act, (size_t)x.row0, I, x.n, row, f);
+      const Rows<uint16_t> dh(a.dh, (size_t)x.row0, 2 * I, x.n, row, f);
 #pragma unroll
-        for (int p = 0; p < TM / 2; ++p) {
-          const int f = x.f0 + pair_feature(l, p);
-          float v[8];
+      for (int p = 0; p < TM / 2; ++p) {
+        const int add = kHalf * (p >> 1) + 32 * (p & 1);
+        const bool there = x.f0 + 64 * l.wm + add < I;
+        typename Kept<kFp8>::Raw gr[TN], ur[TN];
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) {   // all of them in flight
+          gr[tn] = kept.read(there, tn, add, 0);
+          ur[tn] = kept.read(there, tn, add, 1);
+        }
+#pragma unroll
+        for (int tn = 0; tn < TN; ++tn) {
+          float v[8], gv[8], uv[8], av[8], dg[8], du[8];
           in_order(l.g, acc[2 * p][tn], acc[2 * p + 1][tn], v);
-          {
-            if (in && f < I) {
-              float gv[8], uv[8], av[8], dg[8], du[8];
-              kept8<kFp8>(a, row, f, gv);
-              kept8<kFp8>(a, row, I + f, uv);
+          kept.values(gr[tn], gv);
+          kept.values(ur[tn], uv);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float s = sigmoid(gv[q]), gs = gv[q] * s;
-                av[q] = gs * uv[q];
-                dg[q] = v[q] * uv[q] * (s * (1.0f + gv[q] * (1.0f - s)));
-                du[q] = v[q] * gs;
-              }
-              store8(a.act + row * I + f, av);
-              store8(a.dh + row * (2 * (size_t)I) + f, dg);
-              store8(a.dh + row * (2 * (size_t)I) + I + f, du);
-            }
+          for (int q = 0; q < 8; ++q) {
+            const float s = sigmoid(gv[q]), gs = gv[q] * s;
+            av[q] = gs * uv[q];
+            dg[q] = v[q] * uv[q] * (s * (1.0f + gv[q] * (1.0f - s)));
+            du[q] = v[q] * gs;
           }
+          const uint32_t d = (uint32_t)(64 * tn) * act.row_bytes;
+          store16(act.rsrc(there), act.off + 2 * add + d, bf16x8_of(av));
+          store16(dh.rsrc(there), dh.off + 2 * add + 2 * d, bf16x8_of(dg));
+          store16(dh.rsrc(there), dh.off + 2 * add + 2 * d + act.row_bytes, bf16x8_of(du));
         }
       }
     }
@@ -885,12 +946,15 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
 // equal length, so that skewed routing leaves no XCD with the busy experts and the short
 // items fill in at the end (contiguous experts per XCD: Qwen2-shaped dW13 of 3001 tokens with
 // skewed routing 2.4 ms).
+// Both matrices' gradients are one launch, with one end: per expert dW13's tiles, then dW2's.
 struct WeightArgs {
   TrainRows r;
-  const uint16_t* m_rows;
-  const uint16_t* n_rows;
-  void* out;
-  int M, N;
+  struct Product {
+    const uint16_t* m_rows;
+    const uint16_t* n_rows;
+    void* out;
+    int M, N;
+  } p[2];   // M 0: none
 };
 
 template <class TOut>
@@ -901,16 +965,18 @@ struct WeightsJob {
   static constexpr int kEnd = -1;
   const WeightArgs& a;
   const Smem& sm;   // pre: the experts by rank
-  int E, tm_n, tn_n, each, run, hi, start, step, xcd;
+  int each0, each1, run0, run, hi, start, step, xcd;
 
   struct Item {
-    int e, m0, n0, n;
+    int e, k, m0, n0, n;   // k: the product
     int64_t row0;
   };
 
+  static __device__ __forceinline__ int tiles(int n) { return (n + kTile - 1) / kTile; }
+
   __device__ __forceinline__ WeightsJob(const WeightArgs& args, const Lane& l, Smem& m)
       : a(args), sm(m) {
-    E = a.r.counts ? a.r.E : 1;
+    const int E = a.r.counts ? a.r.E : 1;
     int n = 0, row0 = 0;
     if (l.tid < E) {
       n = expert_rows(a.r, l.tid, &row0);
@@ -924,32 +990,37 @@ struct WeightsJob {
       m.pre[rank] = l.tid;
     }
     __syncthreads();
-    tm_n = (a.M + kTile - 1) / kTile;
-    tn_n = (a.N + kTile - 1) / kTile;
-    each = tm_n * tn_n;
-    if (E * (int64_t)each <= (int64_t)gridDim.x) {   // an item a workgroup
-      run = each;
+    each0 = tiles(a.p[0].M) * tiles(a.p[0].N);
+    each1 = tiles(a.p[1].M) * tiles(a.p[1].N);
+    if (E * (int64_t)(each0 + each1) <= (int64_t)gridDim.x) {   // an item a workgroup
+      run0 = each0;
+      run = each0 + each1;
       xcd = -1;
       start = (int)blockIdx.x;
       step = (int)gridDim.x;
     } else {
-      run = (each + 7) / 8;
+      run0 = (each0 + 7) / 8;
+      run = run0 + (each1 + 7) / 8;
       xcd = (int)blockIdx.x % 8;
       start = (int)blockIdx.x / 8;
       step = (int)gridDim.x / 8;
     }
     hi = E * run;
   }
-  // the tile of place it in this XCD's order; >= each: none
-  __device__ __forceinline__ int tile_of(int it, int* e) const {
+  // the expert, product and tile of place it in this XCD's order; false: none
+  __device__ __forceinline__ bool tile_of(int it, int* e, int* k, int* tile) const {
     const int rank = uniform(it / run);
     *e = uniform(sm.pre[rank]);
-    const int at = it - rank * run;
-    return xcd < 0 ? at : ((xcd + *e) & 7) * run + at;
+    int at = it - rank * run;
+    *k = at >= run0;
+    const int part = *k ? run - run0 : run0;
+    if (*k) at -= run0;
+    *tile = xcd < 0 ? at : ((xcd + *e) & 7) * part + at;
+    return *tile < (*k ? each1 : each0);
   }
   __device__ __forceinline__ int held(int it) const {
-    int e;
-    while (it < hi && tile_of(it, &e) >= each) it += step;
+    int e, k, tile;
+    while (it < hi && !tile_of(it, &e, &k, &tile)) it += step;
     return it < hi ? it : kEnd;
   }
   __device__ __forceinline__ int first() const { return held(start); }
@@ -957,7 +1028,9 @@ struct WeightsJob {
 
   __device__ __forceinline__ Item item(int it) const {
     Item x;
-    const int at = tile_of(it, &x.e);
+    int at;
+    tile_of(it, &x.e, &x.k, &at);
+    const int tm_n = tiles(a.p[x.k].M), tn_n = tiles(a.p[x.k].N);
     // tiles in bands of 4 along N, so that those at work together share their operands
     const int band = uniform(at / (4 * tm_n)), in_band = at - band * 4 * tm_n;
     const int width = min(4, tn_n - 4 * band);
@@ -973,12 +1046,14 @@ struct WeightsJob {
   }
   __device__ __forceinline__ bool two(const Item&) const { return true; }
   __device__ __forceinline__ void load(const Lane& l, const Item& x, Across& la, Across& lb) const {
-    la.set(l, a.m_rows + (size_t)x.row0 * a.M, (uint32_t)a.M * 2, x.n, x.m0);
-    lb.set(l, a.n_rows + (size_t)x.row0 * a.N, (uint32_t)a.N * 2, x.n, x.n0);
+    const WeightArgs::Product& p = a.p[x.k];
+    la.set(l, p.m_rows + (size_t)x.row0 * p.M, (uint32_t)p.M * 2, x.n, x.m0);
+    lb.set(l, p.n_rows + (size_t)x.row0 * p.N, (uint32_t)p.N * 2, x.n, x.n0);
   }
   __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN]) const {
-    store_tile(l, acc, static_cast<TOut*>(a.out) + ((size_t)x.e * a.N + x.n0) * a.M + x.m0, a.M,
-               min(kTile, a.N - x.n0), a.M - x.m0);
+    const WeightArgs::Product& p = a.p[x.k];
+    store_tile(l, acc, static_cast<TOut*>(p.out) + ((size_t)x.e * p.N + x.n0) * p.M + x.m0, p.M,
+               min(kTile, p.N - x.n0), p.M - x.m0);
   }
 };
 
@@ -1027,15 +1102,6 @@ hipError_t launch_rows(const Args& a, hipStream_t s) {
   if (pairs == 0) return hipSuccess;
   if (items >= (int64_t)1 << 31) return hipErrorInvalidValue;
   hipLaunchKernelGGL((rows_kernel<kOp, kFp8>), dim3(grid_of(2 * items)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
-}
-
-hipError_t launch_weights(const WeightArgs& a, bool f32, hipStream_t s) {
-  const int64_t items = (int64_t)(a.r.counts ? a.r.E : 1) * ((a.M + kTile - 1) / kTile) *
-                        ((a.N + kTile - 1) / kTile);
-  const dim3 grid(grid_of(items)), block(kThreads);
-  if (f32) hipLaunchKernelGGL(weights_kernel<float>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(weights_kernel<uint16_t>, grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -1089,14 +1155,22 @@ hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* 
   return launch_rows<kDX, false>(a, s);
 }
 
-hipError_t launch_train_dw13(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
-                             void* dw13, bool f32, hipStream_t s) {
-  return launch_weights(WeightArgs{r, x_rows, dh, dw13, r.H, 2 * r.I}, f32, s);
-}
-
-hipError_t launch_train_dw2(const TrainRows& r, const uint16_t* act, const void* dy, void* dw2,
-                            bool f32, hipStream_t s) {
-  return launch_weights(WeightArgs{r, act, static_cast<const uint16_t*>(dy), dw2, r.I, r.H}, f32, s);
+hipError_t launch_train_dw(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
+                           void* dw13, const uint16_t* act, const void* dy, void* dw2, bool f32,
+                           hipStream_t s) {
+  const WeightArgs a{r,
+                     {{x_rows, dh, dw13, dw13 ? r.H : 0, 2 * r.I},
+                      {act, static_cast<const uint16_t*>(dy), dw2, dw2 ? r.I : 0, r.H}}};
+  int64_t items = 0;
+  for (const WeightArgs::Product& p : a.p)
+    items += (int64_t)((p.M + kTile - 1) / kTile) * ((p.N + kTile - 1) / kTile);
+  if (r.counts) items *= r.E;
+  if (items == 0) return hipSuccess;
+  if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
+  const dim3 grid(grid_of(items)), block(kThreads);
+  if (f32) hipLaunchKernelGGL(weights_kernel<float>, grid, block, 0, s, a);
+  else hipLaunchKernelGGL(weights_kernel<uint16_t>, grid, block, 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace moe

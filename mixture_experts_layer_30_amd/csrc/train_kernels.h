@@ -39,13 +39,11 @@ hipError_t launch_train_dact(const TrainRows& r, const void* w2, const void* dy,
 // dx [rows][H] = w13^T dh
 hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
                            hipStream_t s);
-// dw13 [E][2I][H] = sum over an expert's rows of dh x^T (x_rows: x by row); f32: its type is
-// fp32, else bf16
-hipError_t launch_train_dw13(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
-                             void* dw13, bool f32, hipStream_t s);
-// dw2 [E][H][I] = sum over an expert's rows of dy act^T
-hipError_t launch_train_dw2(const TrainRows& r, const uint16_t* act, const void* dy, void* dw2,
-                            bool f32, hipStream_t s);
+// dw13 [E][2I][H] = sum over an expert's rows of dh x^T (x_rows: x by row), and dw2 [E][H][I] that
+// of dy act^T; either null: not wanted; f32: their type is fp32, else bf16
+hipError_t launch_train_dw(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
+                           void* dw13, const uint16_t* act, const void* dy, void* dw2, bool f32,
+                           hipStream_t s);
 
 // [T][H] values in blocks of 32 to e4m3 codes and the biased exponents of the blocks' scales
 hipError_t launch_pack_fp8(const void* x, int dt, int64_t T, int H, uint8_t* codes,

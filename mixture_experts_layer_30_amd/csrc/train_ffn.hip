@@ -577,13 +577,15 @@ __device__ __forceinline__ void store_tile(const Lane& l, const f32x4 (&acc)[TM]
   // up to the end of the last row
   const uint32_t all = (uint32_t)(rows - 1) * row_bytes + (uint32_t)min(cols, kTile) * e;
 #pragma unroll
-  for (int p = 0; p < TM / 2; ++p) {
-    const int f = kHalf * (p >> 1) + 32 * (p & 1);
-    const Rsrc r = make_rsrc(base, f + 64 * l.wm < cols ? all : 0);
+  for (int tn = 0; tn < TN; ++tn) {
+    if (64 * tn >= rows) break;   // few rows: the rest of the code is not even fetched
 #pragma unroll
-    for (int tn = 0; tn < TN; ++tn)
+    for (int p = 0; p < TM / 2; ++p) {
+      const int f = kHalf * (p >> 1) + 32 * (p & 1);
+      const Rsrc r = make_rsrc(base, f + 64 * l.wm < cols ? all : 0);
       store_pair(r, off + (uint32_t)f * e, (uint32_t)(64 * tn) * row_bytes, l.g & 1,
                  acc[2 * p][tn], acc[2 * p + 1][tn], out);
+    }
   }
 }
 
@@ -876,10 +878,11 @@ struct RowsJob {
       const Kept<kFp8> kept(a.h, a.scales, (size_t)x.row0, I, x.n, row, i);
       const Rows<uint16_t> act(a.act, (size_t)x.row0, I, x.n, row, i);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool there = x.f0 + 64 * h + 32 * l.wm < I;
+      for (int tn = 0; tn < TN; ++tn) {
+        if (64 * tn >= x.n) break;   // few rows: the rest of the code is not even fetched
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn) {
+        for (int h = 0; h < 2; ++h) {
+          const bool there = x.f0 + 64 * h + 32 * l.wm < I;
           float gv[8], uv[8], av[8];
           in_order(l.g, acc[4 * h][tn], acc[4 * h + 1][tn], gv);
           in_order(l.g, acc[4 * h + 2][tn], acc[4 * h + 3][tn], uv);
@@ -897,21 +900,24 @@ struct RowsJob {
       const Rows<uint16_t> act(a.act, (size_t)x.row0, I, x.n, row, f);
       const Rows<uint16_t> dh(a.dh, (size_t)x.row0, 2 * I, x.n, row, f);
 #pragma unroll
-      for (int p = 0; p < TM / 2; ++p) {
-        const int add = kHalf * (p >> 1) + 32 * (p & 1);
-        const bool there = x.f0 + 64 * l.wm + add < I;
-        typename Kept<kFp8>::Raw gr[TN], ur[TN];
+      for (int tn = 0; tn < TN; ++tn) {
+        if (64 * tn >= x.n) break;
+        typename Kept<kFp8>::Raw gr[TM / 2], ur[TM / 2];
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn) {   // all of them in flight
-          gr[tn] = kept.read(there, tn, add, 0);
-          ur[tn] = kept.read(there, tn, add, 1);
+        for (int p = 0; p < TM / 2; ++p) {   // all of them in flight
+          const int add = kHalf * (p >> 1) + 32 * (p & 1);
+          const bool there = x.f0 + 64 * l.wm + add < I;
+          gr[p] = kept.read(there, tn, add, 0);
+          ur[p] = kept.read(there, tn, add, 1);
         }
 #pragma unroll
-        for (int tn = 0; tn < TN; ++tn) {
+        for (int p = 0; p < TM / 2; ++p) {
+          const int add = kHalf * (p >> 1) + 32 * (p & 1);
+          const bool there = x.f0 + 64 * l.wm + add < I;
           float v[8], gv[8], uv[8], av[8], dg[8], du[8];
           in_order(l.g, acc[2 * p][tn], acc[2 * p + 1][tn], v);
-          kept.values(gr[tn], gv);
-          kept.values(ur[tn], uv);
+          kept.values(gr[p], gv);
+          kept.values(ur[p], uv);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const float s = sigmoid(gv[q]), gs = gv[q] * s;

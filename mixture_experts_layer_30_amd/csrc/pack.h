@@ -8,7 +8,7 @@
 // A value that is not finite becomes NaN and has no part in the maximum.
 #pragma once
 
-#include "common.h"
+#include "rows.h"
 
 namespace moe {
 
@@ -55,6 +55,12 @@ __device__ __forceinline__ void unpack_e4m3x8(uint2 c, float scale, float* v) {
   const f32x2 e = __builtin_amdgcn_cvt_pk_f32_fp8((int)c.y, true);
   v[0] = a.x * scale; v[1] = a.y * scale; v[2] = b.x * scale; v[3] = b.y * scale;
   v[4] = d.x * scale; v[5] = d.y * scale; v[6] = e.x * scale; v[7] = e.y * scale;
+}
+
+// the largest over a quad of lanes
+__device__ __forceinline__ float quad_max(float v) {
+  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kQuadXor1, 0xF, 0xF, false)));
+  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kQuadXor2, 0xF, 0xF, false)));
 }
 
 }  // namespace moe

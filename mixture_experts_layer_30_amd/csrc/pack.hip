@@ -16,11 +16,6 @@ namespace {
 constexpr int kPackThreads = 256;
 constexpr int kPackUnroll = 4;   // pieces of 8 values a lane has in flight
 
-__device__ __forceinline__ float quad_max(float v) {
-  v = fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kQuadXor1, 0xF, 0xF, false)));
-  return fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), kQuadXor2, 0xF, 0xF, false)));
-}
-
 // pieces: of 8 values, a multiple of 4
 template <class S>
 __global__ __launch_bounds__(kPackThreads) void pack_kernel(const typename S::T* __restrict__ x,

@@ -64,6 +64,12 @@ moe::TrainRows dense(int64_t T, int H, int I) {
   return moe::TrainRows{nullptr, nullptr, nullptr, T, T, 1, 1, H, I};
 }
 
+// bytes of partial sums, past the others: no more than all rows' in every part
+int64_t part_bytes(int64_t rows, int H, int I) {
+  const int64_t most = rows * (2 * I > H ? 2 * I : H) * 4 * moe::kMaxParts;
+  return most < moe::kPartBytes ? most : moe::kPartBytes;
+}
+
 int64_t rounded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
 moe_status forward(const char* what, const moe::TrainRows& r, const void* x, const void* w13,
@@ -79,8 +85,10 @@ moe_status forward(const char* what, const moe::TrainRows& r, const void* x, con
   if (!good(x, 16) || !good(w13, 16) || !good(w2, 16) || !good(y, 16)) return null_pointer(what);
   uint16_t* act = static_cast<uint16_t*>(workspace);
   const hipStream_t s = (hipStream_t)stream;
-  hipError_t e = moe::launch_train_gate_up(r, x, w13, saved, act, s);
-  if (e == hipSuccess) e = moe::launch_train_down(r, w2, act, y, s);
+  const moe::PartSpace space{(float*)(act + rounded(r.rows * r.I * 2) / 2),
+                             part_bytes(r.rows, r.H, r.I)};
+  hipError_t e = moe::launch_train_gate_up(r, x, w13, saved, act, space, s);
+  if (e == hipSuccess) e = moe::launch_train_down(r, w2, act, y, space, s);
   return hip_status(e, what);
 }
 
@@ -106,10 +114,12 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
   uint16_t* act = static_cast<uint16_t*>(workspace);
   uint16_t* dh = act + rounded(r.rows * r.I * 2) / 2;
   uint16_t* x_rows = dh + rounded(r.rows * r.I * 4) / 2;
+  const moe::PartSpace space{(float*)(x_rows + rounded(r.rows * r.H * 2) / 2),
+                             part_bytes(r.rows, r.H, r.I)};
   const hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;
-  if (r.tokens > 0) e = moe::launch_train_dact(r, w2, dy, saved, act, dh, s);
-  if (e == hipSuccess && dx && r.tokens > 0) e = moe::launch_train_dx(r, w13, dh, dx, s);
+  if (r.tokens > 0) e = moe::launch_train_dact(r, w2, dy, saved, act, dh, space, s);
+  if (e == hipSuccess && dx && r.tokens > 0) e = moe::launch_train_dx(r, w13, dh, dx, space, s);
   const uint16_t* xr = static_cast<const uint16_t*>(x);
   if (e == hipSuccess && dw13 && plan && r.tokens > 0) {
     // x by row: the contraction over rows then reads whole lines in order (gathering in it
@@ -119,7 +129,7 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
     xr = x_rows;
   }
   if (e == hipSuccess && (dw13 || dw2))
-    e = moe::launch_train_dw(r, xr, dh, dw13, act, dy, dw2, dwdt == MOE_F32, s);
+    e = moe::launch_train_dw(r, xr, dh, dw13, act, dy, dw2, dwdt == MOE_F32, space, s);
   return hip_status(e, what);
 }
 
@@ -139,12 +149,12 @@ int64_t moe_ffn_train_workspace_bytes(int64_t rows, int H, int I) {
   if (rows < 0 || rows >= (int64_t)1 << 31 || H < 64 || H % 64 != 0 || H > kMaxWidth || I < 64 ||
       I % 64 != 0 || I > kMaxWidth)
     return -1;
-  return rounded(rows * I * 2);
+  return rounded(rows * I * 2) + part_bytes(rows, H, I);
 }
 
 int64_t moe_ffn_backward_workspace_bytes(int64_t rows, int H, int I) {
-  const int64_t act = moe_ffn_train_workspace_bytes(rows, H, I);
-  // a and dh of every row, and x by row
+  const int64_t act = moe_ffn_train_workspace_bytes(rows, H, I);   // a, and partial sums
+  // dh of every row, and x by row
   return act < 0 ? -1 : act + rounded(rows * I * 4) + rounded(rows * H * 2);
 }
 

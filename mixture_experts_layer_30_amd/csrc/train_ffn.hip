@@ -589,6 +589,26 @@ __device__ __forceinline__ void store_tile(const Lane& l, const f32x4 (&acc)[TM]
   }
 }
 
+// The sums of a gate/up tile in fp32, out of rows of 2I values (its first column of gate), 64
+// columns in each half of the tile, up's I further
+__device__ __forceinline__ void store_gate_up(const Lane& l, const f32x4 (&acc)[TM][TN], float* out,
+                                              int I, int rows, int cols) {
+  const uint32_t row_bytes = (uint32_t)I * 8;
+  const uint32_t off = (uint32_t)(l.wn * 16 + l.m) * row_bytes + (uint32_t)(32 * l.wm + 8 * l.g) * 4;
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(out);
+  const uint32_t all = (uint32_t)(rows - 1) * row_bytes + (uint32_t)(I + min(cols, kHalf)) * 4;
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) {
+    if (64 * tn >= rows) break;
+#pragma unroll
+    for (int p = 0; p < TM / 2; ++p) {   // gate, up, gate, up
+      const Rsrc r = make_rsrc(base, 64 * (p >> 1) + 32 * l.wm < cols ? all : 0);
+      store_pair(r, off + (uint32_t)(64 * (p >> 1) + (p & 1 ? I : 0)) * 4,
+                 (uint32_t)(64 * tn) * row_bytes, l.g & 1, acc[2 * p][tn], acc[2 * p + 1][tn], out);
+    }
+  }
+}
+
 __device__ __forceinline__ void bf16x8_to(u32x4 q, float* v) {
   const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
@@ -599,6 +619,18 @@ __device__ __forceinline__ void bf16x8_to(u32x4 q, float* v) {
 }
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+// a, and the gradients of g and u, from that of a
+__device__ __forceinline__ void gradients(const float* da, const float* g, const float* u, float* a,
+                                          float* dg, float* du) {
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    const float s = sigmoid(g[q]), gs = g[q] * s;
+    a[q] = gs * u[q];
+    dg[q] = da[q] * u[q] * (s * (1.0f + g[q] * (1.0f - s)));
+    du[q] = da[q] * gs;
+  }
+}
 
 // the largest of v over the 4 lane groups of a column: 32 features
 __device__ __forceinline__ float column_max(float v) {
@@ -616,6 +648,8 @@ struct Args {
   uint16_t* out;
   uint16_t* h;          // kept values: bf16, or codes
   uint8_t* scales;
+  float* part;          // partial sums [splits][rows][features], where the contraction is split
+  int splits;
 };
 
 // A row buffer from a span's first row on, of `cols` values a row, as a lane sees it: byte
@@ -746,7 +780,10 @@ __device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
 // 128 rows come after all others, whose items take twice as long (Qwen2-shaped da and dx of 3001
 // tokens with skewed routing: 517 -> 472 and 817 -> 742 us).  Where a run's last round would leave
 // half the workgroups or more without an item, its items are cut into two of 128 rows.
-template <Op kOp, bool kFp8>
+//
+// kSplit: the contraction of every item is cut into a.splits parts, items of their own, whose sums
+// go to a.part and are added by the finish kernels.
+template <Op kOp, bool kFp8, bool kSplit>
 struct RowsJob {
   static constexpr bool kAAcross = kOp == kDAct || kOp == kDX, kBAcross = false;
   using A = typename std::conditional<kAAcross, Across, Along>::type;
@@ -760,7 +797,7 @@ struct RowsJob {
   int hi;
 
   struct Item {
-    int e, f0, n;
+    int e, f0, n, part, block0, blocks;   // blocks block0 .. of the contraction
     int64_t row0;
   };
 
@@ -785,9 +822,10 @@ struct RowsJob {
     light0 = xcd * per_light;
     full = max(0, min(per, all - full0));
     const int over = uniform(full % step);
-    cut = 2 * over <= step ? over : 0;
+    cut = !kSplit && 2 * over <= step ? over : 0;
     full -= cut;
     hi = full + 2 * cut + max(0, min(per_light, lights - light0));
+    if (kSplit) hi *= a.splits;
   }
   static __device__ __forceinline__ int spans(int n) { return (n + kTile - 1) / kTile; }
 
@@ -799,6 +837,12 @@ struct RowsJob {
 
   __device__ __forceinline__ Item item(int it) const {
     Item x;
+    x.part = 0;
+    if (kSplit) {
+      const int whole = uniform(it / a.splits);
+      x.part = it - whole * a.splits;
+      it = whole;
+    }
     int tile, skip;
     if (it < full + 2 * cut) {
       const int half = it < full ? 0 : (it - full) & 1;
@@ -819,41 +863,47 @@ struct RowsJob {
     }
     x.f0 = tile * kFeatures;
     x.row0 = uniform(sm.first[x.e]) + (int64_t)skip;
+    const int all = x.n > 0 ? contraction() / kBlock : 0;
+    x.block0 = 0;
+    x.blocks = all;
+    if (kSplit) {
+      const int each = uniform((all + a.splits - 1) / a.splits);
+      x.block0 = min(all, x.part * each);
+      x.blocks = min(each, all - x.block0);
+    }
     return x;
   }
 
   __device__ __forceinline__ int contraction() const {
     return kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
   }
-  __device__ __forceinline__ int blocks(const Item& x) const {
-    return x.n > 0 ? contraction() / kBlock : 0;
-  }
+  __device__ __forceinline__ int blocks(const Item& x) const { return x.blocks; }
   __device__ __forceinline__ bool two(const Item& x) const { return x.n > kHalf; }
 
   __device__ __forceinline__ void load(const Lane& l, const Item& x, A& la, B& lb) const {
-    const int H = a.r.H, I = a.r.I, K = contraction();
-    const uint32_t row_bytes = (uint32_t)K * 2;
+    const int H = a.r.H, I = a.r.I, K = contraction(), k0 = x.block0 * kBlock;
+    const uint32_t row_bytes = (uint32_t)K * 2, k0_bytes = (uint32_t)k0 * 2;
     if constexpr (kOp == kGateUp) {
       if (a.r.counts) {
-        lb.set(l, a.in, (uint32_t)a.r.tokens * row_bytes, [&](int j) -> uint32_t {
+        lb.set(l, a.in + k0, (uint32_t)a.r.tokens * row_bytes - k0_bytes, [&](int j) -> uint32_t {
           const int p = j < x.n ? a.r.sorted_ids[x.row0 + j] : -1;
           const uint32_t t = divided(a.div, (uint32_t)p & 0x7fffffffu);
           return p >= 0 && t < (uint64_t)a.r.tokens ? t * row_bytes : kOutside;
         });
       } else {
-        lb.set(l, a.in + (size_t)x.row0 * K, (uint32_t)x.n * row_bytes,
+        lb.set(l, a.in + (size_t)x.row0 * K + k0, (uint32_t)x.n * row_bytes - k0_bytes,
                [&](int j) -> uint32_t { return (uint32_t)j * row_bytes; });
       }
     } else {
-      lb.set(l, a.in + (size_t)x.row0 * K, (uint32_t)x.n * row_bytes, kHalf * row_bytes,
-             [&](int j) -> uint32_t { return (uint32_t)j * row_bytes; });
+      lb.set(l, a.in + (size_t)x.row0 * K + k0, (uint32_t)x.n * row_bytes - k0_bytes,
+             kHalf * row_bytes, [&](int j) -> uint32_t { return (uint32_t)j * row_bytes; });
     }
     if constexpr (kAAcross) {
       const int F = kOp == kDAct ? I : H;
-      la.set(l, a.w + (size_t)x.e * K * F, (uint32_t)F * 2, K, x.f0);
+      la.set(l, a.w + ((size_t)x.e * K + k0) * F, (uint32_t)F * 2, K - k0, x.f0);
     } else {
       const size_t mat = (kOp == kGateUp ? (size_t)2 : (size_t)1) * I * H;
-      const size_t before = (size_t)x.f0 * K;
+      const size_t before = (size_t)x.f0 * K + k0;
       // of a half's four MFMA tiles (gate/up) two are gate's and two up's, of the same 32 columns
       la.set(l, a.w + (size_t)x.e * mat + before, (uint32_t)((mat - before) * 2),
              kFeatures / 2 * row_bytes, [&](int r) -> uint32_t {
@@ -868,6 +918,15 @@ struct RowsJob {
   __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN]) const {
     const int H = a.r.H, I = a.r.I;
     if (x.n == 0) return;
+    if constexpr (kSplit) {
+      const int F = kOp == kGateUp ? 2 * I : kOp == kDAct ? I : H;
+      float* part = a.part + ((size_t)x.part * a.r.rows + x.row0) * F + x.f0;
+      if constexpr (kOp == kGateUp)
+        store_gate_up(l, acc, part, I, x.n, I - x.f0);
+      else
+        store_tile(l, acc, part, F, x.n, F - x.f0);
+      return;
+    }
     if constexpr (kOp == kDown || kOp == kDX) {
       store_tile(l, acc, a.out + (size_t)x.row0 * H + x.f0, H, x.n, H - x.f0);
       return;
@@ -918,13 +977,7 @@ struct RowsJob {
           in_order(l.g, acc[2 * p][tn], acc[2 * p + 1][tn], v);
           kept.values(gr[p], gv);
           kept.values(ur[p], uv);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float s = sigmoid(gv[q]), gs = gv[q] * s;
-            av[q] = gs * uv[q];
-            dg[q] = v[q] * uv[q] * (s * (1.0f + gv[q] * (1.0f - s)));
-            du[q] = v[q] * gs;
-          }
+          gradients(v, gv, uv, av, dg, du);
           const uint32_t d = (uint32_t)(64 * tn) * act.row_bytes;
           store16(act.rsrc(there), act.off + 2 * add + d, bf16x8_of(av));
           store16(dh.rsrc(there), dh.off + 2 * add + 2 * d, bf16x8_of(dg));
@@ -935,12 +988,12 @@ struct RowsJob {
   }
 };
 
-template <Op kOp, bool kFp8>
+template <Op kOp, bool kFp8, bool kSplit>
 __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
   TRAIN_UNITS;
   __shared__ Smem sm;
   const Lane l(threadIdx.x);
-  RowsJob<kOp, kFp8> job(a, l, sm);
+  RowsJob<kOp, kFp8, kSplit> job(a, l, sm);
   stream(l, job, units);
 }
 
@@ -960,7 +1013,9 @@ struct WeightArgs {
     const uint16_t* n_rows;
     void* out;
     int M, N;
+    int64_t part;   // values of the result; splits > 1: out is [splits][that]
   } p[2];   // M 0: none
+  int splits;
 };
 
 template <class TOut>
@@ -974,7 +1029,7 @@ struct WeightsJob {
   int each0, each1, run0, run, hi, start, step, xcd;
 
   struct Item {
-    int e, k, m0, n0, n;   // k: the product
+    int e, k, m0, n0, n, part;   // k: the product
     int64_t row0;
   };
 
@@ -996,8 +1051,9 @@ struct WeightsJob {
       m.pre[rank] = l.tid;
     }
     __syncthreads();
-    each0 = tiles(a.p[0].M) * tiles(a.p[0].N);
-    each1 = tiles(a.p[1].M) * tiles(a.p[1].N);
+    // the parts of a tile's contraction are tiles of their own
+    each0 = tiles(a.p[0].M) * tiles(a.p[0].N) * a.splits;
+    each1 = tiles(a.p[1].M) * tiles(a.p[1].N) * a.splits;
     if (E * (int64_t)(each0 + each1) <= (int64_t)gridDim.x) {   // an item a workgroup
       run0 = each0;
       run = each0 + each1;
@@ -1036,6 +1092,12 @@ struct WeightsJob {
     Item x;
     int at;
     tile_of(it, &x.e, &x.k, &at);
+    x.part = 0;
+    if (a.splits > 1) {
+      const int tile = uniform(at / a.splits);
+      x.part = at - tile * a.splits;
+      at = tile;
+    }
     const int tm_n = tiles(a.p[x.k].M), tn_n = tiles(a.p[x.k].N);
     // tiles in bands of 4 along N, so that those at work together share their operands
     const int band = uniform(at / (4 * tm_n)), in_band = at - band * 4 * tm_n;
@@ -1045,6 +1107,13 @@ struct WeightsJob {
     x.n0 = (4 * band + in_band - tm * width) * kTile;
     x.n = uniform(sm.rows[x.e]);
     x.row0 = uniform(sm.first[x.e]);
+    if (a.splits > 1) {   // whole blocks of rows
+      const int blocks = (x.n + kBlock - 1) / kBlock;
+      const int rows = uniform((blocks + a.splits - 1) / a.splits) * kBlock;
+      const int before = min(x.n, x.part * rows);
+      x.row0 += before;
+      x.n = min(rows, x.n - before);
+    }
     return x;
   }
   __device__ __forceinline__ int blocks(const Item& x) const {
@@ -1058,7 +1127,8 @@ struct WeightsJob {
   }
   __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN]) const {
     const WeightArgs::Product& p = a.p[x.k];
-    store_tile(l, acc, static_cast<TOut*>(p.out) + ((size_t)x.e * p.N + x.n0) * p.M + x.m0, p.M,
+    store_tile(l, acc, static_cast<TOut*>(p.out) + (size_t)x.part * p.part +
+                           ((size_t)x.e * p.N + x.n0) * p.M + x.m0, p.M,
                min(kTile, p.N - x.n0), p.M - x.m0);
   }
 };
@@ -1070,6 +1140,99 @@ __global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
   const Lane l(threadIdx.x);
   WeightsJob<TOut> job(a, l, sm);
   stream(l, job, units);
+}
+
+// ------------------------------------------------------------------ adding partial sums
+//
+// Where a launch has few items, parts of their contraction run on the other compute units, and
+// their sums are added here in the order of the parts: bound by those sums' bytes, at most
+// kPartBytes.  A lane has 8 neighbours of a row that holds a pair, as the products' epilogues do.
+constexpr int kFinishThreads = 256;
+
+__device__ __forceinline__ void add_parts(const float* p, int64_t stride, int parts, float* v) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+  for (int s = 0; s < parts; ++s) {
+    const f32x4 a = reinterpret_cast<const f32x4*>(p + s * stride)[0];
+    const f32x4 b = reinterpret_cast<const f32x4*>(p + s * stride)[1];
+    v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+    v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+  }
+}
+
+template <Op kOp, bool kFp8>
+__global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(Args a) {
+  const int H = a.r.H, I = a.r.I;
+  const int width = kOp == kGateUp || kOp == kDAct ? I : H, groups = width / 8;
+  const int64_t at = (int64_t)blockIdx.x * kFinishThreads + threadIdx.x;
+  const int64_t row = at / groups;
+  if (row >= a.r.rows) return;
+  const int c = (int)(at - row * groups) * 8;   // 4 lanes share a block of 32, and a row
+  if (a.r.counts) {
+    const int p = a.r.sorted_ids[row];
+    if (p < 0 || p >= a.r.tokens * a.r.K) return;
+  }
+  const int F = kOp == kGateUp ? 2 * I : width;
+  const int64_t stride = a.r.rows * F;
+  float v[8];
+  add_parts(a.part + row * F + c, stride, a.splits, v);
+  if constexpr (kOp == kGateUp) {
+    float u[8], av[8];
+    add_parts(a.part + row * F + I + c, stride, a.splits, u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) av[q] = silu(v[q]) * u[q];
+    *reinterpret_cast<u32x4*>(a.act + row * I + c) = bf16x8_of(av);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float* w = k ? u : v;
+      const int64_t to = row * 2 * I + (k ? I : 0) + c;
+      if constexpr (kFp8) {
+        float most = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) most = abs_max(most, w[q]);
+        const int byte = scale_byte(quad_max(most));
+        *reinterpret_cast<uint2*>(reinterpret_cast<uint8_t*>(a.h) + to) =
+            pack_e4m3x8(w, inverse_scale(byte));
+        if ((c & 31) == 0) a.scales[to / 32] = (uint8_t)byte;
+      } else {
+        *reinterpret_cast<u32x4*>(a.h + to) = bf16x8_of(w);
+      }
+    }
+  } else if constexpr (kOp == kDAct) {
+    float kept[2][8], av[8], dg[8], du[8];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int64_t from = row * 2 * I + (k ? I : 0) + c;
+      if constexpr (kFp8)
+        unpack_e4m3x8(*reinterpret_cast<const uint2*>(reinterpret_cast<const uint8_t*>(a.h) + from),
+                      scale_of(a.scales[from / 32]), kept[k]);
+      else
+        bf16x8_to(*reinterpret_cast<const u32x4*>(a.h + from), kept[k]);
+    }
+    gradients(v, kept[0], kept[1], av, dg, du);
+    *reinterpret_cast<u32x4*>(a.act + row * I + c) = bf16x8_of(av);
+    *reinterpret_cast<u32x4*>(a.dh + row * 2 * I + c) = bf16x8_of(dg);
+    *reinterpret_cast<u32x4*>(a.dh + row * 2 * I + I + c) = bf16x8_of(du);
+  } else {
+    *reinterpret_cast<u32x4*>(a.out + row * H + c) = bf16x8_of(v);
+  }
+}
+
+// values: a multiple of 8
+template <class TOut>
+__global__ __launch_bounds__(kFinishThreads) void finish_weights_kernel(const float* part,
+                                                                        int64_t values, int parts,
+                                                                        TOut* out) {
+  const int64_t at = ((int64_t)blockIdx.x * kFinishThreads + threadIdx.x) * 8;
+  if (at >= values) return;
+  float v[8];
+  add_parts(part + at, values, parts, v);
+  if constexpr (sizeof(TOut) == 2) {
+    *reinterpret_cast<u32x4*>(out + at) = bf16x8_of(v);
+  } else {
+    reinterpret_cast<f32x4*>(out + at)[0] = f32x4{v[0], v[1], v[2], v[3]};
+    reinterpret_cast<f32x4*>(out + at)[1] = f32x4{v[4], v[5], v[6], v[7]};
+  }
 }
 
 // compute units of the device current at the first call, as a multiple of the 8 XCDs
@@ -1097,17 +1260,48 @@ Divider divider(int K) {
   return d;
 }
 
+// Parts of the contraction of a launch of `items` items (at most) of `blocks` blocks, whose sums
+// are `values` in all: as many as fill the compute units, of 8 blocks or more each, where the
+// items would leave three quarters of them idle, and as `room` bytes hold.
+// (DeepSeek-V3-sized weights and one token, or a small dense FFN: a handful of items whose
+// contraction is all of the time.)
+int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room) {
+  if (items < 1 || 4 * items > workgroups() || values < 1) return 1;
+  int64_t n = workgroups() / items;
+  if (n > kMaxParts) n = kMaxParts;
+  if (n > blocks / 8) n = blocks / 8;
+  if (n > room / (4 * values)) n = room / (4 * values);
+  return n < 2 ? 1 : (int)n;
+}
+
 template <Op kOp, bool kFp8>
-hipError_t launch_rows(const Args& a, hipStream_t s) {
+hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
   const int per_tile = kOp == kGateUp ? kTile / 2 : kTile;
   const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
-  // spans: one for each 256 rows, and a short one an expert; twice, as items may be cut in two
+  const int K = kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
+  // spans: one for each 256 rows, and a short one an expert
   const int64_t pairs = a.r.counts ? a.r.tokens * a.r.K : a.r.tokens;
   const int64_t spans = pairs / kTile + (a.r.counts ? (a.r.E < pairs ? a.r.E : pairs) : 1);
   const int64_t items = spans * ((F + per_tile - 1) / per_tile);
   if (pairs == 0) return hipSuccess;
-  if (items >= (int64_t)1 << 31) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((rows_kernel<kOp, kFp8>), dim3(grid_of(2 * items)), dim3(kThreads), 0, s, a);
+  if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
+  const int64_t values = a.r.rows * (kOp == kGateUp ? 2 * (int64_t)F : F);
+  a.part = space.part;
+  a.splits = parts_of(items, K / kBlock, values, space.bytes);
+  if (a.splits == 1) {
+    // twice the items, as they may be cut in two
+    hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(grid_of(2 * items)), dim3(kThreads), 0,
+                       s, a);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL((rows_kernel<kOp, false, true>), dim3(grid_of(items * a.splits)),
+                     dim3(kThreads), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t lanes = a.r.rows * (F / 8);
+  hipLaunchKernelGGL((finish_rows_kernel<kOp, kFp8>),
+                     dim3((unsigned)((lanes + kFinishThreads - 1) / kFinishThreads)),
+                     dim3(kFinishThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -1121,27 +1315,29 @@ Args args_of(const TrainRows& r) {
 }  // namespace
 
 hipError_t launch_train_gate_up(const TrainRows& r, const void* x, const void* w13,
-                                const SavedRows& saved, uint16_t* act, hipStream_t s) {
+                                const SavedRows& saved, uint16_t* act, const PartSpace& space,
+                                hipStream_t s) {
   Args a = args_of(r);
   a.w = static_cast<const uint16_t*>(w13);
   a.in = static_cast<const uint16_t*>(x);
   a.act = act;
   a.h = static_cast<uint16_t*>(saved.h);
   a.scales = saved.scales;
-  return saved.fp8 ? launch_rows<kGateUp, true>(a, s) : launch_rows<kGateUp, false>(a, s);
+  return saved.fp8 ? launch_rows<kGateUp, true>(a, space, s) : launch_rows<kGateUp, false>(a, space, s);
 }
 
 hipError_t launch_train_down(const TrainRows& r, const void* w2, const uint16_t* act, void* y,
-                             hipStream_t s) {
+                             const PartSpace& space, hipStream_t s) {
   Args a = args_of(r);
   a.w = static_cast<const uint16_t*>(w2);
   a.in = act;
   a.out = static_cast<uint16_t*>(y);
-  return launch_rows<kDown, false>(a, s);
+  return launch_rows<kDown, false>(a, space, s);
 }
 
 hipError_t launch_train_dact(const TrainRows& r, const void* w2, const void* dy,
-                             const SavedRows& saved, uint16_t* act, uint16_t* dh, hipStream_t s) {
+                             const SavedRows& saved, uint16_t* act, uint16_t* dh,
+                             const PartSpace& space, hipStream_t s) {
   Args a = args_of(r);
   a.w = static_cast<const uint16_t*>(w2);
   a.in = static_cast<const uint16_t*>(dy);
@@ -1149,34 +1345,58 @@ hipError_t launch_train_dact(const TrainRows& r, const void* w2, const void* dy,
   a.dh = dh;
   a.h = static_cast<uint16_t*>(saved.h);
   a.scales = saved.scales;
-  return saved.fp8 ? launch_rows<kDAct, true>(a, s) : launch_rows<kDAct, false>(a, s);
+  return saved.fp8 ? launch_rows<kDAct, true>(a, space, s) : launch_rows<kDAct, false>(a, space, s);
 }
 
 hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
-                           hipStream_t s) {
+                           const PartSpace& space, hipStream_t s) {
   Args a = args_of(r);
   a.w = static_cast<const uint16_t*>(w13);
   a.in = dh;
   a.out = static_cast<uint16_t*>(dx);
-  return launch_rows<kDX, false>(a, s);
+  return launch_rows<kDX, false>(a, space, s);
 }
 
 hipError_t launch_train_dw(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
                            void* dw13, const uint16_t* act, const void* dy, void* dw2, bool f32,
-                           hipStream_t s) {
-  const WeightArgs a{r,
-                     {{x_rows, dh, dw13, dw13 ? r.H : 0, 2 * r.I},
-                      {act, static_cast<const uint16_t*>(dy), dw2, dw2 ? r.I : 0, r.H}}};
+                           const PartSpace& space, hipStream_t s) {
+  const int64_t matrices = r.counts ? r.E : 1;
+  const int64_t n13 = dw13 ? matrices * 2 * r.I * r.H : 0, n2 = dw2 ? matrices * r.H * r.I : 0;
+  WeightArgs a{r,
+               {{x_rows, dh, dw13, dw13 ? r.H : 0, 2 * r.I, n13},
+                {act, static_cast<const uint16_t*>(dy), dw2, dw2 ? r.I : 0, r.H, n2}},
+               1};
   int64_t items = 0;
   for (const WeightArgs::Product& p : a.p)
-    items += (int64_t)((p.M + kTile - 1) / kTile) * ((p.N + kTile - 1) / kTile);
-  if (r.counts) items *= r.E;
+    items += matrices * ((p.M + kTile - 1) / kTile) * ((p.N + kTile - 1) / kTile);
   if (items == 0) return hipSuccess;
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
-  const dim3 grid(grid_of(items)), block(kThreads);
-  if (f32) hipLaunchKernelGGL(weights_kernel<float>, grid, block, 0, s, a);
+  // the most rows an expert may have
+  const int64_t rows = r.tokens < r.rows ? r.tokens : r.rows;
+  a.splits = parts_of(items, rows / kBlock, n13 + n2, space.bytes);
+  if (a.splits > 1) {
+    a.p[0].out = space.part;
+    a.p[1].out = space.part + a.splits * n13;
+  }
+  const dim3 grid(grid_of(items * a.splits)), block(kThreads);
+  if (f32 || a.splits > 1) hipLaunchKernelGGL(weights_kernel<float>, grid, block, 0, s, a);
   else hipLaunchKernelGGL(weights_kernel<uint16_t>, grid, block, 0, s, a);
-  return hipGetLastError();
+  hipError_t e = hipGetLastError();
+  void* const outs[2] = {dw13, dw2};
+  for (int k = 0; k < 2 && a.splits > 1 && e == hipSuccess; ++k) {
+    const int64_t n = a.p[k].part;
+    if (n == 0) continue;
+    const dim3 g((unsigned)((n / 8 + kFinishThreads - 1) / kFinishThreads)), b(kFinishThreads);
+    const float* part = static_cast<const float*>(a.p[k].out);
+    if (f32)
+      hipLaunchKernelGGL(finish_weights_kernel<float>, g, b, 0, s, part, n, a.splits,
+                         static_cast<float*>(outs[k]));
+    else
+      hipLaunchKernelGGL(finish_weights_kernel<uint16_t>, g, b, 0, s, part, n, a.splits,
+                         static_cast<uint16_t*>(outs[k]));
+    e = hipGetLastError();
+  }
+  return e;
 }
 
 }  // namespace moe

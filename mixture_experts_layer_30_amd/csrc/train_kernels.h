@@ -27,23 +27,34 @@ struct SavedRows {
   bool fp8;
 };
 
+// Room for partial sums: launches of few items split their contraction into parts whose sums are
+// added by a second kernel, as far as the room goes.
+struct PartSpace {
+  float* part;
+  int64_t bytes;
+};
+constexpr int kMaxParts = 16;
+constexpr int64_t kPartBytes = (int64_t)64 << 20;   // no more is needed: see parts_of
+
 // act [rows][I] = silu(g) * u with g, u = w13 x; g and u kept
 hipError_t launch_train_gate_up(const TrainRows& r, const void* x, const void* w13,
-                                const SavedRows& saved, uint16_t* act, hipStream_t s);
+                                const SavedRows& saved, uint16_t* act, const PartSpace& space,
+                                hipStream_t s);
 // y [rows][H] = w2 act
 hipError_t launch_train_down(const TrainRows& r, const void* w2, const uint16_t* act, void* y,
-                             hipStream_t s);
+                             const PartSpace& space, hipStream_t s);
 // from da = w2^T dy: act = silu(g) * u, and dh [rows][2I], the gradients of g and of u
 hipError_t launch_train_dact(const TrainRows& r, const void* w2, const void* dy,
-                             const SavedRows& saved, uint16_t* act, uint16_t* dh, hipStream_t s);
+                             const SavedRows& saved, uint16_t* act, uint16_t* dh,
+                             const PartSpace& space, hipStream_t s);
 // dx [rows][H] = w13^T dh
 hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
-                           hipStream_t s);
+                           const PartSpace& space, hipStream_t s);
 // dw13 [E][2I][H] = sum over an expert's rows of dh x^T (x_rows: x by row), and dw2 [E][H][I] that
 // of dy act^T; either null: not wanted; f32: their type is fp32, else bf16
 hipError_t launch_train_dw(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
                            void* dw13, const uint16_t* act, const void* dy, void* dw2, bool f32,
-                           hipStream_t s);
+                           const PartSpace& space, hipStream_t s);
 
 // [T][H] values in blocks of 32 to e4m3 codes and the biased exponents of the blocks' scales
 hipError_t launch_pack_fp8(const void* x, int dt, int64_t T, int H, uint8_t* codes,

@@ -746,32 +746,47 @@ __device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int* row0)
   return (int)(n < 0 ? 0 : n < r.rows - off ? n : r.rows - off);
 }
 
-// exclusive sums of u over the threads, in pre[0 ..]; the number of threads >= that of values
-__device__ __forceinline__ void prefix(const Lane& l, int u, int values, int* pre, int* wsum) {
-  int incl = u;
+// exclusive sums of u and of v over the threads, in pre_u[0 ..] and pre_v[0 ..], `values` of them
+__device__ __forceinline__ void prefix(const Lane& l, int u, int v, int values, int* pre_u,
+                                       int* pre_v, int (*wsum)[kWaves]) {
+  int su = u, sv = v;
 #pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {
-    const int v = __shfl_up(incl, d, kWave);
-    if (l.lane >= d) incl += v;
+  for (int d = 1; d < kWave; d <<= 1) {   // both side by side: each step is a trip through LDS
+    const int a = __shfl_up(su, d, kWave), b = __shfl_up(sv, d, kWave);
+    if (l.lane >= d) {
+      su += a;
+      sv += b;
+    }
   }
-  if (l.lane == kWave - 1) wsum[l.wave] = incl;
+  if (l.lane == kWave - 1) {
+    wsum[0][l.wave] = su;
+    wsum[1][l.wave] = sv;
+  }
   __syncthreads();
-  int before = 0;
 #pragma unroll
-  for (int v = 0; v < kWaves; ++v) before += v < l.wave ? wsum[v] : 0;
-  if (l.tid < values) pre[l.tid + 1] = before + incl;
-  if (l.tid == 0) pre[0] = 0;
+  for (int w = 0; w < kWaves; ++w)
+    if (w < l.wave) {
+      su += wsum[0][w];
+      sv += wsum[1][w];
+    }
+  if (l.tid < values) {
+    pre_u[l.tid + 1] = su;
+    pre_v[l.tid + 1] = sv;
+  }
+  if (l.tid == 0) pre_u[0] = pre_v[0] = 0;
+  __syncthreads();
 }
 
-// the last of n with pre[i] <= at
+// the last i < n with pre[i] <= at (pre[0] is): a lane looks at four of them, all at once
 __device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
-  int lo = 0, up = n;
-  while (up - lo > 1) {
-    const int mid = (lo + up) >> 1;
-    if (uniform(pre[mid]) <= at) lo = mid;
-    else up = mid;
+  const int lane = threadIdx.x & (kWave - 1);
+  int below = 0;
+#pragma unroll
+  for (int k = 0; k < kMaxE / kWave; ++k) {
+    const int i = lane + k * kWave;
+    below += __popcll(__ballot(i < n && pre[i] <= at));
   }
-  return lo;
+  return below - 1;
 }
 
 // One of the products over rows.  Items: (expert, feature tile, span of up to 256 rows), spans
@@ -811,9 +826,8 @@ struct RowsJob {
       m.first[l.tid] = row0;
       m.rows[l.tid] = n;
     }
-    prefix(l, n > kHalf ? ntiles * spans(n) : 0, nexp, m.pre, m.wsum[0]);
-    prefix(l, n > 0 && n <= kHalf ? ntiles : 0, nexp, m.pre_light, m.wsum[1]);
-    __syncthreads();
+    prefix(l, n > kHalf ? ntiles * spans(n) : 0, n > 0 && n <= kHalf ? ntiles : 0, nexp, m.pre,
+           m.pre_light, m.wsum);
     const int all = uniform(m.pre[nexp]), lights = uniform(m.pre_light[nexp]);
     step = (int)gridDim.x / 8;
     xcd = (int)blockIdx.x % 8;
@@ -847,7 +861,7 @@ struct RowsJob {
     if (it < full + 2 * cut) {
       const int half = it < full ? 0 : (it - full) & 1;
       const int q = full0 + (it < full ? it : full + ((it - full) >> 1));
-      x.e = last_at_most(sm.pre, nexp, q);
+      x.e = uniform(last_at_most(sm.pre, nexp, q));
       const int n = uniform(sm.rows[x.e]), each = spans(n);
       const int at = q - uniform(sm.pre[x.e]);
       tile = uniform(at / each);
@@ -855,7 +869,7 @@ struct RowsJob {
       x.n = max(0, min(it < full ? kTile : kHalf, n - skip));
     } else {
       const int q = light0 + it - full - 2 * cut;
-      x.e = last_at_most(sm.pre_light, nexp, q);
+      x.e = uniform(last_at_most(sm.pre_light, nexp, q));
       const int n = uniform(sm.rows[x.e]);
       tile = q - uniform(sm.pre_light[x.e]);
       x.n = n;
@@ -1047,6 +1061,7 @@ struct WeightsJob {
     __syncthreads();
     if (l.tid < E) {
       int rank = 0;
+#pragma unroll 8
       for (int e = 0; e < E; ++e) rank += m.rows[e] > n || (m.rows[e] == n && e < l.tid);
       m.pre[rank] = l.tid;
     }

@@ -515,7 +515,8 @@ moe_status moe_norm_residual_backward(const void *dr, moe_dtype xdt, const void 
  * products; sums are fp32.  dw13 [E][2I][H] and dw2 [E][H][I] (dense: without E) are
  * of type dwdt, overwritten; an expert without rows (or T = 0) gets zeros.  Each of
  * dxrows, dw13 and dw2 may be NULL, not all of them; x may be NULL where dw13 is, and
- * w13 where dxrows is.  dxrows may not be drows.  No atomics: the same on every run.
+ * w13 where dxrows is.  What is written may overlap nothing that is read (dxrows is
+ * refused where it is drows or x).  No atomics: the same on every run.
  * workspace: 16-byte aligned, with no contents to keep before or after the call; the
  * forward needs moe_ffn_train_workspace_bytes(rows, H, I) bytes, the gradients
  * moe_ffn_backward_workspace_bytes(rows, H, I); calls that may overlap need one each.

@@ -109,7 +109,8 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
     if (!good(dy, 16) || !good(w2, 16) || (dx ? !good(w13, 16) : !optional(w13, 16)) ||
         (dw13 ? !good(x, 16) : !optional(x, 16)))
       return null_pointer(what);
-    if (dx && dx == dy) return fail(MOE_EINVAL, "%s: the rows' gradient overwrites its input", what);
+    if (dx && (dx == dy || dx == x))   // both are read again after dx is written
+      return fail(MOE_EINVAL, "%s: the rows' gradient overwrites its input", what);
   }
   uint16_t* act = static_cast<uint16_t*>(workspace);
   uint16_t* dh = act + rounded(r.rows * r.I * 2) / 2;

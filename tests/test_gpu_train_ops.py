@@ -107,6 +107,15 @@ CASES = [
     (700, 576, 704, 3, 2, 1000, B.PAD_BLOCK, False, True, B.SAVE_FP8),
     (900, 256, 512, 4, 1, 128, B.PAD_MAX, False, True, B.SAVE_BF16),
     (1111, 448, 192, 5, 3, 1, B.PAD_BLOCK, True, False, B.SAVE_BF16),
+    # many tiles of every number of blocks, odd and even
+    (700, 1088, 448, 16, 4, 16, B.PAD_BLOCK, False, False, B.SAVE_FP8),
+    # the last spans of a run in two halves
+    (1500, 320, 1088, 2, 2, 128, B.PAD_BLOCK, False, False, B.SAVE_BF16),
+    # few rows of wide experts: the contraction in parts
+    (2, 4096, 1024, 8, 2, 1, B.PAD_BLOCK, False, False, B.SAVE_BF16),
+    (5, 1024, 2048, 3, 1, 64, B.PAD_MAX, False, False, B.SAVE_FP8),
+    # the weights' gradients in parts
+    (2100, 128, 192, 1, 1, 16, B.PAD_BLOCK, False, False, B.SAVE_FP8),
 ]
 
 
@@ -338,6 +347,72 @@ def test_same_on_every_run_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         same(first, graphed)
         same(first, again)
+
+
+def test_two_calls_at_once():
+    """Steps on two streams, with workspaces of their own, are what each gives alone."""
+    steps = []
+    for k, (T, H, I, E, K, fmt) in enumerate([(400, 576, 320, 7, 3, B.SAVE_FP8),
+                                              (900, 256, 448, 4, 2, B.SAVE_BF16)]):
+        _, _, plan = routed(T, E, K, 16, B.PAD_BLOCK, k)
+        g = gen(20 + k)
+        x, drows = randn(g, T, H), randn(g, plan.cap, H, std=0.1)
+        w13, w2 = weights(g, E, H, I)
+
+        def run(x=x, drows=drows, w13=w13, w2=w2, plan=plan, fmt=fmt):
+            s = B.Saved(plan.cap, w2.shape[2], fmt, DEV)
+            s.h.zero_()
+            out = [torch.zeros_like(drows), torch.zeros_like(drows), torch.empty_like(w13),
+                   torch.empty_like(w2)]
+            n = B.moe_ffn_backward_workspace_bytes(plan.cap, x.shape[1], w2.shape[2])
+            ws = space(n)
+
+            def go(stream=None):
+                B.moe_grouped_ffn_train(x, w13, w2, plan, s, ws, out[0], stream=stream)
+                B.moe_grouped_ffn_backward(drows, x, w13, w2, plan, s, ws, dxrows=out[1],
+                                           dw13=out[2], dw2=out[3], stream=stream)
+            return go, out
+
+        steps.append(run)
+    alone = []
+    for run in steps:
+        go, out = run()
+        go()
+        alone.append(out)
+    both = [run() for run in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for _ in range(3):
+        for (go, _), s in zip(both, streams):
+            go(s)
+    torch.cuda.synchronize()
+    for (_, out), want in zip(both, alone):
+        for a, b in zip(out, want):
+            assert torch.equal(a, b)
+
+
+def test_not_finite_values_kept_in_8_bits():
+    """Of a block of 32 kept values only those that are not finite lose their gradient."""
+    T, H, I = 70, 128, 64
+    g = gen(30)
+    saved, _ = given(T, I, B.SAVE_FP8, g)
+    saved.h[9, 5] = 127             # gate 5 of token 9 is NaN
+    saved.h[40, I + 33] = 255       # up 33 of token 40
+    x, dout = randn(g, T, H), randn(g, T, H)
+    w13, w2 = (w[0] for w in weights(g, 1, H, I))
+    dx, dw13, dw2 = torch.zeros_like(x), torch.zeros_like(w13), torch.zeros_like(w2)
+    ws = space(B.moe_ffn_backward_workspace_bytes(T, H, I))
+    B.dense_ffn_backward(dout, x, w13, w2, saved, ws, dx=dx, dw13=dw13, dw2=dw2)
+    bad = torch.zeros(T, dtype=torch.bool, device=DEV)
+    bad[[9, 40]] = True
+    assert bool(torch.isfinite(dx[~bad]).all()) and bool(torch.isnan(dx[bad]).all())
+    cols = torch.zeros(I, dtype=torch.bool, device=DEV)
+    cols[[5, 33]] = True
+    assert bool(torch.isfinite(dw2[:, ~cols]).all()) and bool(torch.isnan(dw2[:, cols]).all())
+    # the gradient of a gate with the up value NaN is NaN; that of the up value is not
+    rows = torch.zeros(2 * I, dtype=torch.bool, device=DEV)
+    rows[[5, I + 5, 33]] = True
+    assert bool(torch.isfinite(dw13[~rows]).all()) and bool(torch.isnan(dw13[rows]).all())
 
 
 @pytest.mark.parametrize("fmt", [B.SAVE_BF16, B.SAVE_FP8])

@@ -89,6 +89,7 @@ def test_grouped_backward(L):
         (INV, dict(drows=None)), (INV, dict(x=None)), (INV, dict(w13=None)), (INV, dict(w2=None)),
         (INV, dict(x=FAKE + 2, dw13=None)), (INV, dict(w13=FAKE + 2, dxrows=None)),
         (INV, dict(dxrows=None, dw13=None, dw2=None)), (INV, dict(dxrows=FAKE)),
+        (INV, dict(dxrows=3 * FAKE, x=3 * FAKE)),
         (INV, dict(dxrows=FAKE + 8)), (INV, dict(dw13=FAKE + 8)), (INV, dict(dw2=FAKE + 8)),
         (UNS, dict(dwdt=2)), (CAP, dict(bytes=n - 1))])
     assert call(L.moe_grouped_ffn_backward, good, T=0, drows=None, x=None, w13=None, w2=None,
@@ -106,7 +107,7 @@ def test_dense(L):
     good = dict(dout=FAKE, x=FAKE, T=T, H=H, I=I, w13=FAKE, w2=FAKE, saved=saved(), workspace=FAKE,
                 bytes=n, dx=2 * FAKE, dw13=FAKE, dw2=FAKE, dwdt=F32)
     expect(L.dense_ffn_backward, good, SIZES + [
-        (INV, dict(dout=None)), (INV, dict(dx=FAKE)), (INV, dict(dx=None, dw13=None, dw2=None)),
+        (INV, dict(dout=None)), (INV, dict(dx=FAKE)), (INV, dict(dx=3 * FAKE, x=3 * FAKE)), (INV, dict(dx=None, dw13=None, dw2=None)),
         (INV, dict(w2=None)), (INV, dict(x=None)), (UNS, dict(dwdt=-1))])
 
 

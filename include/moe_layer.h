@@ -520,7 +520,8 @@ moe_status moe_norm_residual_backward(const void *dr, moe_dtype xdt, const void 
  * workspace: 16-byte aligned, with no contents to keep before or after the call; the
  * forward needs moe_ffn_train_workspace_bytes(rows, H, I) bytes, the gradients
  * moe_ffn_backward_workspace_bytes(rows, H, I); calls that may overlap need one each.
- * Limits: H, I at most 2^20, an expert's w13 below 4 GB, and the grouped x below 4 GB.
+ * Limits: H and I multiples of 64 up to 2^20, an expert's w13 below 4 GB, T < 2^31 - 256,
+ * and the grouped x below 4 GB.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED, MOE_ECAPACITY (plan, workspace).
  */
 typedef enum { MOE_SAVE_BF16 = 0, MOE_SAVE_FP8 = 1 } moe_save_format;
@@ -557,7 +558,8 @@ moe_status dense_ffn_backward(const void *dout, const void *x, int64_t T, int H,
  * off by at most 2^-4 of |v| and 2^-10 s.  A value that is not finite is kept as NaN and
  * has no part in the maximum.  moe_unpack_fp8 gives code * s, rounded to the type asked
  * for (both hold it exactly but bf16 below 2^-133).
- * x [T][H] dt; codes [T][H]; scales [T][H/32].  Limits: H a multiple of 32, T*H < 2^39.
+ * x [T][H] dt; codes [T][H], not in place of x; scales [T][H/32].  Limits: H a multiple
+ * of 32, T*H < 2^39.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED.
  */
 moe_status moe_pack_fp8(const void *x, moe_dtype dt, int64_t T, int H, uint8_t *codes,

@@ -1,5 +1,5 @@
-// Checks of arguments, their messages and the plan as the kernels take it, shared by the C ABI of the operators around the
-// layer pass and of the training step.
+// Checks of arguments, their messages and the plan as the kernels take it, shared by the C ABI of
+// the operators around the layer pass and of the training step.
 #pragma once
 
 #include <math.h>

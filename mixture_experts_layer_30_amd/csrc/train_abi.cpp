@@ -14,7 +14,8 @@ constexpr int kMaxWidth = 1 << 20;   // of H and I: a span's rows are counted in
 // the FFN's sizes; every matrix of an expert is read through 32-bit offsets
 moe_status check_ffn(const char* what, int64_t T, int H, int I) {
   if (T < 0) return fail(MOE_EINVAL, "%s: T = %lld < 0", what, (long long)T);
-  if (T >= (int64_t)1 << 31) return fail(MOE_EUNSUPPORTED, "%s: T must be < 2^31", what);
+  if (T >= ((int64_t)1 << 31) - 256)   // rows up to a tile's end are counted in 32 bits
+    return fail(MOE_EUNSUPPORTED, "%s: T must be < 2^31 - 256", what);
   if (H < 64 || H % 64 != 0 || H > kMaxWidth || I < 64 || I % 64 != 0 || I > kMaxWidth)
     return fail(MOE_EUNSUPPORTED, "%s: H = %d and I = %d must be multiples of 64 up to 2^20", what,
                 H, I);
@@ -209,6 +210,7 @@ moe_status moe_pack_fp8(const void* x, moe_dtype dt, int64_t T, int H, uint8_t* 
   if (st) return st;
   if (T == 0) return ok();
   if (!good(x, 16) || !good(codes, 16) || !scales) return null_pointer(what);
+  if (codes == x) return fail(MOE_EINVAL, "%s: the codes overwrite x", what);
   return hip_status(moe::launch_pack_fp8(x, dt, T, H, codes, scales, (hipStream_t)stream), what);
 }
 
@@ -219,6 +221,7 @@ moe_status moe_unpack_fp8(const uint8_t* codes, const uint8_t* scales, int64_t T
   if (st) return st;
   if (T == 0) return ok();
   if (!good(codes, 16) || !scales || !good(x, 16)) return null_pointer(what);
+  if (codes == x) return fail(MOE_EINVAL, "%s: x overwrites the codes", what);
   return hip_status(moe::launch_unpack_fp8(codes, scales, T, H, x, dt, (hipStream_t)stream), what);
 }
 

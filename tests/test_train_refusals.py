@@ -42,7 +42,7 @@ def expect(fn, good, table):
         assert fn.__name__.encode() in B.lib().moe_last_error(), bad
 
 
-SIZES = [(INV, dict(T=-1)), (UNS, dict(T=1 << 31)), (UNS, dict(H=0)), (UNS, dict(H=200)),
+SIZES = [(INV, dict(T=-1)), (UNS, dict(T=1 << 31)), (UNS, dict(T=(1 << 31) - 256)), (UNS, dict(H=0)), (UNS, dict(H=200)),
          (UNS, dict(I=0)), (UNS, dict(I=100)), (UNS, dict(H=(1 << 20) + 64)), (UNS, dict(I=1 << 21)),
          (UNS, dict(H=1 << 15, I=1 << 15)), (INV, dict(saved=None)), (INV, dict(saved=saved(2))),
          (INV, dict(saved=saved(h=None))), (INV, dict(saved=saved(h=FAKE + 8))),
@@ -112,13 +112,14 @@ def test_dense(L):
 
 
 def test_pack(L):
-    good = dict(x=FAKE, dt=BF, T=T, H=H, codes=FAKE, scales=FAKE)
+    good = dict(x=FAKE, dt=BF, T=T, H=H, codes=2 * FAKE, scales=FAKE)
     table = [(INV, dict(T=-1)), (UNS, dict(T=1 << 31)), (UNS, dict(H=40)), (UNS, dict(H=0)),
              (UNS, dict(dt=2)), (INV, dict(x=None)), (INV, dict(x=FAKE + 8)),
-             (INV, dict(codes=None)), (INV, dict(codes=FAKE + 8)), (INV, dict(scales=None))]
+             (INV, dict(codes=None)), (INV, dict(codes=FAKE + 8)), (INV, dict(scales=None)),
+             (INV, dict(codes=3 * FAKE, x=3 * FAKE))]
     expect(L.moe_pack_fp8, good, table)
     assert call(L.moe_pack_fp8, good, T=0, x=None, codes=None, scales=None) == B.MOE_OK
-    good = dict(codes=FAKE, scales=FAKE, T=T, H=H, x=FAKE, dt=F32)
+    good = dict(codes=FAKE, scales=FAKE, T=T, H=H, x=2 * FAKE, dt=F32)
     expect(L.moe_unpack_fp8, good, table)
 
 

@@ -516,7 +516,7 @@ moe_status moe_norm_residual_backward(const void *dr, moe_dtype xdt, const void 
  * of type dwdt, overwritten; an expert without rows (or T = 0) gets zeros.  Each of
  * dxrows, dw13 and dw2 may be NULL, not all of them; x may be NULL where dw13 is, and
  * w13 where dxrows is.  What is written may overlap nothing that is read (dxrows is
- * refused where it is drows or x).  No atomics: the same on every run.
+ * refused where it is drows or x).  Sums are in a fixed order: the same on every run.
  * workspace: 16-byte aligned, with no contents to keep before or after the call; the
  * forward needs moe_ffn_train_workspace_bytes(rows, H, I) bytes, the gradients
  * moe_ffn_backward_workspace_bytes(rows, H, I); calls that may overlap need one each.

@@ -120,8 +120,8 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
                              part_bytes(r.rows, r.H, r.I)};
   const hipStream_t s = (hipStream_t)stream;
   hipError_t e = hipSuccess;
-  if (r.tokens > 0) e = moe::launch_train_dact(r, w2, dy, saved, act, dh, space, s);
-  if (e == hipSuccess && dx && r.tokens > 0) e = moe::launch_train_dx(r, w13, dh, dx, space, s);
+  int* counters = (int*)((char*)space.part + rounded(space.bytes));
+  if (r.tokens > 0) e = moe::launch_train_dact(r, w2, dy, saved, act, dh, counters, space, s);
   const uint16_t* xr = static_cast<const uint16_t*>(x);
   if (e == hipSuccess && dw13 && plan && r.tokens > 0) {
     // x by row: the contraction over rows then reads whole lines in order (gathering in it
@@ -130,8 +130,9 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
                             x_rows, s);
     xr = x_rows;
   }
-  if (e == hipSuccess && (dw13 || dw2))
-    e = moe::launch_train_dw(r, xr, dh, dw13, act, dy, dw2, dwdt == MOE_F32, space, s);
+  if (e == hipSuccess)
+    e = moe::launch_train_grads(r, w13, dh, dx, xr, dw13, act, dy, dw2, dwdt == MOE_F32, space,
+                                counters, s);
   return hip_status(e, what);
 }
 
@@ -157,7 +158,9 @@ int64_t moe_ffn_train_workspace_bytes(int64_t rows, int H, int I) {
 int64_t moe_ffn_backward_workspace_bytes(int64_t rows, int H, int I) {
   const int64_t act = moe_ffn_train_workspace_bytes(rows, H, I);   // a, and partial sums
   // dh of every row, and x by row
-  return act < 0 ? -1 : act + rounded(rows * I * 4) + rounded(rows * H * 2);
+  return act < 0 ? -1
+                 : rounded(act) + rounded(rows * I * 4) + rounded(rows * H * 2) +
+                       (rows > 0 ? moe::kCounterBytes : 0);
 }
 
 moe_status moe_grouped_ffn_train(const void* x, int64_t T, int H, int I, int E, int K,

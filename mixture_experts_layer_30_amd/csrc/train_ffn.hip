@@ -89,6 +89,7 @@ struct Smem {
   int first[kMaxE], rows[kMaxE];
   int pre[kMaxE + 1], pre_light[kMaxE + 1];
   int wsum[2][kWaves];
+  int claim[4];   // WeightsJob: its next items
 };
 
 enum Op { kGateUp, kDown, kDAct, kDX };
@@ -359,7 +360,8 @@ __device__ __forceinline__ void read_rows(const Lane& l, const uint8_t* unit, u3
 //
 // Job: kAAcross, kBAcross; first(), next(it), kEnd: the places of this workgroup's items;
 // item(it); and of an item blocks(); two(): whether the rows' second half holds any; load(a, b):
-// sets the loaders; store(acc).
+// sets the loaders; store(acc).  kEmptyLast: no item with blocks comes after one without; claim()
+// and claimed(): at the start and the end of an item (see WeightsJob).
 template <class Job>
 __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) {
   constexpr bool kAA = Job::kAAcross, kBA = Job::kBAcross;
@@ -390,6 +392,7 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
     blocks = job.blocks(x);
     even = (blocks + 1) & ~1;
     if (even > 0) job.load(l.again(), x, la, lb);
+    else if (Job::kEmptyLast) item = Job::kEnd;
   };
   enter();
   // may_end: an item may end here
@@ -523,6 +526,7 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
     const typename Job::Item x = job.item(it);
     const int n = job.blocks(x);
     const bool two = job.two(x);
+    const int later = job.claim(l);
     if (n == 0 || !two) {
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm)
@@ -537,6 +541,11 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
     }
     // what is in flight lands before the stores, so that an item's first phases wait for neither
     wait_vm<0>();
+    job.claimed(l, it, later);
+    if (Job::kEmptyLast && n == 0) {   // what is claimed is seen two items later
+      wait_lgkm0();
+      barrier();
+    }
     job.store(l.again(), x, acc);
     __builtin_amdgcn_sched_barrier(0);
   }
@@ -664,6 +673,7 @@ struct Args {
   uint8_t* scales;
   float* part;          // partial sums [splits][rows][features], where the contraction is split
   int splits;
+  int* counters;        // kDAct: of 8, cleared
 };
 
 // A row buffer from a span's first row on, of `cols` values a row, as a lane sees it: byte
@@ -819,6 +829,7 @@ __device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
 template <Op kOp, bool kFp8, bool kSplit>
 struct RowsJob {
   static constexpr bool kAAcross = kOp == kDAct || kOp == kDX, kBAcross = false;
+  static constexpr bool kEmptyLast = false;
   using A = typename std::conditional<kAAcross, Across, Along>::type;
   using B = typename std::conditional<kOp == kGateUp, Gathered, Along>::type;
   static constexpr int kEnd = -1;
@@ -905,6 +916,9 @@ struct RowsJob {
     }
     return x;
   }
+
+  __device__ __forceinline__ int claim(const Lane&) const { return 0; }
+  __device__ __forceinline__ void claimed(const Lane&, int, int) const {}
 
   __device__ __forceinline__ int contraction() const {
     return kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
@@ -1025,6 +1039,7 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
   TRAIN_UNITS;
   __shared__ Smem sm;
   const Lane l(threadIdx.x);
+  if (kOp == kDAct && blockIdx.x == 0 && l.tid < 8) a.counters[l.tid] = 0;   // see WeightsJob
   RowsJob<kOp, kFp8, kSplit> job(a, l, sm);
   stream(l, job, units);
 }
@@ -1033,10 +1048,10 @@ __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
 // result) and rows of N.  An item is one 256 x 256 tile of one expert's matrix, its
 // contraction the expert's rows; an expert without rows gets zeros.
 //
-// Experts come by falling numbers of rows, the tiles of each dealt to the 8 XCDs in runs of
-// equal length, so that skewed routing leaves no XCD with the busy experts and the short
-// items fill in at the end (contiguous experts per XCD: Qwen2-shaped dW13 of 3001 tokens with
-// skewed routing 2.4 ms).
+// Experts come by falling numbers of rows, those without any last, the tiles of each dealt to the
+// 8 XCDs in runs of equal length, so that skewed routing leaves no XCD with the busy experts and
+// the short items fill in at the end (contiguous experts per XCD: Qwen2-shaped dW13 of 3001 tokens
+// with skewed routing 2.4 ms).
 // Both matrices' gradients are one launch, with one end: per expert dW13's tiles, then dW2's.
 struct WeightArgs {
   TrainRows r;
@@ -1048,16 +1063,23 @@ struct WeightArgs {
     int64_t part;   // values of the result; splits > 1: out is [splits][that]
   } p[2];   // M 0: none
   int splits;
+  int* counters;   // of 8, zeros before the launch (kClaims)
 };
 
-template <class TOut>
+// kClaims: a workgroup's first three items are given, the others claimed in order from a counter,
+// three items ahead, so that workgroups that come later or slower take fewer of them.  Whoever
+// works on a tile, its sums are the same.  Without: splits > 1, or counters that nobody cleared.
+// (Behind dx, with every item given: Qwen2-shaped gradients of 3001 tokens, skewed, 2.73 ms, claimed
+// 2.38; of 200 rows of 1024 x 512 54 and 44 us; dense, 1024 rows of 4096 x 1024, 99 and 104.  With
+// one item given instead of three a dense backward of 4096 x 7168 x 2048 643 -> 695 us.)
+template <class TOut, bool kClaims>
 struct WeightsJob {
-  static constexpr bool kAAcross = true, kBAcross = true;
+  static constexpr bool kAAcross = true, kBAcross = true, kEmptyLast = kClaims;
   using A = Across;
   using B = Across;
   static constexpr int kEnd = -1;
   const WeightArgs& a;
-  const Smem& sm;   // pre: the experts by rank
+  Smem& sm;   // pre: the experts by rank
   int each0, each1, run0, run, hi, start, step, xcd;
 
   struct Item {
@@ -1087,7 +1109,8 @@ struct WeightsJob {
     // the parts of a tile's contraction are tiles of their own
     each0 = tiles(a.p[0].M) * tiles(a.p[0].N) * a.splits;
     each1 = tiles(a.p[1].M) * tiles(a.p[1].N) * a.splits;
-    if (E * (int64_t)(each0 + each1) <= (int64_t)gridDim.x) {   // an item a workgroup
+    // an item a workgroup, or few that share their operands
+    if (E * (int64_t)(each0 + each1) <= (int64_t)gridDim.x || (kClaims && each0 + each1 < 64)) {
       run0 = each0;
       run = each0 + each1;
       xcd = -1;
@@ -1101,6 +1124,50 @@ struct WeightsJob {
       step = (int)gridDim.x / 8;
     }
     hi = E * run;
+    if constexpr (kClaims) {
+      // from the last workgroup on: the first ones may come from other work
+      if (l.tid == 0) {
+        int n = 0;
+        for (int k = 0; k < 3; ++k) {
+          const int it = step - 1 - start + k * step;
+          if (present(it)) m.claim[n++] = it;
+        }
+        while (n < 3) m.claim[n++] = next_claim();   // in the order of the list, as all are
+      }
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ bool present(int it) const {
+    int e, k, tile;
+    return it < hi && tile_of(it, &e, &k, &tile);
+  }
+  // one lane: an item nobody has, or hi
+  __device__ __forceinline__ int next_claim() const {
+    int it;
+    do {
+      it = 3 * step + __hip_atomic_fetch_add(a.counters + max(xcd, 0), 1, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
+    } while (it < hi && !present(it));
+    return it;
+  }
+  // at the start of item number it of this workgroup: the item three further on, claimed; and at
+  // the end of it, where it has come, kept
+  __device__ __forceinline__ int claim(const Lane& l) const {
+    int taken = 0;
+    if constexpr (kClaims)
+      if (l.tid == 0) {
+        int at = max(xcd, 0);
+        asm volatile("" : "+v"(at));   // a lane's own address: what it adds is not waited for here
+        taken = __hip_atomic_fetch_add(a.counters + at, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    return taken;
+  }
+  __device__ __forceinline__ void claimed(const Lane& l, int number, int taken) const {
+    if constexpr (kClaims)
+      if (l.tid == 0) {
+        const int it = 3 * step + taken;
+        sm.claim[(number + 3) & 3] = it < hi && !present(it) ? next_claim() : it;
+      }
   }
   // the expert, product and tile of place it in this XCD's order; false: none
   __device__ __forceinline__ bool tile_of(int it, int* e, int* k, int* tile) const {
@@ -1118,10 +1185,15 @@ struct WeightsJob {
     while (it < hi && !tile_of(it, &e, &k, &tile)) it += step;
     return it < hi ? it : kEnd;
   }
-  __device__ __forceinline__ int first() const { return held(start); }
-  __device__ __forceinline__ int next(int it) const { return held(it + step); }
+  // kClaims: the number of an item of this workgroup
+  __device__ __forceinline__ int first() const { return kClaims ? next(-1) : held(start); }
+  __device__ __forceinline__ int next(int it) const {
+    if (kClaims) return uniform(sm.claim[(it + 1) & 3]) < hi ? it + 1 : kEnd;
+    return held(it + step);
+  }
 
   __device__ __forceinline__ Item item(int it) const {
+    if (kClaims) it = uniform(sm.claim[it & 3]);
     Item x;
     int at;
     tile_of(it, &x.e, &x.k, &at);
@@ -1166,12 +1238,31 @@ struct WeightsJob {
   }
 };
 
-template <class TOut>
+template <class TOut, bool kClaims>
 __global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
   TRAIN_UNITS;
   __shared__ Smem sm;
   const Lane l(threadIdx.x);
-  WeightsJob<TOut> job(a, l, sm);
+  WeightsJob<TOut, kClaims> job(a, l, sm);
+  stream(l, job, units);
+}
+
+// dx, then the weights' gradients, by workgroups as they come: the tiles of the latter fill the
+// rounds that dx leaves part empty.  (In two launches and in one, a backward: tiny layer 36 and
+// 30 us; 200 rows of 1024 x 512 56 and 44; 64 experts of 3584 x 2560, 128 tokens, 1522 and 1470,
+// 3001 tokens 2430 and 2378; 8 of 4096 x 14336, 4096 tokens, 5622 and 5526; dense, 1003 rows of
+// 2048 x 1024, 97 and 99.)
+template <bool kSplit, class TOut>
+__global__ __launch_bounds__(kThreads, 1) void grads_kernel(Args a, WeightArgs w) {
+  TRAIN_UNITS;
+  __shared__ Smem sm;
+  const Lane l(threadIdx.x);
+  {
+    RowsJob<kDX, false, kSplit> job(a, l, sm);
+    stream(l, job, units);
+  }
+  __syncthreads();   // the experts' lists are read to the end
+  WeightsJob<TOut, true> job(w, l, sm);
   stream(l, job, units);
 }
 
@@ -1311,8 +1402,13 @@ int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room, bool x
   return n < 2 ? 1 : (int)n;
 }
 
-template <Op kOp, bool kFp8>
-hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
+// The most items a product over rows has, its parts and its grid
+struct RowsPlan {
+  int64_t items;
+  unsigned grid;
+};
+template <Op kOp>
+hipError_t plan_rows(Args& a, const PartSpace& space, RowsPlan* plan) {
   const int per_tile = kOp == kGateUp ? kTile / 2 : kTile;
   const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
   const int K = kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
@@ -1320,28 +1416,38 @@ hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
   const int64_t pairs = a.r.counts ? a.r.tokens * a.r.K : a.r.tokens;
   const int64_t spans = pairs / kTile + (a.r.counts ? (a.r.E < pairs ? a.r.E : pairs) : 1);
   const int64_t items = spans * ((F + per_tile - 1) / per_tile);
-  if (pairs == 0) return hipSuccess;
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
   const int64_t values = a.r.rows * (kOp == kGateUp ? 2 * (int64_t)F : F);
   a.part = space.part;
   a.splits = parts_of(items, K / kBlock, values, space.bytes, true);
-  if (a.splits == 1) {
-    // twice the items, as they may be cut in two
-    hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(grid_of(2 * items)), dim3(kThreads), 0,
-                       s, a);
-    return hipGetLastError();
-  }
-  // an XCD's run, and its run of short experts, in one round (without: dx of 1003 rows of
-  // 1088 x 1856 48 us, with 30)
-  hipLaunchKernelGGL((rows_kernel<kOp, false, true>),
-                     dim3(grid_of(8 * ((items + 7) / 8 + 1) * a.splits)), dim3(kThreads), 0, s, a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  const int64_t lanes = a.r.rows * (F / 8);
+  plan->items = items;
+  // whole: twice the items, as they may be cut in two; in parts: an XCD's run, and its run of
+  // short experts, in one round (without: dx of 1003 rows of 1088 x 1856 48 us, with 30)
+  plan->grid = grid_of(a.splits == 1 ? 2 * items : 8 * ((items + 7) / 8 + 1) * a.splits);
+  return hipSuccess;
+}
+
+template <Op kOp, bool kFp8>
+hipError_t finish_rows(const Args& a, hipStream_t s) {
+  const int64_t lanes = a.r.rows * ((kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H) / 8);
   hipLaunchKernelGGL((finish_rows_kernel<kOp, kFp8>),
                      dim3((unsigned)((lanes + kFinishThreads - 1) / kFinishThreads)),
                      dim3(kFinishThreads), 0, s, a);
   return hipGetLastError();
+}
+
+template <Op kOp, bool kFp8>
+hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
+  if (a.r.tokens == 0) return hipSuccess;
+  RowsPlan plan;
+  hipError_t e = plan_rows<kOp>(a, space, &plan);
+  if (e != hipSuccess) return e;
+  if (a.splits == 1)
+    hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(plan.grid), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((rows_kernel<kOp, false, true>), dim3(plan.grid), dim3(kThreads), 0, s, a);
+  e = hipGetLastError();
+  return e == hipSuccess && a.splits > 1 ? finish_rows<kOp, kFp8>(a, s) : e;
 }
 
 Args args_of(const TrainRows& r) {
@@ -1375,63 +1481,84 @@ hipError_t launch_train_down(const TrainRows& r, const void* w2, const uint16_t*
 }
 
 hipError_t launch_train_dact(const TrainRows& r, const void* w2, const void* dy,
-                             const SavedRows& saved, uint16_t* act, uint16_t* dh,
+                             const SavedRows& saved, uint16_t* act, uint16_t* dh, int* counters,
                              const PartSpace& space, hipStream_t s) {
   Args a = args_of(r);
   a.w = static_cast<const uint16_t*>(w2);
   a.in = static_cast<const uint16_t*>(dy);
   a.act = act;
   a.dh = dh;
+  a.counters = counters;
   a.h = static_cast<uint16_t*>(saved.h);
   a.scales = saved.scales;
   return saved.fp8 ? launch_rows<kDAct, true>(a, space, s) : launch_rows<kDAct, false>(a, space, s);
 }
 
-hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
-                           const PartSpace& space, hipStream_t s) {
-  Args a = args_of(r);
-  a.w = static_cast<const uint16_t*>(w13);
-  a.in = dh;
-  a.out = static_cast<uint16_t*>(dx);
-  return launch_rows<kDX, false>(a, space, s);
-}
-
-hipError_t launch_train_dw(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
-                           void* dw13, const uint16_t* act, const void* dy, void* dw2, bool f32,
-                           const PartSpace& space, hipStream_t s) {
+hipError_t launch_train_grads(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
+                              const uint16_t* x_rows, void* dw13, const uint16_t* act,
+                              const void* dy, void* dw2, bool f32, const PartSpace& space,
+                              int* counters, hipStream_t s) {
   const int64_t matrices = r.counts ? r.E : 1;
   const int64_t n13 = dw13 ? matrices * 2 * r.I * r.H : 0, n2 = dw2 ? matrices * r.H * r.I : 0;
-  WeightArgs a{r,
+  WeightArgs w{r,
                {{x_rows, dh, dw13, dw13 ? r.H : 0, 2 * r.I, n13},
                 {act, static_cast<const uint16_t*>(dy), dw2, dw2 ? r.I : 0, r.H, n2}},
-               1};
+               1,
+               counters};
   int64_t items = 0;
-  for (const WeightArgs::Product& p : a.p)
+  for (const WeightArgs::Product& p : w.p)
     items += matrices * ((p.M + kTile - 1) / kTile) * ((p.N + kTile - 1) / kTile);
-  if (items == 0) return hipSuccess;
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
   // the most rows an expert may have
   const int64_t rows = r.tokens < r.rows ? r.tokens : r.rows;
-  a.splits = parts_of(items, rows / kBlock, n13 + n2, space.bytes, false);
-  if (a.splits > 1) {
-    a.p[0].out = space.part;
-    a.p[1].out = space.part + a.splits * n13;
+  w.splits = parts_of(items, rows / kBlock, n13 + n2, space.bytes, false);
+  const dim3 block(kThreads);
+  hipError_t e = hipSuccess;
+  if (dx && r.tokens > 0) {
+    Args a = args_of(r);
+    a.w = static_cast<const uint16_t*>(w13);
+    a.in = dh;
+    a.out = static_cast<uint16_t*>(dx);
+    if (items == 0 || w.splits > 1) {
+      e = launch_rows<kDX, false>(a, space, s);
+    } else {
+      RowsPlan plan;
+      e = plan_rows<kDX>(a, space, &plan);
+      if (e != hipSuccess) return e;
+      const dim3 grid(grid_of(plan.grid + items));
+      if (a.splits > 1 && f32) hipLaunchKernelGGL((grads_kernel<true, float>), grid, block, 0, s, a, w);
+      else if (a.splits > 1) hipLaunchKernelGGL((grads_kernel<true, uint16_t>), grid, block, 0, s, a, w);
+      else if (f32) hipLaunchKernelGGL((grads_kernel<false, float>), grid, block, 0, s, a, w);
+      else hipLaunchKernelGGL((grads_kernel<false, uint16_t>), grid, block, 0, s, a, w);
+      e = hipGetLastError();
+      return e == hipSuccess && a.splits > 1 ? finish_rows<kDX, false>(a, s) : e;
+    }
   }
-  const dim3 grid(grid_of(items * a.splits)), block(kThreads);
-  if (f32 || a.splits > 1) hipLaunchKernelGGL(weights_kernel<float>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(weights_kernel<uint16_t>, grid, block, 0, s, a);
-  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || items == 0) return e;
+  const dim3 grid(grid_of(items * w.splits));
+  if (w.splits > 1) {
+    w.p[0].out = space.part;
+    w.p[1].out = space.part + w.splits * n13;
+    hipLaunchKernelGGL((weights_kernel<float, false>), grid, block, 0, s, w);
+  } else if (r.tokens == 0) {
+    if (f32) hipLaunchKernelGGL((weights_kernel<float, false>), grid, block, 0, s, w);
+    else hipLaunchKernelGGL((weights_kernel<uint16_t, false>), grid, block, 0, s, w);
+  } else {
+    if (f32) hipLaunchKernelGGL((weights_kernel<float, true>), grid, block, 0, s, w);
+    else hipLaunchKernelGGL((weights_kernel<uint16_t, true>), grid, block, 0, s, w);
+  }
+  e = hipGetLastError();
   void* const outs[2] = {dw13, dw2};
-  for (int k = 0; k < 2 && a.splits > 1 && e == hipSuccess; ++k) {
-    const int64_t n = a.p[k].part;
+  for (int k = 0; k < 2 && w.splits > 1 && e == hipSuccess; ++k) {
+    const int64_t n = w.p[k].part;
     if (n == 0) continue;
     const dim3 g((unsigned)((n / 8 + kFinishThreads - 1) / kFinishThreads)), b(kFinishThreads);
-    const float* part = static_cast<const float*>(a.p[k].out);
+    const float* part = static_cast<const float*>(w.p[k].out);
     if (f32)
-      hipLaunchKernelGGL(finish_weights_kernel<float>, g, b, 0, s, part, n, a.splits,
+      hipLaunchKernelGGL(finish_weights_kernel<float>, g, b, 0, s, part, n, w.splits,
                          static_cast<float*>(outs[k]));
     else
-      hipLaunchKernelGGL(finish_weights_kernel<uint16_t>, g, b, 0, s, part, n, a.splits,
+      hipLaunchKernelGGL(finish_weights_kernel<uint16_t>, g, b, 0, s, part, n, w.splits,
                          static_cast<uint16_t*>(outs[k]));
     e = hipGetLastError();
   }

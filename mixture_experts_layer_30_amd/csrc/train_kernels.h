@@ -34,6 +34,7 @@ struct PartSpace {
   int64_t bytes;
 };
 constexpr int kMaxParts = 16;
+constexpr int64_t kCounterBytes = 256;
 constexpr int64_t kPartBytes = (int64_t)64 << 20;   // no more is needed: see parts_of
 
 // act [rows][I] = silu(g) * u with g, u = w13 x; g and u kept
@@ -43,18 +44,18 @@ hipError_t launch_train_gate_up(const TrainRows& r, const void* x, const void* w
 // y [rows][H] = w2 act
 hipError_t launch_train_down(const TrainRows& r, const void* w2, const uint16_t* act, void* y,
                              const PartSpace& space, hipStream_t s);
-// from da = w2^T dy: act = silu(g) * u, and dh [rows][2I], the gradients of g and of u
+// from da = w2^T dy: act = silu(g) * u, and dh [rows][2I], the gradients of g and of u; counters
+// (8) are cleared
 hipError_t launch_train_dact(const TrainRows& r, const void* w2, const void* dy,
-                             const SavedRows& saved, uint16_t* act, uint16_t* dh,
+                             const SavedRows& saved, uint16_t* act, uint16_t* dh, int* counters,
                              const PartSpace& space, hipStream_t s);
-// dx [rows][H] = w13^T dh
-hipError_t launch_train_dx(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
-                           const PartSpace& space, hipStream_t s);
-// dw13 [E][2I][H] = sum over an expert's rows of dh x^T (x_rows: x by row), and dw2 [E][H][I] that
-// of dy act^T; either null: not wanted; f32: their type is fp32, else bf16
-hipError_t launch_train_dw(const TrainRows& r, const uint16_t* x_rows, const uint16_t* dh,
-                           void* dw13, const uint16_t* act, const void* dy, void* dw2, bool f32,
-                           const PartSpace& space, hipStream_t s);
+// dx [rows][H] = w13^T dh, dw13 [E][2I][H] = sum over an expert's rows of dh x^T (x_rows: x by row)
+// and dw2 [E][H][I] that of dy act^T, each where given; f32: the type of dw13 and dw2 is fp32, else
+// bf16; counters: those that launch_train_dact has cleared (where there are tokens)
+hipError_t launch_train_grads(const TrainRows& r, const void* w13, const uint16_t* dh, void* dx,
+                              const uint16_t* x_rows, void* dw13, const uint16_t* act,
+                              const void* dy, void* dw2, bool f32, const PartSpace& space,
+                              int* counters, hipStream_t s);
 
 // [T][H] values in blocks of 32 to e4m3 codes and the biased exponents of the blocks' scales
 hipError_t launch_pack_fp8(const void* x, int dt, int64_t T, int H, uint8_t* codes,

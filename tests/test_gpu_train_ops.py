@@ -114,6 +114,8 @@ CASES = [
     # few rows of wide experts: the contraction in parts
     (2, 4096, 1024, 8, 2, 1, B.PAD_BLOCK, False, False, B.SAVE_BF16),
     (5, 1024, 2048, 3, 1, 64, B.PAD_MAX, False, False, B.SAVE_FP8),
+    # the weights' gradients claimed XCD by XCD, from runs of unequal length
+    (600, 1088, 1856, 3, 2, 16, B.PAD_BLOCK, True, False, B.SAVE_FP8),
     # the weights' gradients in parts
     (2100, 128, 192, 1, 1, 16, B.PAD_BLOCK, False, False, B.SAVE_FP8),
 ]

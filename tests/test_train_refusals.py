@@ -57,10 +57,10 @@ ROUTED = [(INV, dict(K=0)), (INV, dict(K=9)), (UNS, dict(E=257)), (INV, dict(pla
 def test_workspace_bytes(L):
     assert L.moe_ffn_train_workspace_bytes(0, H, I) == 0
     # a of every row, and 16 partial sums of its widest product, 64 MiB of them at most; for the
-    # gradients dh and x of every row too
+    # gradients dh and x of every row too, and counters
     n = L.moe_ffn_train_workspace_bytes(384, H, I)
     assert n == 384 * I * 2 + 16 * 384 * 2 * I * 4
-    assert L.moe_ffn_backward_workspace_bytes(384, H, I) == n + 384 * (I * 4 + H * 2)
+    assert L.moe_ffn_backward_workspace_bytes(384, H, I) == n + 384 * (I * 4 + H * 2) + 256
     assert L.moe_ffn_train_workspace_bytes(1 << 16, H, I) == (1 << 16) * I * 2 + (64 << 20)
     for fn in (L.moe_ffn_train_workspace_bytes, L.moe_ffn_backward_workspace_bytes):
         sizes = [fn(rows, H, I) for rows in range(0, 10000, 7)]

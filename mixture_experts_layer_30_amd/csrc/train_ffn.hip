@@ -1387,14 +1387,18 @@ Divider divider(int K) {
 // Parts of the contraction of a launch of `items` items (at most) of `blocks` blocks, whose sums
 // are `values` in all: as many as the compute units take in one round (`xcds`: of runs that each
 // XCD has of its own) where the items would leave three quarters of them idle, 16 blocks or more,
-// and as `room` bytes hold; up to 8 of 4 blocks or more, more of 8.
+// and as `room` bytes hold; up to 8 of 4 blocks or more, more of 8.  others: items of the same
+// launch; where they fit, they have compute units of their own.
 // Measured, whole and in parts: one token of a Mixtral-shaped down product 219 and 51 us; the da
 // and dx of 200 rows of 1024 x 512 48 us in parts of 8 blocks or more, 42 of 4 (128 rows of
 // 4096 x 4096, 16 parts of 4 and 8 of 8: 69 and 65); 300 rows of 512 x 512 forward, of 8 blocks,
-// 33 whole and 42.
-int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room, bool xcds) {
+// 33 whole and 42.  A dense backward, dx in as many parts as without others and in fewer: 1003 rows
+// of 1088 x 1856 97 and 77 us, 900 of 2048 x 1536 102 and 80, 512 of 2048 x 2048 83 and 90.
+int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room, bool xcds,
+             int64_t others = 0) {
   if (items < 1 || 4 * items > workgroups() || blocks < 16 || values < 1) return 1;
-  int64_t n = xcds ? workgroups() / 8 / ((items + 7) / 8) : workgroups() / items;
+  const int64_t units = others < workgroups() ? workgroups() - others : workgroups();
+  int64_t n = xcds ? units / 8 / ((items + 7) / 8) : units / items;
   const int64_t most = blocks / 4 < 8 ? blocks / 4 : blocks / 8 > 8 ? blocks / 8 : 8;
   if (n > kMaxParts) n = kMaxParts;
   if (n > most) n = most;
@@ -1408,7 +1412,7 @@ struct RowsPlan {
   unsigned grid;
 };
 template <Op kOp>
-hipError_t plan_rows(Args& a, const PartSpace& space, RowsPlan* plan) {
+hipError_t plan_rows(Args& a, const PartSpace& space, int64_t others, RowsPlan* plan) {
   const int per_tile = kOp == kGateUp ? kTile / 2 : kTile;
   const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
   const int K = kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
@@ -1419,7 +1423,7 @@ hipError_t plan_rows(Args& a, const PartSpace& space, RowsPlan* plan) {
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
   const int64_t values = a.r.rows * (kOp == kGateUp ? 2 * (int64_t)F : F);
   a.part = space.part;
-  a.splits = parts_of(items, K / kBlock, values, space.bytes, true);
+  a.splits = parts_of(items, K / kBlock, values, space.bytes, true, others);
   plan->items = items;
   // whole: twice the items, as they may be cut in two; in parts: an XCD's run, and its run of
   // short experts, in one round (without: dx of 1003 rows of 1088 x 1856 48 us, with 30)
@@ -1440,7 +1444,7 @@ template <Op kOp, bool kFp8>
 hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
   if (a.r.tokens == 0) return hipSuccess;
   RowsPlan plan;
-  hipError_t e = plan_rows<kOp>(a, space, &plan);
+  hipError_t e = plan_rows<kOp>(a, space, 0, &plan);
   if (e != hipSuccess) return e;
   if (a.splits == 1)
     hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(plan.grid), dim3(kThreads), 0, s, a);
@@ -1523,7 +1527,7 @@ hipError_t launch_train_grads(const TrainRows& r, const void* w13, const uint16_
       e = launch_rows<kDX, false>(a, space, s);
     } else {
       RowsPlan plan;
-      e = plan_rows<kDX>(a, space, &plan);
+      e = plan_rows<kDX>(a, space, items, &plan);
       if (e != hipSuccess) return e;
       const dim3 grid(grid_of(plan.grid + items));
       if (a.splits > 1 && f32) hipLaunchKernelGGL((grads_kernel<true, float>), grid, block, 0, s, a, w);

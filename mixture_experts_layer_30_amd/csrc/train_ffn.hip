@@ -44,12 +44,13 @@
 // Measured (kernel times; the matrix pipe busy, at the clock that the power limit leaves, 1.8 to
 // 2.1 of 2.4 GHz).  Bound by the matrix pipe and, between its turns, by barriers and LDS:
 //   8 experts of 4096 x 14336, 4096 tokens, K = 2: gate/up 1.77 ms, 1.09 PFLOP/s (61%); down 1.01,
-//   0.95; da 1.05, 0.91; dx 1.95, 0.99 (55%); both weights' gradients 2.74, 1.05 (54%)
+//   0.95; da 1.05, 0.91; dx 1.95, 0.99 (55%); both weights' gradients 2.74, 1.05 (54%); these and
+//   dx in one launch 4.46 to 4.75, 1.01 to 1.08 (57%)
 //   one expert of 7168 x 2048, 4096 rows: gate/up 186 to 211 us, 1.14 to 1.29 PFLOP/s (62%)
 // Bound by memory, 64 experts of 3584 x 2560, 128 tokens, K = 8: da 293 us, 4.0 TB/s (the gradients
 // written before still leave the caches); dx 426, 5.5; the weights' gradients 840 to 900 us, 3.5 GB
 // of them (stores alone 646, the rest alone 405: a workgroup's stores and loads wait for each
-// other in one order)
+// other in one order); in one launch 1.21 to 1.31 ms
 //
 // The features of a tile are dealt to MFMA rows so that a lane's sums of two neighbouring MFMA
 // tiles are 8 neighbours in memory (feature(): 16-byte stores, 64 bytes of a row side by side).
@@ -818,7 +819,8 @@ __device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
 // turn, so that the spans that share a weight tile run side by side on one L2.  Experts of up to
 // 128 rows come after all others, whose items take twice as long (Qwen2-shaped da and dx of 3001
 // tokens with skewed routing: 517 -> 472 and 817 -> 742 us).  Where a run's last round would leave
-// half the workgroups or more without an item, its items are cut into two of 128 rows.
+// half the workgroups or more without an item, its items are cut into two of 128 rows (kCut; not
+// where other work fills the round: a dense backward of 1024 rows of 4096 x 1024 104 -> 90 us).
 //
 // An item of up to 128 rows takes 0.8 of a whole one's time, of 32 rows hardly less (Mixtral-shaped
 // dx: 540 and 520 against 670 us): its features come from memory and out of LDS all the same.  So
@@ -826,7 +828,7 @@ __device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
 //
 // kSplit: the contraction of every item is cut into a.splits parts, items of their own, whose sums
 // go to a.part and are added by the finish kernels.
-template <Op kOp, bool kFp8, bool kSplit>
+template <Op kOp, bool kFp8, bool kSplit, bool kCut = !kSplit>
 struct RowsJob {
   static constexpr bool kAAcross = kOp == kDAct || kOp == kDX, kBAcross = false;
   static constexpr bool kEmptyLast = false;
@@ -865,7 +867,7 @@ struct RowsJob {
     light0 = xcd * per_light;
     full = max(0, min(per, all - full0));
     const int over = uniform(full % step);
-    cut = !kSplit && 2 * over <= step ? over : 0;
+    cut = kCut && 2 * over <= step ? over : 0;
     full -= cut;
     hi = full + 2 * cut + max(0, min(per_light, lights - light0));
     if (kSplit) hi *= a.splits;
@@ -1258,7 +1260,7 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(Args a, WeightArgs w
   __shared__ Smem sm;
   const Lane l(threadIdx.x);
   {
-    RowsJob<kDX, false, kSplit> job(a, l, sm);
+    RowsJob<kDX, false, kSplit, false> job(a, l, sm);
     stream(l, job, units);
   }
   __syncthreads();   // the experts' lists are read to the end
@@ -1406,13 +1408,9 @@ int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room, bool x
   return n < 2 ? 1 : (int)n;
 }
 
-// The most items a product over rows has, its parts and its grid
-struct RowsPlan {
-  int64_t items;
-  unsigned grid;
-};
+// The parts of a product over rows, and the grid for the most items it can have
 template <Op kOp>
-hipError_t plan_rows(Args& a, const PartSpace& space, int64_t others, RowsPlan* plan) {
+hipError_t plan_rows(Args& a, const PartSpace& space, int64_t others, unsigned* grid) {
   const int per_tile = kOp == kGateUp ? kTile / 2 : kTile;
   const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
   const int K = kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
@@ -1424,10 +1422,9 @@ hipError_t plan_rows(Args& a, const PartSpace& space, int64_t others, RowsPlan* 
   const int64_t values = a.r.rows * (kOp == kGateUp ? 2 * (int64_t)F : F);
   a.part = space.part;
   a.splits = parts_of(items, K / kBlock, values, space.bytes, true, others);
-  plan->items = items;
   // whole: twice the items, as they may be cut in two; in parts: an XCD's run, and its run of
   // short experts, in one round (without: dx of 1003 rows of 1088 x 1856 48 us, with 30)
-  plan->grid = grid_of(a.splits == 1 ? 2 * items : 8 * ((items + 7) / 8 + 1) * a.splits);
+  *grid = grid_of(a.splits == 1 ? 2 * items : 8 * ((items + 7) / 8 + 1) * a.splits);
   return hipSuccess;
 }
 
@@ -1443,13 +1440,13 @@ hipError_t finish_rows(const Args& a, hipStream_t s) {
 template <Op kOp, bool kFp8>
 hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
   if (a.r.tokens == 0) return hipSuccess;
-  RowsPlan plan;
-  hipError_t e = plan_rows<kOp>(a, space, 0, &plan);
+  unsigned grid;
+  hipError_t e = plan_rows<kOp>(a, space, 0, &grid);
   if (e != hipSuccess) return e;
   if (a.splits == 1)
-    hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(plan.grid), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(grid), dim3(kThreads), 0, s, a);
   else
-    hipLaunchKernelGGL((rows_kernel<kOp, false, true>), dim3(plan.grid), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((rows_kernel<kOp, false, true>), dim3(grid), dim3(kThreads), 0, s, a);
   e = hipGetLastError();
   return e == hipSuccess && a.splits > 1 ? finish_rows<kOp, kFp8>(a, s) : e;
 }
@@ -1526,10 +1523,10 @@ hipError_t launch_train_grads(const TrainRows& r, const void* w13, const uint16_
     if (items == 0 || w.splits > 1) {
       e = launch_rows<kDX, false>(a, space, s);
     } else {
-      RowsPlan plan;
-      e = plan_rows<kDX>(a, space, items, &plan);
+      unsigned rows_grid;
+      e = plan_rows<kDX>(a, space, items, &rows_grid);
       if (e != hipSuccess) return e;
-      const dim3 grid(grid_of(plan.grid + items));
+      const dim3 grid(grid_of(rows_grid + items));
       if (a.splits > 1 && f32) hipLaunchKernelGGL((grads_kernel<true, float>), grid, block, 0, s, a, w);
       else if (a.splits > 1) hipLaunchKernelGGL((grads_kernel<true, uint16_t>), grid, block, 0, s, a, w);
       else if (f32) hipLaunchKernelGGL((grads_kernel<false, float>), grid, block, 0, s, a, w);

@@ -45,7 +45,7 @@
 // 2.1 of 2.4 GHz).  Bound by the matrix pipe and, between its turns, by barriers and LDS:
 //   8 experts of 4096 x 14336, 4096 tokens, K = 2: gate/up 1.77 ms, 1.09 PFLOP/s (61%); down 1.01,
 //   0.95; da 1.05, 0.91; dx 1.95, 0.99 (55%); both weights' gradients 2.74, 1.05 (54%); these and
-//   dx in one launch 4.46 to 4.75, 1.01 to 1.08 (57%)
+//   dx in one launch 4.40 to 4.61, 1.04 to 1.09 (57%)
 //   one expert of 7168 x 2048, 4096 rows: gate/up 186 to 211 us, 1.14 to 1.29 PFLOP/s (62%)
 // Bound by memory, 64 experts of 3584 x 2560, 128 tokens, K = 8: da 293 us, 4.0 TB/s (the gradients
 // written before still leave the caches); dx 426, 5.5; the weights' gradients 840 to 900 us, 3.5 GB

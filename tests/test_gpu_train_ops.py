@@ -351,6 +351,54 @@ def test_same_on_every_run_on_another_stream_and_in_a_graph():
         same(first, again)
 
 
+# many more tiles of the weights' gradients than workgroups: claimed by all, or XCD by XCD
+@pytest.mark.parametrize("T,H,I,E,K", [(900, 512, 448, 128, 4), (1500, 1088, 1856, 6, 2)])
+def test_one_workspace_again_and_again(T, H, I, E, K):
+    """Calls in turn on one workspace, eager and captured, of all gradients and of the weights'
+    alone, give the same values, on one stream and then on another."""
+    _, _, plan = routed(T, E, K, 16, B.PAD_BLOCK, 6)
+    g = gen(6)
+    x, drows = randn(g, T, H), randn(g, plan.cap, H, std=0.1)
+    w13, w2 = weights(g, E, H, I)
+    saved, _ = given(plan.cap, I, B.SAVE_BF16, g)
+    ws = space(B.moe_ffn_backward_workspace_bytes(plan.cap, H, I))
+    out = [torch.empty_like(drows), torch.empty_like(w13), torch.empty_like(w2)]
+
+    def run(rows=True, stream=None):
+        B.moe_grouped_ffn_backward(drows, x, w13, w2, plan, saved, ws, dxrows=out[0] if rows else None,
+                                   dw13=out[1], dw2=out[2], stream=stream)
+
+    def again(call):
+        for t in out:
+            t.fill_(9)
+        torch.cuda.synchronize()
+        call()
+        torch.cuda.synchronize()
+
+    again(run)
+    first = [t.clone() for t in out]
+    for e in range(E):
+        at, tok = expert_rows(plan, e)
+        if len(tok) == 0:
+            continue
+        a = (drows[at].double(), x[tok].double(), w13[e].double(), w2[e].double(), saved.h[at].double())
+        for got, ref, err in zip((first[0][at], first[1][e], first[2][e]), R.backward(*a)[2:],
+                                 R.backward_bounds(*a, HALF_STEP[BF])):
+            within(got, ref, err, e)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    side = torch.cuda.Stream()
+    held_rows = held(plan, T)
+    for _ in range(3):
+        for call in (run, graph.replay, lambda: run(stream=side)):
+            again(call)
+            assert torch.equal(out[0][held_rows], first[0][held_rows])
+            assert torch.equal(out[1], first[1]) and torch.equal(out[2], first[2])
+        again(lambda: run(rows=False))
+        assert torch.equal(out[1], first[1]) and torch.equal(out[2], first[2])
+
+
 def test_two_calls_at_once():
     """Steps on two streams, with workspaces of their own, are what each gives alone."""
     steps = []

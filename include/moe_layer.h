@@ -515,8 +515,9 @@ moe_status moe_norm_residual_backward(const void *dr, moe_dtype xdt, const void 
  * products; sums are fp32.  dw13 [E][2I][H] and dw2 [E][H][I] (dense: without E) are
  * of type dwdt, overwritten; an expert without rows (or T = 0) gets zeros.  Each of
  * dxrows, dw13 and dw2 may be NULL, not all of them; x may be NULL where dw13 is, and
- * w13 where dxrows is.  What is written may overlap nothing that is read (dxrows is
- * refused where it is drows or x).  Sums are in a fixed order: the same on every run.
+ * w13 where dxrows is.  What is written, the workspace too, may overlap nothing that is
+ * read and nothing else that is written: MOE_EINVAL where a value would be lost.  Sums
+ * are in a fixed order: the same on every run.
  * workspace: 16-byte aligned, with no contents to keep before or after the call; the
  * forward needs moe_ffn_train_workspace_bytes(rows, H, I) bytes, the gradients
  * moe_ffn_backward_workspace_bytes(rows, H, I); calls that may overlap need one each.
@@ -558,7 +559,7 @@ moe_status dense_ffn_backward(const void *dout, const void *x, int64_t T, int H,
  * off by at most 2^-4 of |v| and 2^-10 s.  A value that is not finite is kept as NaN and
  * has no part in the maximum.  moe_unpack_fp8 gives code * s, rounded to the type asked
  * for (both hold it exactly but bf16 below 2^-133).
- * x [T][H] dt; codes [T][H], not in place of x; scales [T][H/32].  Limits: H a multiple
+ * x [T][H] dt; codes [T][H]; scales [T][H/32]; none of them overlap.  Limits: H a multiple
  * of 32, T*H < 2^39.
  * Errors: MOE_EINVAL, MOE_EUNSUPPORTED.
  */

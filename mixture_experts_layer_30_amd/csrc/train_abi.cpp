@@ -2,6 +2,8 @@
 // computes is documented in include/moe_layer.h.
 #include <stdint.h>
 
+#include <initializer_list>
+
 #include "block_checks.h"
 #include "train_kernels.h"
 
@@ -56,6 +58,30 @@ moe_status check_space(const char* what, int64_t rows, const void* workspace, in
   return MOE_OK;
 }
 
+// A buffer of a call; bytes 0 or p NULL: none
+struct Buffer {
+  const char* name;
+  const void* p;
+  int64_t bytes;
+};
+
+// what a call writes (each of `written`) overlaps neither the others of them nor what it reads
+moe_status check_apart(const char* what, std::initializer_list<Buffer> written,
+                       std::initializer_list<Buffer> read) {
+  auto meet = [](const Buffer& a, const Buffer& b) {
+    const uintptr_t p = (uintptr_t)a.p, q = (uintptr_t)b.p;
+    return p && q && a.bytes > 0 && b.bytes > 0 && p < q + (uintptr_t)b.bytes &&
+           q < p + (uintptr_t)a.bytes;
+  };
+  for (const Buffer* a = written.begin(); a != written.end(); ++a) {
+    for (const Buffer* b = a + 1; b != written.end(); ++b)
+      if (meet(*a, *b)) return fail(MOE_EINVAL, "%s: %s and %s overlap", what, a->name, b->name);
+    for (const Buffer& b : read)
+      if (meet(*a, b)) return fail(MOE_EINVAL, "%s: %s overwrites %s", what, a->name, b.name);
+  }
+  return MOE_OK;
+}
+
 moe::TrainRows planned(const moe_plan* plan, int64_t T, int E, int K, int H, int I) {
   return moe::TrainRows{plan->expert_counts, plan->expert_offsets, plan->sorted_ids, T, plan->cap,
                         K, E, H, I};
@@ -73,6 +99,13 @@ int64_t part_bytes(int64_t rows, int H, int I) {
 
 int64_t rounded(int64_t bytes) { return (bytes + 255) / 256 * 256; }
 
+Buffer saved_values(const moe::SavedRows& s, const moe::TrainRows& r) {
+  return {"the kept values", s.h, r.rows * r.I * (s.fp8 ? 2 : 4)};
+}
+Buffer saved_scales(const moe::SavedRows& s, const moe::TrainRows& r) {
+  return {"the kept scales", s.fp8 ? s.scales : nullptr, r.rows * r.I / 16};
+}
+
 moe_status forward(const char* what, const moe::TrainRows& r, const void* x, const void* w13,
                    const void* w2, const moe_saved* kept, void* workspace,
                    int64_t workspace_bytes, void* y, void* stream) {
@@ -84,6 +117,13 @@ moe_status forward(const char* what, const moe::TrainRows& r, const void* x, con
   if (st) return st;
   if (r.tokens == 0) return ok();
   if (!good(x, 16) || !good(w13, 16) || !good(w2, 16) || !good(y, 16)) return null_pointer(what);
+  const int64_t matrix = (int64_t)(r.counts ? r.E : 1) * r.H * r.I * 2;
+  const Buffer in{"x", x, r.tokens * r.H * 2}, up{"w13", w13, 2 * matrix}, down{"w2", w2, matrix};
+  const Buffer room{"the workspace", workspace, moe_ffn_train_workspace_bytes(r.rows, r.H, r.I)};
+  const Buffer rows{"rows", y, r.rows * r.H * 2};   // written last, when x and w13 have been read
+  st = check_apart(what, {saved_values(saved, r), saved_scales(saved, r), room}, {in, up, down, rows});
+  if (!st) st = check_apart(what, {rows}, {down});
+  if (st) return st;
   uint16_t* act = static_cast<uint16_t*>(workspace);
   const hipStream_t s = (hipStream_t)stream;
   const moe::PartSpace space{(float*)(act + rounded(r.rows * r.I * 2) / 2),
@@ -110,9 +150,28 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
     if (!good(dy, 16) || !good(w2, 16) || (dx ? !good(w13, 16) : !optional(w13, 16)) ||
         (dw13 ? !good(x, 16) : !optional(x, 16)))
       return null_pointer(what);
-    if (dx && (dx == dy || dx == x))   // both are read again after dx is written
-      return fail(MOE_EINVAL, "%s: the rows' gradient overwrites its input", what);
   }
+  // The gradients of the rows and of the weights are written by workgroups in no order, which
+  // still read dy, x and w13; w2 and the kept values have been read by then.
+  const int64_t matrix = (int64_t)(r.counts ? r.E : 1) * r.H * r.I;
+  const int64_t row_bytes = r.tokens > 0 ? r.rows * r.H * 2 : 0, x_bytes = r.tokens * r.H * 2;
+  const int64_t dw_bytes = dwdt == MOE_F32 ? 4 : 2;
+  const Buffer room{"the workspace", workspace,
+                    moe_ffn_backward_workspace_bytes(r.rows, r.H, r.I)};
+  const Buffer rows{"the rows' gradient", dx, row_bytes};
+  st = check_apart(what,
+                   {rows,
+                    {"dw13", dw13, 2 * matrix * dw_bytes},
+                    {"dw2", dw2, matrix * dw_bytes},
+                    room},
+                   {{"its input", dy, row_bytes},
+                    {"x", dw13 ? x : nullptr, x_bytes},
+                    {"w13", dx && r.tokens > 0 ? w13 : nullptr, 4 * matrix}});
+  if (!st) st = check_apart(what, {rows}, {{"x", x, x_bytes}});
+  if (!st && r.tokens > 0)
+    st = check_apart(what, {room},
+                     {{"w2", w2, 2 * matrix}, saved_values(saved, r), saved_scales(saved, r)});
+  if (st) return st;
   uint16_t* act = static_cast<uint16_t*>(workspace);
   uint16_t* dh = act + rounded(r.rows * r.I * 2) / 2;
   uint16_t* x_rows = dh + rounded(r.rows * r.I * 4) / 2;
@@ -213,7 +272,9 @@ moe_status moe_pack_fp8(const void* x, moe_dtype dt, int64_t T, int H, uint8_t* 
   if (st) return st;
   if (T == 0) return ok();
   if (!good(x, 16) || !good(codes, 16) || !scales) return null_pointer(what);
-  if (codes == x) return fail(MOE_EINVAL, "%s: the codes overwrite x", what);
+  st = check_apart(what, {{"codes", codes, T * H}, {"scales", scales, T * (H / 32)}},
+                   {{"x", x, T * H * (dt == MOE_F32 ? 4 : 2)}});
+  if (st) return st;
   return hip_status(moe::launch_pack_fp8(x, dt, T, H, codes, scales, (hipStream_t)stream), what);
 }
 
@@ -224,7 +285,9 @@ moe_status moe_unpack_fp8(const uint8_t* codes, const uint8_t* scales, int64_t T
   if (st) return st;
   if (T == 0) return ok();
   if (!good(codes, 16) || !scales || !good(x, 16)) return null_pointer(what);
-  if (codes == x) return fail(MOE_EINVAL, "%s: x overwrites the codes", what);
+  st = check_apart(what, {{"x", x, T * H * (dt == MOE_F32 ? 4 : 2)}},
+                   {{"codes", codes, T * H}, {"scales", scales, T * (H / 32)}});
+  if (st) return st;
   return hip_status(moe::launch_unpack_fp8(codes, scales, T, H, x, dt, (hipStream_t)stream), what);
 }
 

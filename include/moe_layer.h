@@ -517,7 +517,9 @@ moe_status moe_norm_residual_backward(const void *dr, moe_dtype xdt, const void 
  * dxrows, dw13 and dw2 may be NULL, not all of them; x may be NULL where dw13 is, and
  * w13 where dxrows is.  What is written, the workspace too, may overlap nothing that is
  * read and nothing else that is written: MOE_EINVAL where a value would be lost.  Sums
- * are in a fixed order: the same on every run.
+ * are in a fixed order: the same on every run of a call.  Which gradients are asked for
+ * is part of the call: where there are few items of work, it decides with the sizes
+ * how many parts a sum is taken in, and so its last bits.
  * workspace: 16-byte aligned, with no contents to keep before or after the call; the
  * forward needs moe_ffn_train_workspace_bytes(rows, H, I) bytes, the gradients
  * moe_ffn_backward_workspace_bytes(rows, H, I); calls that may overlap need one each.

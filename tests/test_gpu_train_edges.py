@@ -1,0 +1,83 @@
+"""Training the experts where buffers end, sums are cut into parts and offsets pass 2 GB: what
+the order of the sums depends on, what lies behind each buffer, and operands close to 4 GB."""
+import pytest
+import torch
+
+import train_reference as R
+from mixture_experts_layer_30_amd import binding as B
+from test_gpu_train_ops import (BF, HALF_STEP, expert_rows, gen, given, randn, routed, space, weights,
+                                within)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.lib()
+
+
+SUBSETS = [("dx", "dw13", "dw2"), ("dx",), ("dw13",), ("dw2",), ("dx", "dw2"), ("dx", "dw13"),
+           ("dw13", "dw2")]
+
+
+def each_subset(run, buffers, refs):
+    """Whichever gradients are asked for, each is within its bound, element by element, and the same
+    on a second run.  (Not the same as in another subset: sums may be taken in other parts.)"""
+    for want in SUBSETS:
+        first, again = (run({k: v for k, v in buffers().items() if k in want}) for _ in range(2))
+        for k in want:
+            for at, ref, err in refs[k]:
+                within(first[k][at], ref, err, (want, k))
+            assert torch.equal(first[k], again[k]), (want, k)
+
+
+# dx in parts, fewer of them next to the weights' tiles; parts of few blocks; the weights'
+# gradients in parts
+@pytest.mark.parametrize("T,H,I", [(1003, 1088, 1856), (200, 1024, 512), (512, 2048, 2048),
+                                   (2100, 128, 192), (2100, 192, 1088)])
+def test_dense_subsets_in_parts(T, H, I):
+    g = gen(T)
+    x, dout = randn(g, T, H), randn(g, T, H, std=0.1)
+    w13, w2 = (w[0] for w in weights(g, 1, H, I))
+    saved, h = given(T, I, B.SAVE_BF16, g)
+    n = B.moe_ffn_backward_workspace_bytes(T, H, I)
+
+    def run(out):
+        B.dense_ffn_backward(dout, x, w13, w2, saved, space(n), **out)
+        return out
+
+    a = (dout.double(), x.double(), w13.double(), w2.double(), h)
+    refs = {k: [(slice(None), ref, err)] for k, ref, err in
+            zip(("dx", "dw13", "dw2"), R.backward(*a)[2:], R.backward_bounds(*a, HALF_STEP[BF]))}
+    each_subset(run, lambda: dict(dx=torch.zeros_like(x), dw13=torch.zeros_like(w13),
+                                  dw2=torch.zeros_like(w2)), refs)
+
+
+@pytest.mark.parametrize("T,H,I,E,K", [(1500, 320, 1088, 2, 2), (1100, 256, 128, 4, 1),
+                                       (256, 1024, 1024, 4, 2), (40, 1024, 1024, 3, 2)])
+def test_grouped_subsets_in_parts(T, H, I, E, K):
+    _, _, plan = routed(T, E, K, 16, B.PAD_BLOCK, T)
+    g = gen(T + 1)
+    x, drows = randn(g, T, H), randn(g, plan.cap, H, std=0.1)
+    w13, w2 = weights(g, E, H, I)
+    saved, h = given(plan.cap, I, B.SAVE_FP8, g)
+    n = B.moe_ffn_backward_workspace_bytes(plan.cap, H, I)
+
+    def run(out):
+        names = {"dxrows" if k == "dx" else k: v for k, v in out.items()}
+        B.moe_grouped_ffn_backward(drows, x, w13, w2, plan, saved, space(n), **names)
+        return out
+
+    refs = {"dx": [], "dw13": [], "dw2": []}
+    for e in range(E):
+        at, tok = expert_rows(plan, e)
+        if len(tok) == 0:
+            continue
+        a = (drows[at].double(), x[tok].double(), w13[e].double(), w2[e].double(), h[at])
+        for k, where, ref, err in zip(refs, (at, e, e), R.backward(*a)[2:],
+                                      R.backward_bounds(*a, HALF_STEP[BF])):
+            refs[k].append((where, ref, err))
+    each_subset(run, lambda: dict(dx=torch.zeros_like(drows), dw13=torch.zeros_like(w13),
+                                  dw2=torch.zeros_like(w2)), refs)

@@ -35,7 +35,9 @@ struct PartSpace {
 };
 constexpr int kMaxParts = 16;
 constexpr int64_t kCounterBytes = 256;
-constexpr int64_t kPartBytes = (int64_t)64 << 20;   // no more is needed: see parts_of
+// no more is needed: the parts of a launch are no more items than it has compute units, and each
+// has at most 256 x 256 sums
+constexpr int64_t kPartBytes = (int64_t)64 << 20;
 
 // act [rows][I] = silu(g) * u with g, u = w13 x; g and u kept
 hipError_t launch_train_gate_up(const TrainRows& r, const void* x, const void* w13,

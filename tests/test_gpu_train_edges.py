@@ -5,8 +5,8 @@ import torch
 
 import train_reference as R
 from mixture_experts_layer_30_amd import binding as B
-from test_gpu_train_ops import (BF, HALF_STEP, expert_rows, gen, given, randn, routed, space, weights,
-                                within)
+from test_gpu_train_ops import (BF, DEV, HALF_STEP, expert_rows, gen, given, held, new_saved, randn,
+                                routed, space, weights, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -81,3 +81,36 @@ def test_grouped_subsets_in_parts(T, H, I, E, K):
             refs[k].append((where, ref, err))
     each_subset(run, lambda: dict(dx=torch.zeros_like(drows), dw13=torch.zeros_like(w13),
                                   dw2=torch.zeros_like(w2)), refs)
+
+
+@pytest.mark.parametrize("fmt", [B.SAVE_BF16, B.SAVE_FP8])
+@pytest.mark.parametrize("T,H,I,E,K", [(2, 1024, 2048, 4, 2), (1, 4096, 1024, 8, 2),
+                                       (9, 1088, 1856, 3, 3)])
+def test_padding_changes_no_value(T, H, I, E, K, fmt):
+    """Few rows of wide experts, whose contraction is cut into parts, are the same bits however
+    far apart the alignment lays them."""
+    seen = []
+    for block, pad in ((1, B.PAD_BLOCK), (16, B.PAD_BLOCK), (128, B.PAD_MAX), (1024, B.PAD_MAX)):
+        _, _, plan = routed(T, E, K, block, pad, 12)
+        g = gen(12)
+        x = randn(g, T, H)
+        w13, w2 = weights(g, E, H, I)
+        dpairs = randn(g, T * K, H, std=0.1)
+        at = plan.inv_pos[:T * K].long()
+        drows = torch.full((plan.cap, H), float("nan"), dtype=BF, device=DEV)
+        drows[at] = dpairs
+        saved = new_saved(plan.cap, I, fmt)
+        rows, dxrows = torch.zeros_like(drows), torch.zeros_like(drows)
+        dw13, dw2 = torch.zeros_like(w13), torch.zeros_like(w2)
+        B.moe_grouped_ffn_train(x, w13, w2, plan, saved,
+                                space(B.moe_ffn_train_workspace_bytes(plan.cap, H, I)), rows)
+        B.moe_grouped_ffn_backward(drows, x, w13, w2, plan, saved,
+                                   space(B.moe_ffn_backward_workspace_bytes(plan.cap, H, I)),
+                                   dxrows=dxrows, dw13=dw13, dw2=dw2)
+        kept = [saved.h[at].view(torch.uint8)] + ([saved.scales[at]] if fmt == B.SAVE_FP8 else [])
+        seen.append([rows[at], dxrows[at], dw13, dw2] + kept)
+        free = ~held(plan, T)
+        assert not rows[free].any() and not dxrows[free].any()
+    for other in seen[1:]:
+        for a, b in zip(seen[0], other):
+            assert torch.equal(a, b)

@@ -94,6 +94,8 @@ struct Smem {
 };
 
 enum Op { kGateUp, kDown, kDAct, kDX };
+// The contraction whole, or in parts whose sums are kept by row, or by pair
+enum Split { kWhole, kByRow, kByPair };
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 typedef __attribute__((address_space(3))) void* LdsPtr;
@@ -362,7 +364,8 @@ __device__ __forceinline__ void read_rows(const Lane& l, const uint8_t* unit, u3
 // Job: kAAcross, kBAcross; first(), next(it), kEnd: the places of this workgroup's items;
 // item(it); and of an item blocks(); two(): whether the rows' second half holds any; load(a, b):
 // sets the loaders; store(acc).  kEmptyLast: no item with blocks comes after one without; claim()
-// and claimed(): at the start and the end of an item (see WeightsJob).
+// and claimed(): at the start and the end of an item (see WeightsJob); what claim() gives also goes
+// to store().
 template <class Job>
 __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) {
   constexpr bool kAA = Job::kAAcross, kBA = Job::kBAcross;
@@ -527,7 +530,7 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
     const typename Job::Item x = job.item(it);
     const int n = job.blocks(x);
     const bool two = job.two(x);
-    const int later = job.claim(l);
+    const typename Job::Claim later = job.claim(l, x);
     if (n == 0 || !two) {
 #pragma unroll
       for (int tm = 0; tm < TM; ++tm)
@@ -547,7 +550,7 @@ __device__ __forceinline__ void stream(const Lane& l, Job& job, const Units& u) 
       wait_lgkm0();
       barrier();
     }
-    job.store(l.again(), x, acc);
+    job.store(l.again(), x, acc, later);
     __builtin_amdgcn_sched_barrier(0);
   }
   wait_vm<0>();   // no load into LDS outlives the workgroup
@@ -613,28 +616,47 @@ __device__ __forceinline__ void store_tile(const Lane& l, const f32x4 (&acc)[TM]
   }
 }
 
-// A tile's partial sums in fp32, out (its first column) of `pairs` rows of F values, one for each
-// pair: at(tn), and none where that is no pair.  Up's columns of a gate/up tile, 64 in each half
-// after gate's, go `up` further.  A part is at most half of kPartBytes.
-constexpr uint32_t kNowhere = 0x80000000u;   // past it, and so is a row further
-template <bool kGateUp, class At>
-__device__ __forceinline__ void store_parts(const Lane& l, const f32x4 (&acc)[TM][TN], float* out,
-                                            uint32_t pairs, int F, int f0, int cols, int up, int n,
-                                            At at) {
-  const uint32_t row_bytes = (uint32_t)F * 4;
-  const uint32_t col = (uint32_t)((kGateUp ? 32 : 64) * l.wm + 8 * l.g) * 4;
+// The sums of a gate/up tile in fp32, out of rows of 2I values (its first column of gate), 64
+// columns in each half of the tile, up's I further
+__device__ __forceinline__ void store_gate_up(const Lane& l, const f32x4 (&acc)[TM][TN], float* out,
+                                              int I, int rows, int cols) {
+  const uint32_t row_bytes = (uint32_t)I * 8;
+  const uint32_t off = (uint32_t)(l.wn * 16 + l.m) * row_bytes + (uint32_t)(32 * l.wm + 8 * l.g) * 4;
   const uint8_t* base = reinterpret_cast<const uint8_t*>(out);
-  const uint32_t all = pairs * row_bytes - (uint32_t)f0 * 4;
+  const uint32_t all = (uint32_t)(rows - 1) * row_bytes + (uint32_t)(I + min(cols, kHalf)) * 4;
 #pragma unroll
   for (int tn = 0; tn < TN; ++tn) {
-    if (64 * tn >= n) break;
-    const uint32_t pair = (uint32_t)at(tn);
-    const uint32_t off = pair < pairs ? pair * row_bytes + col : kNowhere;
+    if (64 * tn >= rows) break;
 #pragma unroll
-    for (int p = 0; p < TM / 2; ++p) {   // gate/up: gate, up, gate, up
+    for (int p = 0; p < TM / 2; ++p) {   // gate, up, gate, up
+      const Rsrc r = make_rsrc(base, 64 * (p >> 1) + 32 * l.wm < cols ? all : 0);
+      store_pair(r, off + (uint32_t)(64 * (p >> 1) + (p & 1 ? I : 0)) * 4,
+                 (uint32_t)(64 * tn) * row_bytes, l.g & 1, acc[2 * p][tn], acc[2 * p + 1][tn], out);
+    }
+  }
+}
+
+// The same of either tile by pair: out, of rows of F values, one for each pair, at column f0.  pair:
+// that of this lane's rows; all: bytes of the rows together, at most half of kPartBytes.
+constexpr uint32_t kNowhere = 0x80000000u;   // past any of them, and so are a row's columns after it
+template <bool kGateUp>
+__device__ __forceinline__ void store_by_pair(const Lane& l, const f32x4 (&acc)[TM][TN], float* out,
+                                              uint32_t all, int F, int I, int f0, int rows,
+                                              const int (&pair)[TN]) {
+  constexpr int kWide = kGateUp ? 32 : 64;   // columns of a wavefront row in a half
+  const int cols = (kGateUp ? I : F) - f0;
+  const uint32_t row_bytes = (uint32_t)F * 4, col = (uint32_t)(kWide * l.wm + 8 * l.g) * 4;
+  const uint8_t* base = reinterpret_cast<const uint8_t*>(out + f0);
+  all -= (uint32_t)f0 * 4;
+#pragma unroll
+  for (int tn = 0; tn < TN; ++tn) {
+    if (64 * tn >= rows) break;
+    const uint32_t off = tile_row(l, tn) < rows ? (uint32_t)pair[tn] * row_bytes + col : kNowhere;
+#pragma unroll
+    for (int p = 0; p < TM / 2; ++p) {
       const int f = kGateUp ? 64 * (p >> 1) : kHalf * (p >> 1) + 32 * (p & 1);
-      const Rsrc r = make_rsrc(base, f + (kGateUp ? 32 : 64) * l.wm < cols ? all : 0);
-      store_pair(r, off, (uint32_t)(f + (kGateUp && (p & 1) ? up : 0)) * 4, l.g & 1, acc[2 * p][tn],
+      const Rsrc r = make_rsrc(base, f + kWide * l.wm < cols ? all : 0);
+      store_pair(r, off, (uint32_t)(f + (kGateUp && (p & 1) ? I : 0)) * 4, l.g & 1, acc[2 * p][tn],
                  acc[2 * p + 1][tn], out);
     }
   }
@@ -679,8 +701,10 @@ struct Args {
   uint16_t* out;
   uint16_t* h;          // kept values: bf16, or codes
   uint8_t* scales;
-  float* part;          // partial sums [splits][pairs][features], where the contraction is split
+  float* part;          // partial sums [splits][part_rows][features], where the contraction is split
   int splits;
+  bool by_pair;         // part_rows: a row for each pair; else the rows of the buffers
+  int64_t part_rows;
   int* counters;        // kDAct: of 8, cleared
 };
 
@@ -767,11 +791,6 @@ struct Kept {
   }
 };
 
-// the pairs that the rows can hold
-__host__ __device__ __forceinline__ int64_t pairs_of(const TrainRows& r) {
-  return r.counts ? r.tokens * r.K : r.tokens;
-}
-
 // the rows of expert e, inside the row buffers whatever the plan says
 __device__ __forceinline__ int expert_rows(const TrainRows& r, int e, int* row0) {
   *row0 = 0;
@@ -840,7 +859,7 @@ __device__ __forceinline__ int last_at_most(const int* pre, int n, int at) {
 //
 // kSplit: the contraction of every item is cut into a.splits parts, items of their own, whose sums
 // go to a.part and are added by the finish kernels.
-template <Op kOp, bool kFp8, bool kSplit, bool kCut = !kSplit>
+template <Op kOp, bool kFp8, Split kSplit, bool kCut = kSplit == kWhole>
 struct RowsJob {
   static constexpr bool kAAcross = kOp == kDAct || kOp == kDX, kBAcross = false;
   static constexpr bool kEmptyLast = false;
@@ -882,7 +901,7 @@ struct RowsJob {
     cut = kCut && 2 * over <= step ? over : 0;
     full -= cut;
     hi = full + 2 * cut + max(0, min(per_light, lights - light0));
-    if (kSplit) hi *= a.splits;
+    if (kSplit != kWhole) hi *= a.splits;
   }
   static __device__ __forceinline__ int spans(int n) { return (n + kTile - 1) / kTile; }
 
@@ -895,7 +914,7 @@ struct RowsJob {
   __device__ __forceinline__ Item item(int it) const {
     Item x;
     x.part = 0;
-    if (kSplit) {
+    if (kSplit != kWhole) {
       const int whole = uniform(it / a.splits);
       x.part = it - whole * a.splits;
       it = whole;
@@ -923,7 +942,7 @@ struct RowsJob {
     const int all = x.n > 0 ? contraction() / kBlock : 0;
     x.block0 = 0;
     x.blocks = all;
-    if (kSplit) {
+    if (kSplit != kWhole) {
       const int each = uniform((all + a.splits - 1) / a.splits);
       x.block0 = min(all, x.part * each);
       x.blocks = min(each, all - x.block0);
@@ -931,8 +950,22 @@ struct RowsJob {
     return x;
   }
 
-  __device__ __forceinline__ int claim(const Lane&) const { return 0; }
-  __device__ __forceinline__ void claimed(const Lane&, int, int) const {}
+  // kByPair: the pairs of this lane's rows, loaded at the start of an item, used at its end (loaded
+  // there, between the stores, each load waits for the stores before it)
+  struct Claim {
+    int pair[TN];
+  };
+  __device__ __forceinline__ Claim claim(const Lane& l, const Item& x) const {
+    Claim c{};
+    if constexpr (kSplit == kByPair) {
+      const Rsrc ids = make_rsrc(a.r.sorted_ids + x.row0, (uint32_t)x.n * 4);
+#pragma unroll
+      for (int tn = 0; tn < TN; ++tn)
+        c.pair[tn] = __builtin_amdgcn_raw_buffer_load_b32(ids, tile_row(l, tn) * 4, 0, 0);
+    }
+    return c;
+  }
+  __device__ __forceinline__ void claimed(const Lane&, int, const Claim&) const {}
 
   __device__ __forceinline__ int contraction() const {
     return kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
@@ -975,18 +1008,23 @@ struct RowsJob {
     }
   }
 
-  __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN]) const {
+  __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN],
+                                        const Claim& c) const {
     const int H = a.r.H, I = a.r.I;
     if (x.n == 0) return;
-    if constexpr (kSplit) {
+    if constexpr (kSplit == kByPair) {
       const int F = kOp == kGateUp ? 2 * I : kOp == kDAct ? I : H;
-      const int64_t pairs = pairs_of(a.r);
-      store_parts<kOp == kGateUp>(l, acc, a.part + (size_t)x.part * pairs * F + x.f0, (uint32_t)pairs, F,
-                                  x.f0, (kOp == kGateUp ? I : F) - x.f0, I, x.n, [&](int tn) {
-                                    const int row = tile_row(l, tn);
-                                    if (row >= x.n) return -1;
-                                    return a.r.counts ? a.r.sorted_ids[x.row0 + row] : (int)x.row0 + row;
-                                  });
+      store_by_pair<kOp == kGateUp>(l, acc, a.part + (size_t)x.part * a.part_rows * F,
+                                    (uint32_t)a.part_rows * (uint32_t)F * 4, F, I, x.f0, x.n, c.pair);
+      return;
+    }
+    if constexpr (kSplit == kByRow) {
+      const int F = kOp == kGateUp ? 2 * I : kOp == kDAct ? I : H;
+      float* part = a.part + ((size_t)x.part * a.r.rows + x.row0) * F + x.f0;
+      if constexpr (kOp == kGateUp)
+        store_gate_up(l, acc, part, I, x.n, I - x.f0);
+      else
+        store_tile(l, acc, part, F, x.n, F - x.f0);
       return;
     }
     if constexpr (kOp == kDown || kOp == kDX) {
@@ -1050,7 +1088,7 @@ struct RowsJob {
   }
 };
 
-template <Op kOp, bool kFp8, bool kSplit>
+template <Op kOp, bool kFp8, Split kSplit>
 __global__ __launch_bounds__(kThreads, 1) void rows_kernel(Args a) {
   TRAIN_UNITS;
   __shared__ Smem sm;
@@ -1168,7 +1206,8 @@ struct WeightsJob {
   }
   // at the start of item number it of this workgroup: the item three further on, claimed; and at
   // the end of it, where it has come, kept
-  __device__ __forceinline__ int claim(const Lane& l) const {
+  typedef int Claim;
+  __device__ __forceinline__ int claim(const Lane& l, const Item&) const {
     int taken = 0;
     if constexpr (kClaims)
       if (l.tid == 0) {
@@ -1246,7 +1285,8 @@ struct WeightsJob {
     la.set(l, p.m_rows + (size_t)x.row0 * p.M, (uint32_t)p.M * 2, x.n, x.m0);
     lb.set(l, p.n_rows + (size_t)x.row0 * p.N, (uint32_t)p.N * 2, x.n, x.n0);
   }
-  __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN]) const {
+  __device__ __forceinline__ void store(const Lane& l, const Item& x, f32x4 (&acc)[TM][TN],
+                                        int) const {
     const WeightArgs::Product& p = a.p[x.k];
     store_tile(l, acc, static_cast<TOut*>(p.out) + (size_t)x.part * p.part +
                            ((size_t)x.e * p.N + x.n0) * p.M + x.m0, p.M,
@@ -1268,7 +1308,7 @@ __global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
 // 30 us; 200 rows of 1024 x 512 56 and 44; 64 experts of 3584 x 2560, 128 tokens, 1522 and 1470,
 // 3001 tokens 2430 and 2378; 8 of 4096 x 14336, 4096 tokens, 5622 and 5526; dense, 1003 rows of
 // 2048 x 1024, 97 and 99.)
-template <bool kSplit, class TOut>
+template <Split kSplit, class TOut>
 __global__ __launch_bounds__(kThreads, 1) void grads_kernel(Args a, WeightArgs w) {
   TRAIN_UNITS;
   __shared__ Smem sm;
@@ -1286,8 +1326,8 @@ __global__ __launch_bounds__(kThreads, 1) void grads_kernel(Args a, WeightArgs w
 //
 // Where a launch has few items, parts of their contraction run on the other compute units, and
 // their sums are added here in the order of the parts: bound by those sums' bytes, at most
-// kPartBytes.  They are kept by pair, so that padding costs no room and changes no sum (by row, one
-// token of a Mixtral-shaped layer forward, its rows 128 apart, took 153 us, and 138 16 apart).
+// kPartBytes.  Where padding leaves no room for them by row they are kept by pair, so that it
+// changes neither the parts nor a sum.
 // A lane has 8 neighbours of a row that holds a pair, as the products' epilogues do.
 constexpr int kFinishThreads = 256;
 
@@ -1302,7 +1342,7 @@ __device__ __forceinline__ void add_parts(const float* p, int64_t stride, int pa
   }
 }
 
-template <Op kOp, bool kFp8>
+template <Op kOp, bool kFp8, bool kPair>
 __global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(Args a) {
   const int H = a.r.H, I = a.r.I;
   const int width = kOp == kGateUp || kOp == kDAct ? I : H, groups = width / 8;
@@ -1310,16 +1350,19 @@ __global__ __launch_bounds__(kFinishThreads) void finish_rows_kernel(Args a) {
   const int64_t row = at / groups;
   if (row >= a.r.rows) return;
   const int c = (int)(at - row * groups) * 8;   // 4 lanes share a block of 32, and a row
-  const int64_t pairs = pairs_of(a.r);
-  const int64_t pair = a.r.counts ? a.r.sorted_ids[row] : row;
-  if (pair < 0 || pair >= pairs) return;
+  int64_t from = row;
+  if (a.r.counts) {
+    const int p = a.r.sorted_ids[row];
+    if (p < 0 || p >= a.r.tokens * a.r.K) return;
+    if (kPair) from = p;
+  }
   const int F = kOp == kGateUp ? 2 * I : width;
-  const int64_t stride = pairs * F;
+  const int64_t stride = a.part_rows * F;
   float v[8];
-  add_parts(a.part + pair * F + c, stride, a.splits, v);
+  add_parts(a.part + from * F + c, stride, a.splits, v);
   if constexpr (kOp == kGateUp) {
     float u[8], av[8];
-    add_parts(a.part + pair * F + I + c, stride, a.splits, u);
+    add_parts(a.part + from * F + I + c, stride, a.splits, u);
 #pragma unroll
     for (int q = 0; q < 8; ++q) av[q] = silu(v[q]) * u[q];
     *reinterpret_cast<u32x4*>(a.act + row * I + c) = bf16x8_of(av);
@@ -1430,13 +1473,19 @@ hipError_t plan_rows(Args& a, const PartSpace& space, int64_t others, unsigned* 
   const int F = kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H;
   const int K = kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
   // spans: one for each 256 rows, and a short one an expert
-  const int64_t pairs = pairs_of(a.r);
+  const int64_t pairs = a.r.counts ? a.r.tokens * a.r.K : a.r.tokens;
   const int64_t spans = pairs / kTile + (a.r.counts ? (a.r.E < pairs ? a.r.E : pairs) : 1);
   const int64_t items = spans * ((F + per_tile - 1) / per_tile);
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
-  const int64_t values = pairs * (kOp == kGateUp ? 2 * (int64_t)F : F);
+  const int64_t width = kOp == kGateUp ? 2 * (int64_t)F : F;
   a.part = space.part;
-  a.splits = parts_of(items, K / kBlock, values, space.bytes, true, others);
+  a.splits = parts_of(items, K / kBlock, pairs * width, space.bytes, true, others);
+  // By row where there is room for the padding too: by pair, whose rows a tile scatters, da and dx of
+  // 300 rows of 1024 x 2048 for two experts take 61 us for 59.  In the parts that have room by row,
+  // and by pair: one token of a Mixtral-shaped layer forward 153 and 139 us with its rows 128 apart,
+  // 304 and 141 with 1024.
+  a.by_pair = a.r.counts && a.splits > 1 && a.splits > space.bytes / (4 * a.r.rows * width);
+  a.part_rows = a.by_pair ? pairs : a.r.rows;
   // whole: twice the items, as they may be cut in two; in parts: an XCD's run, and its run of
   // short experts, in one round (without: dx of 1003 rows of 1088 x 1856 48 us, with 30)
   *grid = grid_of(a.splits == 1 ? 2 * items : 8 * ((items + 7) / 8 + 1) * a.splits);
@@ -1446,24 +1495,39 @@ hipError_t plan_rows(Args& a, const PartSpace& space, int64_t others, unsigned* 
 template <Op kOp, bool kFp8>
 hipError_t finish_rows(const Args& a, hipStream_t s) {
   const int64_t lanes = a.r.rows * ((kOp == kGateUp || kOp == kDAct ? a.r.I : a.r.H) / 8);
-  hipLaunchKernelGGL((finish_rows_kernel<kOp, kFp8>),
-                     dim3((unsigned)((lanes + kFinishThreads - 1) / kFinishThreads)),
-                     dim3(kFinishThreads), 0, s, a);
+  const dim3 grid((unsigned)((lanes + kFinishThreads - 1) / kFinishThreads)), block(kFinishThreads);
+  if (a.by_pair) hipLaunchKernelGGL((finish_rows_kernel<kOp, kFp8, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((finish_rows_kernel<kOp, kFp8, false>), grid, block, 0, s, a);
   return hipGetLastError();
+}
+
+template <Op kOp, bool kFp8>
+hipError_t launch_planned(const Args& a, unsigned grid, hipStream_t s) {
+  if (a.splits == 1)
+    hipLaunchKernelGGL((rows_kernel<kOp, kFp8, kWhole>), dim3(grid), dim3(kThreads), 0, s, a);
+  else if (!a.by_pair)
+    hipLaunchKernelGGL((rows_kernel<kOp, false, kByRow>), dim3(grid), dim3(kThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((rows_kernel<kOp, false, kByPair>), dim3(grid), dim3(kThreads), 0, s, a);
+  const hipError_t e = hipGetLastError();
+  return e == hipSuccess && a.splits > 1 ? finish_rows<kOp, kFp8>(a, s) : e;
 }
 
 template <Op kOp, bool kFp8>
 hipError_t launch_rows(Args a, const PartSpace& space, hipStream_t s) {
   if (a.r.tokens == 0) return hipSuccess;
   unsigned grid;
-  hipError_t e = plan_rows<kOp>(a, space, 0, &grid);
-  if (e != hipSuccess) return e;
-  if (a.splits == 1)
-    hipLaunchKernelGGL((rows_kernel<kOp, kFp8, false>), dim3(grid), dim3(kThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((rows_kernel<kOp, false, true>), dim3(grid), dim3(kThreads), 0, s, a);
-  e = hipGetLastError();
-  return e == hipSuccess && a.splits > 1 ? finish_rows<kOp, kFp8>(a, s) : e;
+  const hipError_t e = plan_rows<kOp>(a, space, 0, &grid);
+  return e == hipSuccess ? launch_planned<kOp, kFp8>(a, grid, s) : e;
+}
+
+template <class TOut>
+hipError_t launch_joined(const Args& a, const WeightArgs& w, unsigned grid, hipStream_t s) {
+  const dim3 g(grid), b(kThreads);
+  if (a.splits == 1) hipLaunchKernelGGL((grads_kernel<kWhole, TOut>), g, b, 0, s, a, w);
+  else if (!a.by_pair) hipLaunchKernelGGL((grads_kernel<kByRow, TOut>), g, b, 0, s, a, w);
+  else hipLaunchKernelGGL((grads_kernel<kByPair, TOut>), g, b, 0, s, a, w);
+  return hipGetLastError();
 }
 
 Args args_of(const TrainRows& r) {
@@ -1535,20 +1599,16 @@ hipError_t launch_train_grads(const TrainRows& r, const void* w13, const uint16_
     a.w = static_cast<const uint16_t*>(w13);
     a.in = dh;
     a.out = static_cast<uint16_t*>(dx);
-    if (items == 0 || w.splits > 1) {
-      e = launch_rows<kDX, false>(a, space, s);
-    } else {
-      unsigned rows_grid;
-      e = plan_rows<kDX>(a, space, items, &rows_grid);
-      if (e != hipSuccess) return e;
-      const dim3 grid(grid_of(rows_grid + items));
-      if (a.splits > 1 && f32) hipLaunchKernelGGL((grads_kernel<true, float>), grid, block, 0, s, a, w);
-      else if (a.splits > 1) hipLaunchKernelGGL((grads_kernel<true, uint16_t>), grid, block, 0, s, a, w);
-      else if (f32) hipLaunchKernelGGL((grads_kernel<false, float>), grid, block, 0, s, a, w);
-      else hipLaunchKernelGGL((grads_kernel<false, uint16_t>), grid, block, 0, s, a, w);
-      e = hipGetLastError();
+    const int64_t beside = w.splits == 1 ? items : 0;
+    unsigned rows_grid;
+    e = plan_rows<kDX>(a, space, beside, &rows_grid);
+    if (e != hipSuccess) return e;
+    if (beside > 0) {
+      const unsigned grid = grid_of(rows_grid + items);
+      e = f32 ? launch_joined<float>(a, w, grid, s) : launch_joined<uint16_t>(a, w, grid, s);
       return e == hipSuccess && a.splits > 1 ? finish_rows<kDX, false>(a, s) : e;
     }
+    e = launch_planned<kDX, false>(a, rows_grid, s);
   }
   if (e != hipSuccess || items == 0) return e;
   const dim3 grid(grid_of(items * w.splits));

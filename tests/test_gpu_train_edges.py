@@ -5,8 +5,8 @@ import torch
 
 import train_reference as R
 from mixture_experts_layer_30_amd import binding as B
-from test_gpu_train_ops import (BF, DEV, HALF_STEP, expert_rows, gen, given, held, new_saved, randn,
-                                routed, space, weights, within)
+from test_gpu_train_ops import (BF, DEV, HALF_STEP, check_kept, expert_rows, gen, given, held,
+                                new_saved, randn, routed, space, weights, within)
 
 pytestmark = pytest.mark.gpu
 
@@ -83,25 +83,25 @@ def test_grouped_subsets_in_parts(T, H, I, E, K):
                                   dw2=torch.zeros_like(w2)), refs)
 
 
+@pytest.mark.parametrize("dwdt", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("fmt", [B.SAVE_BF16, B.SAVE_FP8])
 @pytest.mark.parametrize("T,H,I,E,K", [(2, 1024, 2048, 4, 2), (1, 4096, 1024, 8, 2),
-                                       (9, 1088, 1856, 3, 3)])
-def test_padding_changes_no_value(T, H, I, E, K, fmt):
+                                       (9, 1088, 1856, 3, 3), (200, 1024, 512, 2, 1)])
+def test_padding_changes_no_value(T, H, I, E, K, fmt, dwdt):
     """Few rows of wide experts, whose contraction is cut into parts, are the same bits however
-    far apart the alignment lays them."""
+    far apart the alignment lays them, and within their bounds."""
+    g = gen(12)
+    x, dpairs = randn(g, T, H), randn(g, T * K, H, std=0.1)
+    w13, w2 = weights(g, E, H, I)
     seen = []
     for block, pad in ((1, B.PAD_BLOCK), (16, B.PAD_BLOCK), (128, B.PAD_MAX), (1024, B.PAD_MAX)):
         _, _, plan = routed(T, E, K, block, pad, 12)
-        g = gen(12)
-        x = randn(g, T, H)
-        w13, w2 = weights(g, E, H, I)
-        dpairs = randn(g, T * K, H, std=0.1)
         at = plan.inv_pos[:T * K].long()
         drows = torch.full((plan.cap, H), float("nan"), dtype=BF, device=DEV)
         drows[at] = dpairs
         saved = new_saved(plan.cap, I, fmt)
         rows, dxrows = torch.zeros_like(drows), torch.zeros_like(drows)
-        dw13, dw2 = torch.zeros_like(w13), torch.zeros_like(w2)
+        dw13, dw2 = (torch.full(w.shape, 9.0, dtype=dwdt, device=DEV) for w in (w13, w2))
         B.moe_grouped_ffn_train(x, w13, w2, plan, saved,
                                 space(B.moe_ffn_train_workspace_bytes(plan.cap, H, I)), rows)
         B.moe_grouped_ffn_backward(drows, x, w13, w2, plan, saved,
@@ -111,6 +111,22 @@ def test_padding_changes_no_value(T, H, I, E, K, fmt):
         seen.append([rows[at], dxrows[at], dw13, dw2] + kept)
         free = ~held(plan, T)
         assert not rows[free].any() and not dxrows[free].any()
+        if block > 1:
+            continue
+        for e in range(E):
+            here, tok = expert_rows(plan, e)
+            if len(tok) == 0:
+                assert not dw13[e].any() and not dw2[e].any()
+                continue
+            a = x[tok].double(), w13[e].double(), w2[e].double()
+            err_h, err_y = R.forward_bounds(*a)
+            h, _, y = R.forward(*a)
+            h = check_kept(saved, here, h, err_h)
+            within(rows[here], y, err_y, ("rows", e))
+            a = (drows[here].double(),) + a + (h,)
+            for got, ref, err in zip((dxrows[here], dw13[e], dw2[e]), R.backward(*a)[2:],
+                                     R.backward_bounds(*a, HALF_STEP[dwdt])):
+                within(got, ref, err, ("gradients", e))
     for other in seen[1:]:
         for a, b in zip(seen[0], other):
             assert torch.equal(a, b)

@@ -77,7 +77,7 @@ moe_status moe_permute(const void* x, moe_dtype dt, int64_t T, int H, int E, int
   if (T == 0) return ok();
   if (!good(x, 16) || !good(rows, 16)) return null_pointer(what);
   return hip_status(moe::launch_permute(x, dt, T, K, H, plan_rows(plan, K), E, plan->cap, rows,
-                                        (hipStream_t)stream),
+                                        true, (hipStream_t)stream),
                     what);
 }
 

@@ -5,9 +5,10 @@
 
 namespace moe {
 
-// Rows in the alignment's order and back (rm: the plan's arrays and block_m).
+// Rows in the alignment's order and back (rm: the plan's arrays and block_m).  zeroed: the padding
+// rows are; else they are left as they were.
 hipError_t launch_permute(const void* x, int dt, int64_t T, int K, int H, const RowMap& rm, int E,
-                          int64_t cap, void* rows, hipStream_t s);
+                          int64_t cap, void* rows, bool zeroed, hipStream_t s);
 // w null: weights 1
 hipError_t launch_unpermute(const void* rows, int rdt, const float* w, const void* shared, int sdt,
                             int64_t T, int K, int H, const int32_t* inv_pos, int64_t cap,

@@ -446,10 +446,10 @@ hipError_t unpermute_backward_t(const void* dout, const void* rows, const float*
 }  // namespace
 
 hipError_t launch_permute(const void* x, int dt, int64_t T, int K, int H, const RowMap& rm, int E,
-                          int64_t cap, void* rows, hipStream_t s) {
+                          int64_t cap, void* rows, bool zeroed, hipStream_t s) {
   const int nv = dt == kDtF32 ? H / 4 : H / 8;
   const Padding pad = padding_of(rm, E, cap, T * K, nv);
-  const int64_t pads = E * pad.subs;
+  const int64_t pads = zeroed ? E * pad.subs : 0;
   return with_lanes(nv, [&](auto lanes) {
     constexpr int kLanes = decltype(lanes)::value;
     const int chunks = (nv + kLanes - 1) / kLanes;

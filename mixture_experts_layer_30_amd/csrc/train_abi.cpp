@@ -184,9 +184,10 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
   const uint16_t* xr = static_cast<const uint16_t*>(x);
   if (e == hipSuccess && dw13 && plan && r.tokens > 0) {
     // x by row: the contraction over rows then reads whole lines in order (gathering in it
-    // took the registers that hide its loads; the copy is 1% of a Mixtral-shaped backward)
+    // took the registers that hide its loads; the copy is 1% of a Mixtral-shaped backward).  The
+    // product reads no padding rows.
     e = moe::launch_permute(x, moe::kDtBF16, r.tokens, r.K, r.H, plan_rows(plan, r.K), r.E, r.rows,
-                            x_rows, s);
+                            x_rows, false, s);
     xr = x_rows;
   }
   if (e == hipSuccess)

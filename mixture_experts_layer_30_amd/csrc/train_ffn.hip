@@ -1447,22 +1447,34 @@ Divider divider(int K) {
 // Parts of the contraction of a launch of `items` items (at most) of `blocks` blocks, whose sums
 // are `values` in all: as many as the compute units take in one round (`xcds`: of runs that each
 // XCD has of its own) where the items would leave three quarters of them idle, 16 blocks or more,
-// and as `room` bytes hold; up to 8 of 4 blocks or more, more of 8.  others: items of the same
-// launch; where they fit, they have compute units of their own.
+// and as `room` bytes hold; up to 8 of 4 blocks or more, more of 8.
 // Measured, whole and in parts: one token of a Mixtral-shaped down product 219 and 51 us; the da
 // and dx of 200 rows of 1024 x 512 48 us in parts of 8 blocks or more, 42 of 4 (128 rows of
 // 4096 x 4096, 16 parts of 4 and 8 of 8: 69 and 65); 300 rows of 512 x 512 forward, of 8 blocks,
-// 33 whole and 42.  A dense backward, dx in as many parts as without others and in fewer: 1003 rows
-// of 1088 x 1856 97 and 77 us, 900 of 2048 x 1536 102 and 80, 512 of 2048 x 2048 83 and 90.
+// 33 whole and 42.
+// others: items of the same launch, of other_blocks.  Where they fit, they have compute units of
+// their own and leave fewer parts, unless that makes a part longer by more than 8 blocks and by
+// more than two of the others, which a workgroup then does after it.  Measured, a dense backward
+// with such fewer parts of dx and with all: 1003 rows of 1088 x 1856 (5 parts or 8) 74 and 95 us,
+// 900 of 2048 x 1536 (3, 8) 79 and 100, 768 of 2048 x 2048 (2, 8; as long as two others) 97 and 99,
+// 640 94 and 90, 512 91 and 84, 232 of 1472 x 3584 (whole, 14) 183 and 79.
 int parts_of(int64_t items, int64_t blocks, int64_t values, int64_t room, bool xcds,
-             int64_t others = 0) {
+             int64_t others = 0, int64_t other_blocks = 0) {
   if (items < 1 || 4 * items > workgroups() || blocks < 16 || values < 1) return 1;
-  const int64_t units = others < workgroups() ? workgroups() - others : workgroups();
-  int64_t n = xcds ? units / 8 / ((items + 7) / 8) : units / items;
+  const auto fit = [&](int64_t units) { return xcds ? units / 8 / ((items + 7) / 8) : units / items; };
+  int64_t n = fit(workgroups());
   const int64_t most = blocks / 4 < 8 ? blocks / 4 : blocks / 8 > 8 ? blocks / 8 : 8;
   if (n > kMaxParts) n = kMaxParts;
   if (n > most) n = most;
   if (n > room / (4 * values)) n = room / (4 * values);
+  if (others > 0 && others < workgroups()) {
+    int64_t own = fit(workgroups() - others);
+    if (own < 1) own = 1;
+    if (own < n) {
+      const int64_t longer = (blocks + own - 1) / own - (blocks + n - 1) / n;
+      if (longer <= 8 || longer <= 2 * other_blocks) n = own;
+    }
+  }
   return n < 2 ? 1 : (int)n;
 }
 
@@ -1474,12 +1486,15 @@ hipError_t plan_rows(Args& a, const PartSpace& space, int64_t others, unsigned* 
   const int K = kOp == kGateUp || kOp == kDAct ? a.r.H : kOp == kDown ? a.r.I : 2 * a.r.I;
   // spans: one for each 256 rows, and a short one an expert
   const int64_t pairs = a.r.counts ? a.r.tokens * a.r.K : a.r.tokens;
-  const int64_t spans = pairs / kTile + (a.r.counts ? (a.r.E < pairs ? a.r.E : pairs) : 1);
+  const int64_t experts = a.r.counts ? (a.r.E < pairs ? a.r.E : pairs) : 1;
+  const int64_t spans = pairs / kTile + experts;
   const int64_t items = spans * ((F + per_tile - 1) / per_tile);
   if (items >= (int64_t)1 << 30) return hipErrorInvalidValue;
   const int64_t width = kOp == kGateUp ? 2 * (int64_t)F : F;
   a.part = space.part;
-  a.splits = parts_of(items, K / kBlock, pairs * width, space.bytes, true, others);
+  // blocks of a weights' tile: an expert's rows, of the busier ones twice the mean
+  const int64_t tile_blocks = ((experts > 1 ? 2 : 1) * pairs / experts + kBlock - 1) / kBlock;
+  a.splits = parts_of(items, K / kBlock, pairs * width, space.bytes, true, others, tile_blocks);
   // By row where there is room for the padding too: by pair, whose rows a tile scatters, da and dx of
   // 300 rows of 1024 x 2048 for two experts take 61 us for 59.  In the parts that have room by row,
   // and by pair: one token of a Mixtral-shaped layer forward 153 and 139 us with its rows 128 apart,

@@ -36,7 +36,7 @@ def each_subset(run, buffers, refs):
 # dx in parts, fewer of them next to the weights' tiles; parts of few blocks; the weights'
 # gradients in parts
 @pytest.mark.parametrize("T,H,I", [(1003, 1088, 1856), (200, 1024, 512), (512, 2048, 2048),
-                                   (2100, 128, 192), (2100, 192, 1088)])
+                                   (232, 1472, 3584), (2100, 128, 192), (2100, 192, 1088)])
 def test_dense_subsets_in_parts(T, H, I):
     g = gen(T)
     x, dout = randn(g, T, H), randn(g, T, H, std=0.1)

@@ -1305,9 +1305,9 @@ __global__ __launch_bounds__(kThreads, 1) void weights_kernel(WeightArgs a) {
 
 // dx, then the weights' gradients, by workgroups as they come: the tiles of the latter fill the
 // rounds that dx leaves part empty.  (In two launches and in one, a backward: tiny layer 36 and
-// 30 us; 200 rows of 1024 x 512 56 and 44; 64 experts of 3584 x 2560, 128 tokens, 1522 and 1470,
-// 3001 tokens 2430 and 2378; 8 of 4096 x 14336, 4096 tokens, 5622 and 5526; dense, 1003 rows of
-// 2048 x 1024, 97 and 99.)
+// 29 us; 64 experts of 3584 x 2560, 128 tokens, 1522 and 1470, 3001 tokens 2430 and 2378; 8 of
+// 4096 x 14336, 4096 tokens, 5622 and 5526; dense, 200 rows of 1024 x 512 57 and 44, 1003 of
+// 2048 x 1024 98 and 73, 512 of 2048 x 2048 87 and 83, 2000 of 1024 x 1024 107 both.)
 template <Split kSplit, class TOut>
 __global__ __launch_bounds__(kThreads, 1) void grads_kernel(Args a, WeightArgs w) {
   TRAIN_UNITS;

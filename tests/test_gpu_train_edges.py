@@ -1,5 +1,6 @@
-"""Training the experts where buffers end, sums are cut into parts and offsets pass 2 GB: what
-the order of the sums depends on, what lies behind each buffer, and operands close to 4 GB."""
+"""Training the experts where sums are cut into parts, buffers end and offsets pass 2 GB: subsets of
+the gradients, padding of every width, an expert in both slots of a token, what lies around each
+buffer, and operands close to 4 GB."""
 import pytest
 import torch
 

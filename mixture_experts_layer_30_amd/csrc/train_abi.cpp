@@ -156,7 +156,7 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
   const int64_t matrix = (int64_t)(r.counts ? r.E : 1) * r.H * r.I;
   const int64_t row_bytes = r.tokens > 0 ? r.rows * r.H * 2 : 0, x_bytes = r.tokens * r.H * 2;
   const int64_t dw_bytes = dwdt == MOE_F32 ? 4 : 2;
-  const Buffer room{"the workspace", workspace,
+  const Buffer room{"the workspace", r.tokens > 0 ? workspace : nullptr,
                     moe_ffn_backward_workspace_bytes(r.rows, r.H, r.I)};
   const Buffer rows{"the rows' gradient", dx, row_bytes};
   st = check_apart(what,
@@ -164,7 +164,7 @@ moe_status backward(const char* what, const moe::TrainRows& r, const moe_plan* p
                     {"dw13", dw13, 2 * matrix * dw_bytes},
                     {"dw2", dw2, matrix * dw_bytes},
                     room},
-                   {{"its input", dy, row_bytes},
+                   {{"the output's gradient", dy, row_bytes},
                     {"x", dw13 ? x : nullptr, x_bytes},
                     {"w13", dx && r.tokens > 0 ? w13 : nullptr, 4 * matrix}});
   if (!st) st = check_apart(what, {rows}, {{"x", x, x_bytes}});

@@ -84,7 +84,12 @@ def test_what_is_not_read_may_be_overwritten(L):  # noqa: F811
     assert b"workspace overwrites w2" in said(dw2=s.at["x"], dw13=None, dx=None, **last)
     assert b"workspace overwrites w2" in said(dw13=s.at["w13"], dx=None, dw2=None, **last)
     assert b"workspace overwrites w2" in said(w13=None, dx=None, **last)
-    # without tokens nothing is read
+    # without tokens nothing is read and the workspace is not used
+    plan = ctypes.byref(B.moe_plan(1 << 16, 1 << 16, 1 << 16, 1 << 16, 1 << 16, 16, CAP))
+    saved = ctypes.byref(B.moe_saved(0, None, None))
+    assert B.lib().moe_grouped_ffn_backward(
+        s.at["dx"], s.at["dx"], 0, H, I, E, K, s.at["dx"], s.at["dx"], plan, saved, s.at["dx"],
+        B.lib().moe_ffn_backward_workspace_bytes(CAP, H, I), s.at["dx"], None, None, BF, None) == B.MOE_OK
     assert B.lib().dense_ffn_backward(None, None, 0, H, I, s.at["dw13"], None,
                                       ctypes.byref(B.moe_saved(0, None, None)), None, 0, None,
                                       s.at["dw13"], s.at["dw13"], BF, None) == B.MOE_EINVAL
